@@ -21,6 +21,12 @@ EXPORTS = ("wkv7_checkpoint_bytes", "wkv7_backward_workspace_bytes", "wkv7_forwa
 # ... and every function include/rwkv8.h declares
 RWKV8_EXPORTS = ("rwkv8_checkpoint_bytes", "rwkv8_backward_workspace_bytes", "rwkv8_forward",
                  "rwkv8_backward")
+# ... include/gdr.h and include/residual_norm.h
+GDR_EXPORTS = ("gdr_checkpoint_bytes", "gdr_forward_workspace_bytes", "gdr_backward_workspace_bytes",
+               "gdr_forward", "gdr_backward", "gdr_decode", "gdr_epilogue_workspace_bytes",
+               "gdr_epilogue_forward", "gdr_epilogue_backward")
+RESIDUAL_NORM_EXPORTS = ("residual_norm_workspace_bytes", "residual_norm_forward",
+                         "residual_norm_backward")
 WKV7_FAULT_RWKV8_DECAY = 2
 
 WKV7_NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -41,6 +47,27 @@ class Shape(ctypes.Structure):
 class Rwkv8Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
                 ("Hv", ctypes.c_int64), ("L", ctypes.c_int64), ("E", ctypes.c_int64)]
+
+
+GDR_NORM_QK = 1   # gdr_shape.flags bit
+
+
+class GdrShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("Hv", ctypes.c_int64), ("K", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("nseq", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class GdrEpilogueShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("H", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("Hw", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class ResidualNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class Wkv7Error(RuntimeError):
@@ -96,6 +123,23 @@ def lib():
     L.rwkv8_forward.restype = i32
     L.rwkv8_backward.argtypes = [s8] + [vp] * 14 + [vp, sz, vp]
     L.rwkv8_backward.restype = i32
+    sg, se, sn = (ctypes.POINTER(x) for x in (GdrShape, GdrEpilogueShape, ResidualNormShape))
+    i64 = ctypes.c_int64
+    for name, args, res in (
+            ("gdr_checkpoint_bytes", [sg], sz),
+            ("gdr_forward_workspace_bytes", [sg], sz),
+            ("gdr_backward_workspace_bytes", [sg, i32], sz),
+            ("gdr_forward", [sg] + [vp] * 10 + [vp, sz, vp], i32),
+            ("gdr_backward", [sg] + [vp] * 16 + [vp, sz, vp], i32),
+            ("gdr_decode", [sg] + [vp] * 6 + [i64, vp, vp, vp], i32),
+            ("gdr_epilogue_workspace_bytes", [se], sz),
+            ("gdr_epilogue_forward", [se] + [vp] * 4 + [vp], i32),
+            ("gdr_epilogue_backward", [se] + [vp] * 7 + [vp, sz, vp], i32),
+            ("residual_norm_workspace_bytes", [sn], sz),
+            ("residual_norm_forward", [sn] + [vp] * 6 + [vp], i32),
+            ("residual_norm_backward", [sn] + [vp] * 10 + [vp, sz, vp], i32)):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, res
     _LIB = L
     return L
 

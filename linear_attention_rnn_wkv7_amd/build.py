@@ -19,7 +19,9 @@ LIB = os.path.join(PKG, "libwkv7.so")
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["wkv7_abi.cpp", "wkv7_fwd.hip", "wkv7_bwd.hip", "wkv7_bwdc.hip", "wkv7_fwdc.hip",
            "wkv7_decode.hip", "wkv7_split.hip",
-           "wkv7_epilogue.hip", "wkv7_noalloc.hip", "rwkv8.hip"]
+           "wkv7_epilogue.hip", "wkv7_noalloc.hip", "rwkv8.hip",
+           "gdr_abi.cpp", "gdr_prep.hip", "gdr_scan.hip", "gdr_grads.hip", "gdr_decode.hip",
+           "gdr_norm.hip"]
 ARCH = "gfx950"
 
 # Packed-FP32 VALU forms are switched off for the device code.
