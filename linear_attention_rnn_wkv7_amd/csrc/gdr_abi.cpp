@@ -355,11 +355,10 @@ int residual_norm_forward(const residual_norm_shape *shape, const void *x, const
     wkv7::gdr::NormLaunch L;
     const int rc = check(shape, &L);
     if (rc != WKV7_OK) return rc;
-    if (scale && !y) return WKV7_ERR_INVALID;
     for (const void *p : {x, y, (const void *)scale, (const void *)w, (const void *)x_out, (const void *)h})
         if (!aligned(p)) return WKV7_ERR_INVALID;
     if (L.rows == 0) return WKV7_OK;
-    if (!x || !w || !h) return WKV7_ERR_INVALID;
+    if (!x || !w || !h || (scale && !y)) return WKV7_ERR_INVALID;
     L.x = x;
     L.y = y;
     L.scale = scale;
