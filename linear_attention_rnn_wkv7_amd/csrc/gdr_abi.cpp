@@ -67,9 +67,9 @@ int check(const gdr_shape *s, Dims *d)
     else if (!mul_ok(s->B, d->nck, &d->slots))
         return WKV7_ERR_INVALID;
     if (d->slots > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
-    const int64_t el = d->dtype == WKV7_F32 ? 4 : 2 * wkv7::gdr::kParts;
     if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 4096), &x))
         return WKV7_ERR_INVALID;   // any sum of the workspace's parts
+    const int64_t el = d->dtype == WKV7_F32 ? 4 : 2 * wkv7::gdr::kParts;
     d->states = (size_t)(per * s->K * s->V * 4);
     d->rows = (size_t)(per * 64 * s->V * 4);
     d->table = (size_t)(per * wkv7::gdr::kTableFloats * 4);

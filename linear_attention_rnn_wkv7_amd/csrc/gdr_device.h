@@ -55,6 +55,11 @@ struct Num<bf16> {
     using Oct = bf16x8;
 };
 
+// Parts of P and of the operands of y: y is rounded to T, so that with bf16
+// two parts (2^-16 of each term) are 2^-8 of that rounding.
+template <typename T>
+constexpr int kYParts = sizeof(T) == 4 ? 1 : 2;
+
 // LDS row padding: 16 bytes, so that 16 rows' 16-byte reads meet all banks.
 template <typename T>
 constexpr int kPad = 16 / (int)sizeof(T);
@@ -73,17 +78,18 @@ struct Frag {
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-template <int PA, int PB>
+// kLim: products of parts i + j >= kLim are left out.
+template <int kLim = kParts, int PA, int PB>
 __device__ __forceinline__ f32x4 mma(f32x4 c, const Frag<bf16, PA> &a, const Frag<bf16, PB> &b)
 {
 #pragma unroll
     for (int i = PA - 1; i >= 0; --i)
 #pragma unroll
         for (int j = PB - 1; j >= 0; --j)
-            if (i + j < kParts) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
+            if (i + j < kLim) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
     return c;
 }
-template <int PA, int PB>
+template <int kLim = kParts, int PA, int PB>
 __device__ __forceinline__ f32x4 mma(f32x4 c, const Frag<float, PA> &a, const Frag<float, PB> &b)
 {
 #pragma unroll
@@ -138,6 +144,83 @@ __device__ __forceinline__ Frag<T, P> load_packed(const T *base, int frag, int l
 // upper one (a transposed lower): steps it / 2 .. 1.
 __device__ __forceinline__ constexpr int low_frag(int it, int ks) { return it < 2 ? it : 2 * it - 2 + ks; }
 __device__ __forceinline__ constexpr int up_frag(int it, int ks) { return it < 2 ? 2 * it + ks : it + 2; }
+
+// Chunk operands that are copied straight into LDS, [64][K] by rows, cannot
+// be padded; the 16-byte pieces of row t are permuted instead, piece p at
+// p ^ swizzle(t), so that neither 16 rows' reads of one piece nor 8 rows' of
+// two meet a bank twice.
+template <typename T, int K>
+struct Swizzled {
+    static constexpr int kRowBytes = K * (int)sizeof(T), kPieces = kRowBytes / 16, kBytes = 64 * kRowBytes;
+
+    __device__ static __forceinline__ int swizzle(int t)
+    {
+        return kPieces == 8 ? ((t >> 1) & 3) << 1 | ((t >> 3) & 1) : (t & 7) << 1 | ((t >> 3) & 1);
+    }
+    __device__ static __forceinline__ int at(int t, int byte)
+    {
+        return t * kRowBytes + (((byte >> 4) ^ swizzle(t)) << 4 | (byte & 15));
+    }
+    // Row 16 it + l16 as an operand: k = 32 ks + the order above.
+    __device__ static __forceinline__ Frag<T, 1> rows(const char *lds, int it, int ks, int lg, int l16)
+    {
+        using Quad = typename Num<T>::Quad;
+        const int b = (32 * ks + 4 * lg) * (int)sizeof(T);
+        const char *r = lds + 16 * it * kRowBytes;
+        const Quad lo = *reinterpret_cast<const Quad *>(r + at(l16, b));
+        const Quad hi = *reinterpret_cast<const Quad *>(r + at(l16, b + 16 * (int)sizeof(T)));
+        Frag<T, 1> f;
+        f.p[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        return f;
+    }
+    // Column 16 i + l16 as an operand, k = tokens 32 ks + the order above.
+    // bf16: the transposing LDS read hands each 16 lanes' 4 x 16 block (row
+    // l16 / 4, four columns to a lane) out by columns.
+    __device__ static __forceinline__ Frag<T, 1> cols(const char *lds, int i, int ks, int lg, int l16)
+    {
+        Frag<T, 1> f;
+        if constexpr (sizeof(T) == 2) {
+            typename Num<T>::Quad x[2];
+            const int t = 4 * lg + (l16 >> 2);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char *p = lds + (32 * ks + 16 * h) * kRowBytes + at(t, 32 * i + 8 * (l16 & 3));
+                x[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                    (__attribute__((address_space(3))) bf16x4 *)(const __attribute__((address_space(3))) char *)p);
+            }
+            f.p[0] = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f.p[0][j] = *reinterpret_cast<const float *>(lds + (32 * ks + 16 * (j >> 2)) * kRowBytes +
+                                                             at(4 * lg + (j & 3), 64 * i + 4 * l16));
+        }
+        return f;
+    }
+};
+
+// Copies by the waves of a workgroup straight into LDS (1 KB per wave and
+// instruction); complete after wait_dma() and a barrier.  A swizzled operand,
+// rows `stride` elements apart; rows behind the last of `len` repeat it (their
+// weights are zero).
+template <typename T, int K>
+__device__ __forceinline__ void dma_rows(char *lds, const T *src, int64_t stride, int len, int wave, int waves, int lane)
+{
+    using S = Swizzled<T, K>;
+    for (int n = wave; n < S::kBytes / 1024; n += waves) {
+        const int t = (n * 64 + lane) / S::kPieces, p = (n * 64 + lane) % S::kPieces;
+        const int u = t < len ? t : len - 1;
+        dma16(reinterpret_cast<const char *>(src + u * stride) + ((p ^ S::swizzle(t)) << 4),
+              reinterpret_cast<const float *>(lds + n * 1024));
+    }
+}
+template <int kBytes>
+__device__ __forceinline__ void dma_flat(char *lds, const void *src, int wave, int waves, int lane)
+{
+    static_assert(kBytes % 1024 == 0, "whole copies");
+    for (int n = wave; n < kBytes / 1024; n += waves)
+        dma16(static_cast<const char *>(src) + n * 1024 + lane * 16, reinterpret_cast<const float *>(lds + n * 1024));
+}
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(bf16 x) { return (float)x; }
@@ -205,6 +288,13 @@ __device__ __forceinline__ Chunk locate(const Map &m, int64_t slot)
 __device__ __forceinline__ f32x4 row4(const float *tab, int kind, int i0)
 {
     return *reinterpret_cast<const f32x4 *>(tab + kind * 64 + i0);
+}
+
+// Between a wave's own LDS writes and its other lanes' reads of them.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // Sum over the 64 lanes, in every lane.

@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
         if (tid < 64) {
             const float G = s.tab[4 * 64 + tid] + s.tab[5 * 64 + tid];
             const float dhi = s.tab[4 * 64 + 63] - s.tab[4 * 64 + tid], dlo = s.tab[5 * 64 + 63] - s.tab[5 * 64 + tid];
-            s.gam[tid] = expf(G);
-            s.eh[tid] = expf(dhi + dlo);
+            s.gam[tid] = __builtin_amdgcn_exp2f(G);
+            s.eh[tid] = __builtin_amdgcn_exp2f(dhi + dlo);
         }
         ip = wave_sum(ip);
         if (lane == 0) s.ip[w] = ip;
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
                     const int i = 16 * it + 4 * lg + r;
                     float v = 0.f;
                     if (zx ? i > j : i >= j) {
-                        const float gd = expf((s.tab[4 * 64 + i] - Ghj) + (s.tab[5 * 64 + i] - Glj));
+                        const float gd = __builtin_amdgcn_exp2f((s.tab[4 * 64 + i] - Ghj) + (s.tab[5 * 64 + i] - Glj));
                         v = gd * (zx ? -X[it][r] : Z[it][r]);
                     }
                     // row i, k = j
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
             double dG = (double)x[0] + x[1] - (double)be * x[2];
             const double end = wave_sum((double)be * x[3]);
             if (lane == 63)
-                dG += end + (double)expf(s.tab[4 * 64 + 63]) * ((double)s.ip[0] + s.ip[1] + ((double)s.ip[2] + s.ip[3]));
+                dG += end + (double)__builtin_amdgcn_exp2f(s.tab[4 * 64 + 63]) * ((double)s.ip[0] + s.ip[1] + ((double)s.ip[2] + s.ip[3]));
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double dn = __shfl_down(dG, d);

@@ -15,7 +15,7 @@ namespace gdr {
 
 constexpr int kChunk = 64;   // tokens of a chunk
 // A chunk's triangular factors are kept in fragment order: 6 fragments (the
-// 16 x 32 blocks that touch the triangle) of 64 lanes x 8 values, per plane.
+// 16 x 32 blocks that touch the triangle) of 64 lanes x 8 values, per part.
 constexpr int kFragElems = 6 * 64 * 8;
 // bf16 parts that stand for an fp32 value as a matrix operand.
 constexpr int kParts = 3;
@@ -47,7 +47,7 @@ struct Launch {
     float *ws_ds = nullptr, *ws_dr = nullptr;   // [slots][Hv][K][V], [slots][Hv][64][V]
     // both
     float *table = nullptr;                     // [slots][Hv][8][64]
-    void *tfrag = nullptr, *pfrag = nullptr;    // [slots][Hv][planes][6][64][8]
+    void *tfrag = nullptr, *pfrag = nullptr;    // [slots][Hv][parts][6][64][8]
 };
 
 // Triangular factors and decay tables of every chunk; transposed ones for

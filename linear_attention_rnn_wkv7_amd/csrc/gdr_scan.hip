@@ -34,61 +34,119 @@ struct ScanArgs {
     int group;
 };
 
-// Rows of [64][K] (stride Hk * K in memory) into LDS by rows and transposed.
-template <typename T, int K, bool kRows, bool kCols>
-__device__ __forceinline__ void stage(const T *src, int64_t stride, int len, T *rows, T *cols, int tid, int nt)
+// A wave's 64 x 16 tiles of a chunk of a [tokens][Hv][V] tensor, by buffer
+// accesses: rows behind the chunk's last read as zero and are not written.
+template <typename T>
+struct Cols {
+    BufRsrc buf;
+    uint32_t at, step;   // this lane's first row and column; bytes of a token
+
+    __device__ __forceinline__ Cols(const T *base, int64_t stride, int64_t V, int64_t col, int len, int lg)
+        : buf(raw_buffer(base, (uint32_t)(((len - 1) * stride + V) * (int64_t)sizeof(T)))),
+          at((uint32_t)((4 * lg * stride + col) * (int64_t)sizeof(T))), step((uint32_t)(stride * (int64_t)sizeof(T)))
+    {
+    }
+    __device__ __forceinline__ uint32_t off(int i) const { return at + (16 * (i >> 2) + (i & 3)) * step; }
+    __device__ __forceinline__ T load(int i) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off(i), 0, 0));
+        else
+            return __builtin_bit_cast(T, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(buf, (int)off(i), 0, 0));
+    }
+    __device__ __forceinline__ void store(int i, float x) const
+    {
+        if constexpr (sizeof(T) == 4)
+            bstore(buf, off(i), x);
+        else
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (T)x), buf, (int)off(i), 0, 0);
+    }
+};
+
+// Where a workgroup stands in its sequence.
+struct Pos {
+    int64_t tok, ch;
+    int len;
+};
+__device__ __forceinline__ Pos chunk_at(int64_t lo, int64_t hi, int64_t slot0, int64_t c, int64_t Hv, int64_t hv)
 {
-    using Quad = typename Num<T>::Quad;
-    constexpr int LD = K + kPad<T>, LT = 64 + kPad<T>;
-    for (int b = tid; b < 16 * (K / 4); b += nt) {
-        const int col = 4 * (b % (K / 4)), t0 = 4 * (b / (K / 4));
-        Quad x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            x[r] = Quad{};
-            if (t0 + r < len) x[r] = *reinterpret_cast<const Quad *>(src + (t0 + r) * stride + col);
+    const int64_t tok = lo + c * kChunk;
+    return {tok, (slot0 + c) * Hv + hv, hi - tok < kChunk ? (int)(hi - tok) : kChunk};
+}
+
+// One chunk's operands in LDS.  The copies of the next chunk run while this
+// one is computed, into a second set, where two fit into 160 KB (all but
+// fp32 with K = 128).
+template <typename T, int K, int PP>
+struct Operands {
+    static constexpr int kMat = Swizzled<T, K>::kBytes;
+    static constexpr int kT = Num<T>::kPlanes * kFragElems * (int)sizeof(T), kP = PP * kFragElems * (int)sizeof(T);
+    static constexpr int kTab = kTableFloats * 4;
+    static constexpr int kBytes = 2 * kMat + kT + kP + kTab;
+    static constexpr int kSets = 2 * kBytes <= 160 * 1024 ? 2 : 1;
+    char *base;
+
+    __device__ __forceinline__ char *k() const { return base; }
+    __device__ __forceinline__ char *q() const { return base + kMat; }
+    __device__ __forceinline__ const T *t() const { return reinterpret_cast<const T *>(base + 2 * kMat); }
+    __device__ __forceinline__ const T *p() const { return reinterpret_cast<const T *>(base + 2 * kMat + kT); }
+    __device__ __forceinline__ const float *tab() const
+    {
+        return reinterpret_cast<const float *>(base + 2 * kMat + kT + kP);
+    }
+    template <bool kAll>
+    __device__ __forceinline__ void copy(const ScanArgs<T> &a, const Pos &at, int64_t hk, int wave, int waves, int lane) const
+    {
+        const int64_t o = (at.tok * a.Hk + hk) * K;
+        dma_rows<T, K>(k(), a.k + o, a.Hk * K, at.len, wave, waves, lane);
+        dma_flat<kT>(base + 2 * kMat, a.tfrag + at.ch * (kT / (int)sizeof(T)), wave, waves, lane);
+        dma_flat<kTab>(base + 2 * kMat + kT + kP, a.table + at.ch * kTableFloats, wave, waves, lane);
+        if constexpr (kAll) {
+            dma_rows<T, K>(q(), a.q + o, a.Hk * K, at.len, wave, waves, lane);
+            dma_flat<kP>(base + 2 * kMat + kT, a.pfrag + at.ch * (kP / (int)sizeof(T)), wave, waves, lane);
         }
-        if constexpr (kRows) {
+    }
+};
+
+template <typename T, int P, int Q>
+__device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
+{
+    Frag<T, Q> g;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) *reinterpret_cast<Quad *>(rows + (t0 + r) * LD + kpos(col)) = x[r];
-        }
-        if constexpr (kCols) {
+    for (int i = 0; i < Q; ++i) g.p[i] = f.p[i];
+    return g;
+}
+
+// A value that was loaded before the copies of the next chunk are issued is
+// waited for here, not behind them.
+template <typename T>
+__device__ __forceinline__ void settle(T (&x)[16])
+{
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Quad z = {x[0][i], x[1][i], x[2][i], x[3][i]};
-                *reinterpret_cast<Quad *>(cols + (col + i) * LT + kpos(t0)) = z;
-            }
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            asm volatile("" : "+v"(x[i]));
+        } else {
+            unsigned u = __builtin_bit_cast(unsigned short, x[i]);
+            asm volatile("" : "+v"(u));
+            x[i] = __builtin_bit_cast(T, (unsigned short)u);
         }
     }
 }
 
-// A chunk's fragments and table rows into LDS.
-template <typename T>
-__device__ __forceinline__ void stage_frags(const T *src, T *dst, int tid, int nt)
-{
-    using Oct = typename Num<T>::Oct;
-    for (int i = tid; i < Num<T>::kPlanes * kFragElems / 8; i += nt)
-        reinterpret_cast<Oct *>(dst)[i] = reinterpret_cast<const Oct *>(src)[i];
-}
-
-template <typename T, int K>
-struct FwdLds {
-    T k[64 * (K + kPad<T>)], q[64 * (K + kPad<T>)], kt[K * (64 + kPad<T>)];
-    T t[Num<T>::kPlanes * kFragElems], p[Num<T>::kPlanes * kFragElems];
-    float tab[8 * 64];
-};
-
 template <typename T, int K, bool kY>
 __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
 {
-    constexpr int P = Num<T>::kPlanes, LD = K + kPad<T>, LT = 64 + kPad<T>;
+    constexpr int P = Num<T>::kPlanes, PY = kYParts<T>;
     constexpr int KT = K / 16, KS = K / 32;
-    __shared__ __align__(16) char buf[sizeof(FwdLds<T, K>)];
-    FwdLds<T, K> &s = *reinterpret_cast<FwdLds<T, K> *>(buf);
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    using Op = Operands<T, K, PY>;
+    using Sw = Swizzled<T, K>;
+    __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
+    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
-    const int64_t col = 16 * ((int64_t)blockIdx.x * (nt >> 6) + (tid >> 6)) + l16;
-    const bool own = col < a.V;   // whole waves
+    const int64_t col = 16 * ((int64_t)blockIdx.x * waves + wave) + l16;
+    const bool own = 16 * ((int64_t)blockIdx.x * waves + wave) < a.V;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
@@ -99,92 +157,93 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
     for (int i = 0; i < KT; ++i)
         S[i] = a.s0 && own ? *reinterpret_cast<const f32x4 *>(a.s0 + so + 16 * i) : zero4();
 
+    T vn[16];
+    auto fetch = [&](int64_t c) {
+        const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
+        Op{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)}.template copy<kY>(a, at, hk, wave, waves, lane);
+        if (own) {
+            const Cols<T> v(a.v + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) vn[i] = v.load(i);
+        }
+    };
+    if (nc > 0) fetch(0);
     for (int64_t c = 0; c < nc; ++c) {
-        const int64_t tok = lo + c * kChunk, ch = (slot0 + c) * a.Hv + hv;
-        const int len = hi - tok < kChunk ? (int)(hi - tok) : kChunk;
-        __syncthreads();   // the previous chunk's operands are done with
-        stage<T, K, true, true>(a.k + (tok * a.Hk + hk) * K, a.Hk * K, len, s.k, s.kt, tid, nt);
-        if constexpr (kY) {
-            stage<T, K, true, false>(a.q + (tok * a.Hk + hk) * K, a.Hk * K, len, s.q, nullptr, tid, nt);
-            stage_frags(a.pfrag + ch * P * kFragElems, s.p, tid, nt);
-        }
-        stage_frags(a.tfrag + ch * P * kFragElems, s.t, tid, nt);
-        for (int i = tid; i < kTableFloats / 4; i += nt)
-            reinterpret_cast<f32x4 *>(s.tab)[i] = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[i];
+        const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
+        const Op s{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)};
         f32x4 R[4];
+        wait_dma();
+        if (own) {
+            settle(vn);
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * it + 4 * lg + r;
-                R[it][r] = own && t < len ? to_f32(a.v[((tok + t) * a.Hv + hv) * a.V + col]) : 0.f;
-            }
-        __syncthreads();
-        if (!own) continue;
-        if (a.st) {
-#pragma unroll
-            for (int i = 0; i < KT; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a.st[(ch * K + 16 * i + 4 * lg + r) * a.V + col] = S[i][r];
+            for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = to_f32(vn[i]);
         }
-        Frag<T, P> Sf[KS];
+        __syncthreads();   // the copies have landed, and the other set is free
+        if (Op::kSets == 2 && c + 1 < nc) fetch(c + 1);
+        if (own) {
+            if (a.st) {
+                float *st = a.st + at.ch * K * a.V;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) Sf[ks] = make_frag<T, P>(S[2 * ks], S[2 * ks + 1]);
-        f32x4 Y[4];
+                for (int i = 0; i < KT; ++i)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            f32x4 acc = zero4();
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                acc = mma(acc, load_frag<T, 1>(s.k, 16 * it + l16, LD, ks, lg, 0), Sf[ks]);
-            R[it] -= row4(s.tab, 0, 16 * it + 4 * lg) * acc;
-            if constexpr (kY) {
-                acc = zero4();
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    acc = mma(acc, load_frag<T, 1>(s.q, 16 * it + l16, LD, ks, lg, 0), Sf[ks]);
-                Y[it] = row4(s.tab, 1, 16 * it + 4 * lg) * acc;
+                    for (int r = 0; r < 4; ++r) st[(uint32_t)((16 * i + 4 * lg + r) * (int)a.V + (int)col)] = S[i][r];
             }
-        }
-        const Frag<T, P> Rf[2] = {make_frag<T, P>(R[0], R[1]), make_frag<T, P>(R[2], R[3])};
-        f32x4 E[4];
+            Frag<T, P> Sf[KS];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            E[it] = zero4();
-#pragma unroll
-            for (int ks = 0; ks <= it / 2; ++ks)
-                E[it] = mma(E[it], load_packed<T, P>(s.t, low_frag(it, ks), lane), Rf[ks]);
-            if (a.rows) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a.rows[(ch * 64 + 16 * it + 4 * lg + r) * a.V + col] = E[it][r];
-            }
-        }
-        if constexpr (kY) {
-            const Frag<T, P> Ef[2] = {make_frag<T, P>(E[0], E[1]), make_frag<T, P>(E[2], E[3])};
+            for (int ks = 0; ks < KS; ++ks) Sf[ks] = make_frag<T, P>(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
+                f32x4 acc = zero4();
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) acc = mma(acc, Sw::rows(s.k(), it, ks, lg, l16), Sf[ks]);
+                R[it] -= row4(s.tab(), 0, 16 * it + 4 * lg) * acc;
+            }
+            const Frag<T, P> Rf[2] = {make_frag<T, P>(R[0], R[1]), make_frag<T, P>(R[2], R[3])};
+            f32x4 E[4];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                E[it] = zero4();
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks)
-                    Y[it] = mma(Y[it], load_packed<T, P>(s.p, low_frag(it, ks), lane), Ef[ks]);
+                    E[it] = mma(E[it], load_packed<T, P>(s.t(), low_frag(it, ks), lane), Rf[ks]);
+            }
+            if (a.rows) {
+                float *rows = a.rows + at.ch * 64 * a.V;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * it + 4 * lg + r;
-                    if (t < len) a.y[((tok + t) * a.Hv + hv) * a.V + col] = (T)Y[it][r];
+                for (int i = 0; i < 16; ++i)
+                    rows[(uint32_t)((16 * (i >> 2) + 4 * lg + (i & 3)) * (int)a.V + (int)col)] = E[i >> 2][i & 3];
+            }
+            if constexpr (kY) {
+                const Frag<T, PY> Ef[2] = {make_frag<T, PY>(E[0], E[1]), make_frag<T, PY>(E[2], E[3])};
+                const Cols<T> y(a.y + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    f32x4 Y = zero4();
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+                        Y = mma<PY>(Y, Sw::rows(s.q(), it, ks, lg, l16), first_parts<T, P, PY>(Sf[ks]));
+                    Y *= row4(s.tab(), 1, 16 * it + 4 * lg);
+#pragma unroll
+                    for (int ks = 0; ks <= it / 2; ++ks)
+                        Y = mma<PY>(Y, load_packed<T, PY>(s.p(), low_frag(it, ks), lane), Ef[ks]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y.store(4 * it + r, Y[r]);
                 }
             }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) E[it] *= row4(s.tab(), 2, 16 * it + 4 * lg);
+            const Frag<T, P> Wf[2] = {make_frag<T, P>(E[0], E[1]), make_frag<T, P>(E[2], E[3])};
+            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                S[i] *= last;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) S[i] = mma(S[i], Sw::cols(s.k(), i, ks, lg, l16), Wf[ks]);
+            }
         }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) E[it] *= row4(s.tab, 2, 16 * it + 4 * lg);
-        const Frag<T, P> Wf[2] = {make_frag<T, P>(E[0], E[1]), make_frag<T, P>(E[2], E[3])};
-        const float last = expf(s.tab[4 * 64 + 63]);
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            S[i] *= last;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                S[i] = mma(S[i], load_frag<T, 1>(s.kt, 16 * i + l16, LT, ks, lg, 0), Wf[ks]);
+        if (Op::kSets == 1 && c + 1 < nc) {
+            __syncthreads();
+            fetch(c + 1);
         }
     }
     if (a.sT && own) {
@@ -194,23 +253,18 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
 }
 
 template <typename T, int K>
-struct RevLds {
-    T k[64 * (K + kPad<T>)], kt[K * (64 + kPad<T>)], qt[K * (64 + kPad<T>)];
-    T t[Num<T>::kPlanes * kFragElems], p[Num<T>::kPlanes * kFragElems];
-    float tab[8 * 64];
-};
-
-template <typename T, int K>
 __global__ void __launch_bounds__(512) gdr_reverse_kernel(ScanArgs<T> a)
 {
-    constexpr int P = Num<T>::kPlanes, LD = K + kPad<T>, LT = 64 + kPad<T>;
+    constexpr int P = Num<T>::kPlanes;
     constexpr int KT = K / 16, KS = K / 32;
-    __shared__ __align__(16) char buf[sizeof(RevLds<T, K>)];
-    RevLds<T, K> &s = *reinterpret_cast<RevLds<T, K> *>(buf);
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    using Op = Operands<T, K, P>;
+    using Sw = Swizzled<T, K>;
+    __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
+    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
-    const int64_t col = 16 * ((int64_t)blockIdx.x * (nt >> 6) + (tid >> 6)) + l16;
-    const bool own = col < a.V;
+    const int64_t col = 16 * ((int64_t)blockIdx.x * waves + wave) + l16;
+    const bool own = 16 * ((int64_t)blockIdx.x * waves + wave) < a.V;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
@@ -221,75 +275,84 @@ __global__ void __launch_bounds__(512) gdr_reverse_kernel(ScanArgs<T> a)
     for (int i = 0; i < KT; ++i)
         D[i] = a.dsT && own ? *reinterpret_cast<const f32x4 *>(a.dsT + so + 16 * i) : zero4();
 
+    T yn[16];
+    auto fetch = [&](int64_t c) {
+        const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
+        Op{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)}.template copy<true>(a, at, hk, wave, waves, lane);
+        if (own) {
+            const Cols<T> y(a.dy + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) yn[i] = y.load(i);
+        }
+    };
+    if (nc > 0) fetch(nc - 1);
     for (int64_t c = nc - 1; c >= 0; --c) {
-        const int64_t tok = lo + c * kChunk, ch = (slot0 + c) * a.Hv + hv;
-        const int len = hi - tok < kChunk ? (int)(hi - tok) : kChunk;
-        __syncthreads();
-        stage<T, K, true, true>(a.k + (tok * a.Hk + hk) * K, a.Hk * K, len, s.k, s.kt, tid, nt);
-        stage<T, K, false, true>(a.q + (tok * a.Hk + hk) * K, a.Hk * K, len, nullptr, s.qt, tid, nt);
-        stage_frags(a.pfrag + ch * P * kFragElems, s.p, tid, nt);
-        stage_frags(a.tfrag + ch * P * kFragElems, s.t, tid, nt);
-        for (int i = tid; i < kTableFloats / 4; i += nt)
-            reinterpret_cast<f32x4 *>(s.tab)[i] = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[i];
+        const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
+        const Op s{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)};
         f32x4 dY[4];
+        wait_dma();
+        if (own) {
+            settle(yn);
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * it + 4 * lg + r;
-                dY[it][r] = own && t < len ? to_f32(a.dy[((tok + t) * a.Hv + hv) * a.V + col]) : 0.f;
-            }
+            for (int i = 0; i < 16; ++i) dY[i >> 2][i & 3] = to_f32(yn[i]);
+        }
         __syncthreads();
-        if (!own) continue;
+        if (Op::kSets == 2 && c > 0) fetch(c - 1);
+        if (own) {
+            float *st = a.st + at.ch * K * a.V;
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
+            for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                a.st[(ch * K + 16 * i + 4 * lg + r) * a.V + col] = D[i][r];
-        Frag<T, P> Df[KS];
+                for (int r = 0; r < 4; ++r) st[(uint32_t)((16 * i + 4 * lg + r) * (int)a.V + (int)col)] = D[i][r];
+            Frag<T, P> Df[KS];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) Df[ks] = make_frag<T, P>(D[2 * ks], D[2 * ks + 1]);
-        const Frag<T, 1> dYf[2] = {make_frag<T, 1>(dY[0], dY[1]), make_frag<T, 1>(dY[2], dY[3])};
-        f32x4 dE[4];
+            for (int ks = 0; ks < KS; ++ks) Df[ks] = make_frag<T, P>(D[2 * ks], D[2 * ks + 1]);
+            const Frag<T, 1> dYf[2] = {make_frag<T, 1>(dY[0], dY[1]), make_frag<T, 1>(dY[2], dY[3])};
+            f32x4 dE[4];
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            f32x4 acc = zero4();
+            for (int jt = 0; jt < 4; ++jt) {
+                f32x4 acc = zero4();
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                acc = mma(acc, load_frag<T, 1>(s.k, 16 * jt + l16, LD, ks, lg, 0), Df[ks]);
-            dE[jt] = row4(s.tab, 2, 16 * jt + 4 * lg) * acc;
+                for (int ks = 0; ks < KS; ++ks) acc = mma(acc, Sw::rows(s.k(), jt, ks, lg, l16), Df[ks]);
+                dE[jt] = row4(s.tab(), 2, 16 * jt + 4 * lg) * acc;
 #pragma unroll
-            for (int ks = jt / 2; ks < 2; ++ks)
-                dE[jt] = mma(dE[jt], load_packed<T, P>(s.p, up_frag(jt, ks), lane), dYf[ks]);
-        }
-        const Frag<T, P> dEf[2] = {make_frag<T, P>(dE[0], dE[1]), make_frag<T, P>(dE[2], dE[3])};
-        f32x4 dR[4];
-#pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            dR[jt] = zero4();
-#pragma unroll
-            for (int ks = jt / 2; ks < 2; ++ks)
-                dR[jt] = mma(dR[jt], load_packed<T, P>(s.t, up_frag(jt, ks), lane), dEf[ks]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = 16 * jt + 4 * lg + r;
-                a.rows[(ch * 64 + t) * a.V + col] = dR[jt][r];
-                if (t < len) a.dv[((tok + t) * a.Hv + hv) * a.V + col] = (T)dR[jt][r];
+                for (int ks = jt / 2; ks < 2; ++ks)
+                    dE[jt] = mma(dE[jt], load_packed<T, P>(s.p(), up_frag(jt, ks), lane), dYf[ks]);
             }
-            dY[jt] *= row4(s.tab, 1, 16 * jt + 4 * lg);
-            dR[jt] *= -row4(s.tab, 0, 16 * jt + 4 * lg);
-        }
-        const Frag<T, P> Yf[2] = {make_frag<T, P>(dY[0], dY[1]), make_frag<T, P>(dY[2], dY[3])};
-        const Frag<T, P> Rf[2] = {make_frag<T, P>(dR[0], dR[1]), make_frag<T, P>(dR[2], dR[3])};
-        const float last = expf(s.tab[4 * 64 + 63]);
+            const Frag<T, P> dEf[2] = {make_frag<T, P>(dE[0], dE[1]), make_frag<T, P>(dE[2], dE[3])};
+            f32x4 dR[4];
+            float *rows = a.rows + at.ch * 64 * a.V;
+            const Cols<T> dv(a.dv + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            D[i] *= last;
+            for (int jt = 0; jt < 4; ++jt) {
+                dR[jt] = zero4();
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                D[i] = mma(D[i], load_frag<T, 1>(s.qt, 16 * i + l16, LT, ks, lg, 0), Yf[ks]);
-                D[i] = mma(D[i], load_frag<T, 1>(s.kt, 16 * i + l16, LT, ks, lg, 0), Rf[ks]);
+                for (int ks = jt / 2; ks < 2; ++ks)
+                    dR[jt] = mma(dR[jt], load_packed<T, P>(s.t(), up_frag(jt, ks), lane), dEf[ks]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    rows[(uint32_t)((16 * jt + 4 * lg + r) * (int)a.V + (int)col)] = dR[jt][r];
+                    dv.store(4 * jt + r, dR[jt][r]);
+                }
+                dY[jt] *= row4(s.tab(), 1, 16 * jt + 4 * lg);
+                dR[jt] *= -row4(s.tab(), 0, 16 * jt + 4 * lg);
             }
+            const Frag<T, P> Yf[2] = {make_frag<T, P>(dY[0], dY[1]), make_frag<T, P>(dY[2], dY[3])};
+            const Frag<T, P> Rf[2] = {make_frag<T, P>(dR[0], dR[1]), make_frag<T, P>(dR[2], dR[3])};
+            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                D[i] *= last;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    D[i] = mma(D[i], Sw::cols(s.q(), i, ks, lg, l16), Yf[ks]);
+                    D[i] = mma(D[i], Sw::cols(s.k(), i, ks, lg, l16), Rf[ks]);
+                }
+            }
+        }
+        if (Op::kSets == 1 && c > 0) {
+            __syncthreads();
+            fetch(c - 1);
         }
     }
     if (a.ds0 && own) {
@@ -325,8 +388,8 @@ ScanArgs<T> scan_args(const Launch &a)
     return p;
 }
 
-// Slabs per workgroup: as many as there are (8 at most), fewer while that
-// leaves compute units without a workgroup.
+// Slabs per workgroup, a wave each: as many as there are (8 at most), fewer
+// while that leaves compute units without a workgroup.
 void scan_grid(const Launch &a, dim3 *grid, dim3 *block)
 {
     const int64_t slabs = a.V / 16, units = a.map.nseq * a.Hv;
