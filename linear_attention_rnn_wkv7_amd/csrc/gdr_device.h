@@ -199,27 +199,40 @@ struct Swizzled {
     }
 };
 
-// Copies by the waves of a workgroup straight into LDS (1 KB per wave and
-// instruction); complete after wait_dma() and a barrier.  A swizzled operand,
-// rows `stride` elements apart; rows behind the last of `len` repeat it (their
-// weights are zero).
+// Copies by one wave straight into LDS (1 KB per instruction); complete after
+// wait_dma() and a barrier.  A swizzled operand, rows `stride` elements apart
+// (a multiple of K); rows behind the last of `len` repeat it (their weights
+// are zero).
 template <typename T, int K>
-__device__ __forceinline__ void dma_rows(char *lds, const T *src, int64_t stride, int len, int wave, int waves, int lane)
+__device__ __forceinline__ void dma_rows(char *lds, const T *src, int64_t stride, int len, int lane)
 {
     using S = Swizzled<T, K>;
-    for (int n = wave; n < S::kBytes / 1024; n += waves) {
-        const int t = (n * 64 + lane) / S::kPieces, p = (n * 64 + lane) % S::kPieces;
-        const int u = t < len ? t : len - 1;
-        dma16(reinterpret_cast<const char *>(src + u * stride) + ((p ^ S::swizzle(t)) << 4),
-              reinterpret_cast<const float *>(lds + n * 1024));
+    constexpr int kRows = 64 / S::kPieces;   // rows per copy
+    const unsigned to = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    const int row = lane / S::kPieces, piece = lane % S::kPieces;
+    const uint32_t step = (uint32_t)(stride * (int64_t)sizeof(T));
+    if (len == kChunk) {
+        // swizzle() only moves bits: that of n * kRows + row is the exclusive or
+        const uint32_t off = row * step + ((piece ^ S::swizzle(row)) << 4);
+        const char *base = reinterpret_cast<const char *>(src);
+#pragma unroll
+        for (int n = 0; n < S::kBytes / 1024; ++n, base += kRows * step)
+            dma16_split(base, off ^ (S::swizzle(n * kRows) << 4), to + n * 1024);
+    } else {
+        for (int n = 0; n < S::kBytes / 1024; ++n) {
+            const int t = n * kRows + row, u = t < len ? t : len - 1;
+            dma16_split(src, u * step + ((piece ^ S::swizzle(t)) << 4), to + n * 1024);
+        }
     }
 }
 template <int kBytes>
-__device__ __forceinline__ void dma_flat(char *lds, const void *src, int wave, int waves, int lane)
+__device__ __forceinline__ void dma_flat(char *lds, const void *src, int lane)
 {
     static_assert(kBytes % 1024 == 0, "whole copies");
-    for (int n = wave; n < kBytes / 1024; n += waves)
-        dma16(static_cast<const char *>(src) + n * 1024 + lane * 16, reinterpret_cast<const float *>(lds + n * 1024));
+    const unsigned to = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+#pragma unroll
+    for (int n = 0; n < kBytes / 1024; ++n)
+        dma16_split(static_cast<const char *>(src) + n * 1024, lane * 16, to + n * 1024);
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

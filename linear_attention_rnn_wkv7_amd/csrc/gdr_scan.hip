@@ -34,6 +34,14 @@ struct ScanArgs {
     int group;
 };
 
+// The lane's first row and column in a wave's tiles, fresh to the compiler at
+// each use: otherwise it keeps every offset made from it in a register.
+__device__ __forceinline__ uint32_t fresh(uint32_t x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // A wave's 64 x 16 tiles of a chunk of a [tokens][Hv][V] tensor, by buffer
 // accesses: rows behind the chunk's last read as zero and are not written.
 template <typename T>
@@ -43,7 +51,7 @@ struct Cols {
 
     __device__ __forceinline__ Cols(const T *base, int64_t stride, int64_t V, int64_t col, int len, int lg)
         : buf(raw_buffer(base, (uint32_t)(((len - 1) * stride + V) * (int64_t)sizeof(T)))),
-          at((uint32_t)((4 * lg * stride + col) * (int64_t)sizeof(T))), step((uint32_t)(stride * (int64_t)sizeof(T)))
+          at(fresh((uint32_t)((4 * lg * stride + col) * (int64_t)sizeof(T)))), step((uint32_t)(stride * (int64_t)sizeof(T)))
     {
     }
     __device__ __forceinline__ uint32_t off(int i) const { return at + (16 * (i >> 2) + (i & 3)) * step; }
@@ -60,6 +68,22 @@ struct Cols {
             bstore(buf, off(i), x);
         else
             __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (T)x), buf, (int)off(i), 0, 0);
+    }
+};
+
+// Whole 16-row tiles i of a [rows][V] fp32 matrix.
+struct Tiles {
+    BufRsrc buf;
+    uint32_t at, step;
+
+    __device__ __forceinline__ Tiles(float *base, int rows, int64_t V, int64_t col, int lg)
+        : buf(raw_buffer(base, (uint32_t)(rows * V * 4))), at(fresh((uint32_t)((4 * lg * V + col) * 4))), step((uint32_t)(V * 4))
+    {
+    }
+    __device__ __forceinline__ void store(int i, f32x4 x) const
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bstore(buf, at + (16 * i + r) * step, x[r]);
     }
 };
 
@@ -95,15 +119,15 @@ struct Operands {
         return reinterpret_cast<const float *>(base + 2 * kMat + kT + kP);
     }
     template <bool kAll>
-    __device__ __forceinline__ void copy(const ScanArgs<T> &a, const Pos &at, int64_t hk, int wave, int waves, int lane) const
+    __device__ __forceinline__ void copy(const ScanArgs<T> &a, const Pos &at, int64_t hk, int lane) const
     {
         const int64_t o = (at.tok * a.Hk + hk) * K;
-        dma_rows<T, K>(k(), a.k + o, a.Hk * K, at.len, wave, waves, lane);
-        dma_flat<kT>(base + 2 * kMat, a.tfrag + at.ch * (kT / (int)sizeof(T)), wave, waves, lane);
-        dma_flat<kTab>(base + 2 * kMat + kT + kP, a.table + at.ch * kTableFloats, wave, waves, lane);
+        dma_rows<T, K>(k(), a.k + o, a.Hk * K, at.len, lane);
+        dma_flat<kT>(base + 2 * kMat, a.tfrag + at.ch * (kT / (int)sizeof(T)), lane);
+        dma_flat<kTab>(base + 2 * kMat + kT + kP, a.table + at.ch * kTableFloats, lane);
         if constexpr (kAll) {
-            dma_rows<T, K>(q(), a.q + o, a.Hk * K, at.len, wave, waves, lane);
-            dma_flat<kP>(base + 2 * kMat + kT, a.pfrag + at.ch * (kP / (int)sizeof(T)), wave, waves, lane);
+            dma_rows<T, K>(q(), a.q + o, a.Hk * K, at.len, lane);
+            dma_flat<kP>(base + 2 * kMat + kT, a.pfrag + at.ch * (kP / (int)sizeof(T)), lane);
         }
     }
 };
@@ -117,39 +141,47 @@ __device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
     return g;
 }
 
-// A value that was loaded before the copies of the next chunk are issued is
-// waited for here, not behind them.
-template <typename T>
-__device__ __forceinline__ void settle(T (&x)[16])
+// The last wave of a workgroup copies the operands, chunk by chunk, one ahead
+// of the others: issuing copies stalls whenever the memory system has no room
+// for more, and would stall the products with it.  One barrier per chunk: the
+// copies for it have landed, and the set of the chunk before is free.
+template <typename T, int K, int PP, bool kAll>
+__device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, char *buf, int64_t lo, int64_t hi, int64_t slot0,
+                                          int64_t hv, int64_t hk, int64_t first, int64_t step, int64_t nc, int lane)
 {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            asm volatile("" : "+v"(x[i]));
-        } else {
-            unsigned u = __builtin_bit_cast(unsigned short, x[i]);
-            asm volatile("" : "+v"(u));
-            x[i] = __builtin_bit_cast(T, (unsigned short)u);
-        }
+    using Op = Operands<T, K, PP>;
+    __builtin_amdgcn_s_setprio(2);
+    for (int64_t i = 0, c = first; i < nc; ++i, c += step) {
+        if (Op::kSets == 1 && i > 0) __syncthreads();   // the only set is free
+        Op{buf + (Op::kSets == 2 ? (i & 1) * Op::kBytes : 0)}.template copy<kAll>(
+            a, chunk_at(lo, hi, slot0, c, a.Hv, hv), hk, lane);
+        wait_dma();
+        __syncthreads();
     }
 }
 
+constexpr int kMaxThreads = 64 * 9;   // 8 slabs and the copies
+
 template <typename T, int K, bool kY>
-__global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
+__global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes, PY = kYParts<T>;
     constexpr int KT = K / 16, KS = K / 32;
     using Op = Operands<T, K, PY>;
     using Sw = Swizzled<T, K>;
     __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
-    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), slabs = (blockDim.x >> 6) - 1;
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
-    const int64_t col = 16 * ((int64_t)blockIdx.x * waves + wave) + l16;
-    const bool own = 16 * ((int64_t)blockIdx.x * waves + wave) < a.V;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
+    if (wave == slabs) {
+        copy_loop<T, K, PY, kY>(a, buf, lo, hi, slot0, hv, hk, 0, 1, nc, lane);
+        return;
+    }
+    const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
+    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
 
     f32x4 S[KT];
     const int64_t so = ((seq * a.Hv + hv) * a.V + col) * K + 4 * lg;
@@ -160,43 +192,41 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
     T vn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
-        Op{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)}.template copy<kY>(a, at, hk, wave, waves, lane);
-        if (own) {
-            const Cols<T> v(a.v + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+        const Cols<T> v(a.v + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) vn[i] = v.load(i);
-        }
+        for (int i = 0; i < 16; ++i) vn[i] = v.load(i);
     };
-    if (nc > 0) fetch(0);
+    if (own && nc > 0) fetch(0);
     for (int64_t c = 0; c < nc; ++c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const Op s{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)};
-        f32x4 R[4];
-        wait_dma();
+        __syncthreads();
         if (own) {
-            settle(vn);
+            f32x4 R[4], Y[4];
 #pragma unroll
             for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = to_f32(vn[i]);
-        }
-        __syncthreads();   // the copies have landed, and the other set is free
-        if (Op::kSets == 2 && c + 1 < nc) fetch(c + 1);
-        if (own) {
+            if (c + 1 < nc) fetch(c + 1);
             if (a.st) {
-                float *st = a.st + at.ch * K * a.V;
+                const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
-                for (int i = 0; i < KT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) st[(uint32_t)((16 * i + 4 * lg + r) * (int)a.V + (int)col)] = S[i][r];
+                for (int i = 0; i < KT; ++i) st.store(i, S[i]);
             }
-            Frag<T, P> Sf[KS];
+            {   // K S and Q S
+                f32x4 acc[4];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) Sf[ks] = make_frag<T, P>(S[2 * ks], S[2 * ks + 1]);
+                for (int it = 0; it < 4; ++it) acc[it] = Y[it] = zero4();
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                f32x4 acc = zero4();
+                for (int ks = 0; ks < KS; ++ks) {
+                    const Frag<T, P> Sf = make_frag<T, P>(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) acc = mma(acc, Sw::rows(s.k(), it, ks, lg, l16), Sf[ks]);
-                R[it] -= row4(s.tab(), 0, 16 * it + 4 * lg) * acc;
+                    for (int it = 0; it < 4; ++it) {
+                        acc[it] = mma(acc[it], Sw::rows(s.k(), it, ks, lg, l16), Sf);
+                        if constexpr (kY)
+                            Y[it] = mma<PY>(Y[it], Sw::rows(s.q(), it, ks, lg, l16), first_parts<T, P, PY>(Sf));
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < 4; ++it) R[it] -= row4(s.tab(), 0, 16 * it + 4 * lg) * acc[it];
             }
             const Frag<T, P> Rf[2] = {make_frag<T, P>(R[0], R[1]), make_frag<T, P>(R[2], R[3])};
             f32x4 E[4];
@@ -208,26 +238,21 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
                     E[it] = mma(E[it], load_packed<T, P>(s.t(), low_frag(it, ks), lane), Rf[ks]);
             }
             if (a.rows) {
-                float *rows = a.rows + at.ch * 64 * a.V;
+                const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    rows[(uint32_t)((16 * (i >> 2) + 4 * lg + (i & 3)) * (int)a.V + (int)col)] = E[i >> 2][i & 3];
+                for (int i = 0; i < 4; ++i) rows.store(i, E[i]);
             }
             if constexpr (kY) {
                 const Frag<T, PY> Ef[2] = {make_frag<T, PY>(E[0], E[1]), make_frag<T, PY>(E[2], E[3])};
                 const Cols<T> y(a.y + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    f32x4 Y = zero4();
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-                        Y = mma<PY>(Y, Sw::rows(s.q(), it, ks, lg, l16), first_parts<T, P, PY>(Sf[ks]));
-                    Y *= row4(s.tab(), 1, 16 * it + 4 * lg);
+                    Y[it] *= row4(s.tab(), 1, 16 * it + 4 * lg);
 #pragma unroll
                     for (int ks = 0; ks <= it / 2; ++ks)
-                        Y = mma<PY>(Y, load_packed<T, PY>(s.p(), low_frag(it, ks), lane), Ef[ks]);
+                        Y[it] = mma<PY>(Y[it], load_packed<T, PY>(s.p(), low_frag(it, ks), lane), Ef[ks]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) y.store(4 * it + r, Y[r]);
+                    for (int r = 0; r < 4; ++r) y.store(4 * it + r, Y[it][r]);
                 }
             }
 #pragma unroll
@@ -241,10 +266,7 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
                 for (int ks = 0; ks < 2; ++ks) S[i] = mma(S[i], Sw::cols(s.k(), i, ks, lg, l16), Wf[ks]);
             }
         }
-        if (Op::kSets == 1 && c + 1 < nc) {
-            __syncthreads();
-            fetch(c + 1);
-        }
+        if (Op::kSets == 1 && c + 1 < nc) __syncthreads();
     }
     if (a.sT && own) {
 #pragma unroll
@@ -253,21 +275,25 @@ __global__ void __launch_bounds__(512) gdr_scan_kernel(ScanArgs<T> a)
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(512) gdr_reverse_kernel(ScanArgs<T> a)
+__global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes;
     constexpr int KT = K / 16, KS = K / 32;
     using Op = Operands<T, K, P>;
     using Sw = Swizzled<T, K>;
     __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
-    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), slabs = (blockDim.x >> 6) - 1;
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
-    const int64_t col = 16 * ((int64_t)blockIdx.x * waves + wave) + l16;
-    const bool own = 16 * ((int64_t)blockIdx.x * waves + wave) < a.V;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
+    if (wave == slabs) {
+        copy_loop<T, K, P, true>(a, buf, lo, hi, slot0, hv, hk, nc - 1, -1, nc, lane);
+        return;
+    }
+    const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
+    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
 
     f32x4 D[KT];
     const int64_t so = ((seq * a.Hv + hv) * a.V + col) * K + 4 * lg;
@@ -278,82 +304,79 @@ __global__ void __launch_bounds__(512) gdr_reverse_kernel(ScanArgs<T> a)
     T yn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
-        Op{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)}.template copy<true>(a, at, hk, wave, waves, lane);
-        if (own) {
-            const Cols<T> y(a.dy + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+        const Cols<T> y(a.dy + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) yn[i] = y.load(i);
-        }
+        for (int i = 0; i < 16; ++i) yn[i] = y.load(i);
     };
-    if (nc > 0) fetch(nc - 1);
-    for (int64_t c = nc - 1; c >= 0; --c) {
+    if (own && nc > 0) fetch(nc - 1);
+    for (int64_t i = 0; i < nc; ++i) {
+        const int64_t c = nc - 1 - i;
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
-        const Op s{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)};
-        f32x4 dY[4];
-        wait_dma();
-        if (own) {
-            settle(yn);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dY[i >> 2][i & 3] = to_f32(yn[i]);
-        }
+        const Op s{buf + (Op::kSets == 2 ? (i & 1) * Op::kBytes : 0)};
         __syncthreads();
-        if (Op::kSets == 2 && c > 0) fetch(c - 1);
         if (own) {
-            float *st = a.st + at.ch * K * a.V;
+            f32x4 dY[4];
 #pragma unroll
-            for (int i = 0; i < KT; ++i)
+            for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = to_f32(yn[j]);
+            if (c > 0) fetch(c - 1);
+            const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) st[(uint32_t)((16 * i + 4 * lg + r) * (int)a.V + (int)col)] = D[i][r];
-            Frag<T, P> Df[KS];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) Df[ks] = make_frag<T, P>(D[2 * ks], D[2 * ks + 1]);
-            const Frag<T, 1> dYf[2] = {make_frag<T, 1>(dY[0], dY[1]), make_frag<T, 1>(dY[2], dY[3])};
+            for (int j = 0; j < KT; ++j) st.store(j, D[j]);
             f32x4 dE[4];
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt) {
-                f32x4 acc = zero4();
+            for (int jt = 0; jt < 4; ++jt) dE[jt] = zero4();
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) acc = mma(acc, Sw::rows(s.k(), jt, ks, lg, l16), Df[ks]);
-                dE[jt] = row4(s.tab(), 2, 16 * jt + 4 * lg) * acc;
+            for (int ks = 0; ks < KS; ++ks) {
+                const Frag<T, P> Df = make_frag<T, P>(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
-                for (int ks = jt / 2; ks < 2; ++ks)
-                    dE[jt] = mma(dE[jt], load_packed<T, P>(s.p(), up_frag(jt, ks), lane), dYf[ks]);
+                for (int jt = 0; jt < 4; ++jt) dE[jt] = mma(dE[jt], Sw::rows(s.k(), jt, ks, lg, l16), Df);
             }
-            const Frag<T, P> dEf[2] = {make_frag<T, P>(dE[0], dE[1]), make_frag<T, P>(dE[2], dE[3])};
+            {
+                const Frag<T, 1> dYf[2] = {make_frag<T, 1>(dY[0], dY[1]), make_frag<T, 1>(dY[2], dY[3])};
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    dE[jt] *= row4(s.tab(), 2, 16 * jt + 4 * lg);
+#pragma unroll
+                    for (int ks = jt / 2; ks < 2; ++ks)
+                        dE[jt] = mma(dE[jt], load_packed<T, P>(s.p(), up_frag(jt, ks), lane), dYf[ks]);
+                }
+            }
             f32x4 dR[4];
-            float *rows = a.rows + at.ch * 64 * a.V;
-            const Cols<T> dv(a.dv + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+            {
+                const Frag<T, P> dEf[2] = {make_frag<T, P>(dE[0], dE[1]), make_frag<T, P>(dE[2], dE[3])};
+                const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
+                const Cols<T> dv(a.dv + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
+#pragma unroll
+                for (int jt = 0; jt < 4; ++jt) {
+                    dR[jt] = zero4();
+#pragma unroll
+                    for (int ks = jt / 2; ks < 2; ++ks)
+                        dR[jt] = mma(dR[jt], load_packed<T, P>(s.t(), up_frag(jt, ks), lane), dEf[ks]);
+                    rows.store(jt, dR[jt]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dv.store(4 * jt + r, dR[jt][r]);
+                }
+            }
+            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
+#pragma unroll
+            for (int j = 0; j < KT; ++j) D[j] *= last;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
-                dR[jt] = zero4();
-#pragma unroll
-                for (int ks = jt / 2; ks < 2; ++ks)
-                    dR[jt] = mma(dR[jt], load_packed<T, P>(s.t(), up_frag(jt, ks), lane), dEf[ks]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    rows[(uint32_t)((16 * jt + 4 * lg + r) * (int)a.V + (int)col)] = dR[jt][r];
-                    dv.store(4 * jt + r, dR[jt][r]);
-                }
                 dY[jt] *= row4(s.tab(), 1, 16 * jt + 4 * lg);
                 dR[jt] *= -row4(s.tab(), 0, 16 * jt + 4 * lg);
             }
-            const Frag<T, P> Yf[2] = {make_frag<T, P>(dY[0], dY[1]), make_frag<T, P>(dY[2], dY[3])};
-            const Frag<T, P> Rf[2] = {make_frag<T, P>(dR[0], dR[1]), make_frag<T, P>(dR[2], dR[3])};
-            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
 #pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                D[i] *= last;
+            for (int ks = 0; ks < 2; ++ks) {
+                const Frag<T, P> Yf = make_frag<T, P>(dY[2 * ks], dY[2 * ks + 1]);
+                const Frag<T, P> Rf = make_frag<T, P>(dR[2 * ks], dR[2 * ks + 1]);
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    D[i] = mma(D[i], Sw::cols(s.q(), i, ks, lg, l16), Yf[ks]);
-                    D[i] = mma(D[i], Sw::cols(s.k(), i, ks, lg, l16), Rf[ks]);
+                for (int j = 0; j < KT; ++j) {
+                    D[j] = mma(D[j], Sw::cols(s.q(), j, ks, lg, l16), Yf);
+                    D[j] = mma(D[j], Sw::cols(s.k(), j, ks, lg, l16), Rf);
                 }
             }
         }
-        if (Op::kSets == 1 && c > 0) {
-            __syncthreads();
-            fetch(c - 1);
-        }
+        if (Op::kSets == 1 && c > 0) __syncthreads();
     }
     if (a.ds0 && own) {
 #pragma unroll
@@ -397,7 +420,7 @@ void scan_grid(const Launch &a, dim3 *grid, dim3 *block)
     while (units * groups < 256 && groups < slabs) ++groups;
     const int64_t per = (slabs + groups - 1) / groups;
     *grid = dim3((unsigned)((slabs + per - 1) / per), (unsigned)a.Hv, (unsigned)a.map.nseq);
-    *block = dim3((unsigned)(64 * per));
+    *block = dim3((unsigned)(64 * (per + 1)));   // and the copies'
 }
 
 template <typename T, int K>
