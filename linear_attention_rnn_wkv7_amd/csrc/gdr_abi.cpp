@@ -21,7 +21,8 @@ struct Dims {
     bool packed;
     int dtype, norm;
     float scale;
-    size_t states, rows, table, frags;   // bytes: chunk states, chunk rows, tables, one factor
+    size_t states, rows, table;       // bytes: chunk states, chunk rows, tables
+    size_t factors, factors_t;        // of the forward's and the backward's factors, or 0
     bool empty() const { return Hv == 0 || (packed ? seqs == 0 : B == 0); }
     bool tokens() const { return !empty() && B * T > 0; }
 };
@@ -67,21 +68,28 @@ int check(const gdr_shape *s, Dims *d)
     else if (!mul_ok(s->B, d->nck, &d->slots))
         return WKV7_ERR_INVALID;
     if (d->slots > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
-    if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 4096), &x))
+    if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 2 * 4096), &x))
         return WKV7_ERR_INVALID;   // any sum of the workspace's parts
-    const int64_t el = d->dtype == WKV7_F32 ? 4 : 2 * wkv7::gdr::kParts;
     d->states = (size_t)(per * s->K * s->V * 4);
     d->rows = (size_t)(per * 64 * s->V * 4);
+    const bool makes = wkv7::gdr::scan_makes_factors(d->dtype, s->K, s->V, d->seqs * s->Hv);
+    d->factors = makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, false);
+    d->factors_t = makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, true);
     d->table = (size_t)(per * wkv7::gdr::kTableFloats * 4);
-    d->frags = (size_t)(per * wkv7::gdr::kFragElems * el);
     return WKV7_OK;
 }
 
+size_t forward_bytes(const Dims &d) { return round_up(d.factors); }
 size_t record_bytes(const Dims &d) { return round_up(d.states) + round_up(d.rows); }
-size_t factor_bytes(const Dims &d) { return round_up(d.table) + 2 * round_up(d.frags); }
+// the tables, the factors, D and dR (sized as the record), and the record if it
+// is not given
+size_t backward_bytes(const Dims &d, bool ckpt_provided)
+{
+    return round_up(d.table) + round_up(d.factors_t) + record_bytes(d) * (ckpt_provided ? 1 : 2);
+}
 
 wkv7::gdr::Launch base(const Dims &d, const void *q, const void *k, const void *v, const float *g,
-                       const float *beta, const float *s0, const int32_t *starts, char *ws)
+                       const float *beta, const float *s0, const int32_t *starts)
 {
     wkv7::gdr::Launch L;
     L.map = {d.packed ? starts : nullptr, d.T, d.seqs, d.nck, d.slots};
@@ -99,9 +107,6 @@ wkv7::gdr::Launch base(const Dims &d, const void *q, const void *k, const void *
     L.g = g;
     L.beta = beta;
     L.s0 = s0;
-    L.table = reinterpret_cast<float *>(ws);
-    L.tfrag = ws + round_up(d.table);
-    L.pfrag = ws + round_up(d.table) + round_up(d.frags);
     return L;
 }
 
@@ -194,14 +199,14 @@ size_t gdr_forward_workspace_bytes(const gdr_shape *shape)
 {
     Dims d;
     if (check(shape, &d) != WKV7_OK || !d.tokens()) return 0;
-    return factor_bytes(d);
+    return forward_bytes(d);
 }
 
 size_t gdr_backward_workspace_bytes(const gdr_shape *shape, int ckpt_provided)
 {
     Dims d;
     if (check(shape, &d) != WKV7_OK || !d.tokens()) return 0;
-    return factor_bytes(d) + record_bytes(d) * (ckpt_provided ? 1 : 2);   // D, dR: as the record
+    return backward_bytes(d, ckpt_provided != 0);
 }
 
 int gdr_forward(const gdr_shape *shape, const void *q, const void *k, const void *v, const float *g,
@@ -218,15 +223,15 @@ int gdr_forward(const gdr_shape *shape, const void *q, const void *k, const void
         if (!sT) return WKV7_OK;
         return status(wkv7::launch_fill(sT, s0, (size_t)(d.seqs * d.Hv * d.K * d.V), stream));
     }
-    rc = check_workspace(workspace, workspace_bytes, factor_bytes(d));
+    rc = check_workspace(workspace, workspace_bytes, forward_bytes(d));
     if (rc != WKV7_OK) return rc;
-    wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts, static_cast<char *>(workspace));
+    wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts);
+    L.factors = d.factors ? workspace : nullptr;
     L.y = y;
     L.sT = sT;
     set_record(&L, d, ckpt);
     if (!y && !sT && !ckpt) return WKV7_OK;
-    rc = status(wkv7::gdr::launch_prep(L, false, stream));
-    return rc != WKV7_OK ? rc : status(wkv7::gdr::launch_scan(L, stream));
+    return status(wkv7::gdr::launch_scan(L, stream));
 }
 
 int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const void *v, const float *g,
@@ -245,19 +250,19 @@ int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const voi
         if (!ds0) return WKV7_OK;
         return status(wkv7::launch_fill(ds0, dsT, (size_t)(d.seqs * d.Hv * d.K * d.V), stream));
     }
-    rc = check_workspace(workspace, workspace_bytes, factor_bytes(d) + record_bytes(d) * (ckpt ? 1 : 2));
+    rc = check_workspace(workspace, workspace_bytes, backward_bytes(d, ckpt != nullptr));
     if (rc != WKV7_OK) return rc;
-    char *ws = static_cast<char *>(workspace);
-    wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts, ws);
-    char *grads = ws + factor_bytes(d);
+    char *ws = static_cast<char *>(workspace), *grads = ws + round_up(d.table) + round_up(d.factors_t);
+    wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts);
+    L.table = static_cast<float *>(workspace);
+    L.factors = d.factors_t ? ws + round_up(d.table) : nullptr;   // at least the forward's
     L.ws_ds = reinterpret_cast<float *>(grads);
     L.ws_dr = reinterpret_cast<float *>(grads + round_up(d.states));
     if (ckpt) {
         set_record(&L, d, ckpt);
     } else {
         set_record(&L, d, reinterpret_cast<const float *>(grads + record_bytes(d)));
-        rc = status(wkv7::gdr::launch_prep(L, false, stream));
-        if (rc == WKV7_OK) rc = status(wkv7::gdr::launch_scan(L, stream));
+        rc = status(wkv7::gdr::launch_scan(L, stream));
         if (rc != WKV7_OK) return rc;
     }
     L.dy = dy;
@@ -268,8 +273,7 @@ int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const voi
     L.dg = dg;
     L.dbeta = dbeta;
     L.ds0 = ds0;
-    rc = status(wkv7::gdr::launch_prep(L, true, stream));
-    if (rc == WKV7_OK) rc = status(wkv7::gdr::launch_reverse(L, stream));
+    rc = status(wkv7::gdr::launch_reverse(L, stream));
     if (rc == WKV7_OK) rc = status(wkv7::gdr::launch_grads(L, stream));
     return rc;
 }

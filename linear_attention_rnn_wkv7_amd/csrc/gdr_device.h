@@ -98,20 +98,60 @@ __device__ __forceinline__ f32x4 mma(f32x4 c, const Frag<float, PA> &a, const Fr
     return c;
 }
 
+// Two floats rounded to bf16, the first in the low half: one conversion (the
+// empty asm keeps the compiler from converting each value by itself and
+// packing afterwards).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    asm("" : "+v"(u));
+    return u;
+}
+
+// kN floats as P parts: x[p] takes part p, pairs packed.
+template <int kN, int P>
+__device__ __forceinline__ void split(float (&v)[kN], uint32_t (&x)[P][kN / 2])
+{
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i) {
+            x[p][i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            if (p + 1 < P) {
+                v[2 * i] -= bf16_lo(x[p][i]);
+                v[2 * i + 1] -= bf16_hi(x[p][i]);
+            }
+        }
+}
+
+// Four values as P parts of an operand's quad.
+template <typename T, int P>
+__device__ __forceinline__ void split_quad(f32x4 x, typename Num<T>::Quad (&q)[P])
+{
+    if constexpr (sizeof(T) == 4) {
+        q[0] = x;
+    } else {
+        float v[4] = {x[0], x[1], x[2], x[3]};
+        uint32_t u[P][2];
+        split(v, u);
+#pragma unroll
+        for (int p = 0; p < P; ++p) __builtin_memcpy(&q[p], u[p], 8);
+    }
+}
+
 // Two result tiles (rows 0..15 and 16..31 of a step) as one operand.
 template <typename T, int P>
 __device__ __forceinline__ Frag<T, P> make_frag(f32x4 lo, f32x4 hi)
 {
     Frag<T, P> f;
-    f32x8 x = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     if constexpr (sizeof(T) == 4) {
-        f.p[0] = x;
+        f.p[0] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     } else {
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        uint32_t u[P][4];
+        split(v, u);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            f.p[i] = __builtin_convertvector(x, bf16x8);
-            if (i + 1 < P) x -= __builtin_convertvector(f.p[i], f32x8);
-        }
+        for (int p = 0; p < P; ++p) __builtin_memcpy(&f.p[p], u[p], 16);
     }
     return f;
 }
@@ -129,21 +169,13 @@ __device__ __forceinline__ Frag<T, P> load_frag(const T *base, int row, int ld, 
     return f;
 }
 
-// ... of an array in fragment order.
-template <typename T, int P>
-__device__ __forceinline__ Frag<T, P> load_packed(const T *base, int frag, int lane)
+// The lane number, or an offset made from it, fresh to the compiler: in a loop
+// it otherwise keeps everything computed from it in registers of its own.
+__device__ __forceinline__ uint32_t fresh(uint32_t x)
 {
-    Frag<T, P> f;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-        f.p[i] = *reinterpret_cast<const typename Num<T>::Oct *>(base + i * kFragElems + (frag * 64 + lane) * 8);
-    return f;
+    asm volatile("" : "+v"(x));
+    return x;
 }
-
-// Fragments of a lower triangle: row tile `it` needs steps 0 .. it / 2; of an
-// upper one (a transposed lower): steps it / 2 .. 1.
-__device__ __forceinline__ constexpr int low_frag(int it, int ks) { return it < 2 ? it : 2 * it - 2 + ks; }
-__device__ __forceinline__ constexpr int up_frag(int it, int ks) { return it < 2 ? 2 * it + ks : it + 2; }
 
 // Chunk operands that are copied straight into LDS, [64][K] by rows, cannot
 // be padded; the 16-byte pieces of row t are permuted instead, piece p at
@@ -226,7 +258,7 @@ __device__ __forceinline__ void dma_rows(char *lds, const T *src, int64_t stride
     }
 }
 template <int kBytes>
-__device__ __forceinline__ void dma_flat(char *lds, const void *src, int lane)
+__device__ __forceinline__ void dma_flat(void *lds, const void *src, int lane)
 {
     static_assert(kBytes % 1024 == 0, "whole copies");
     const unsigned to = (unsigned)(uintptr_t)(__attribute__((address_space(3))) char *)lds;

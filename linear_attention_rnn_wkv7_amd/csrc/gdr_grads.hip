@@ -19,7 +19,7 @@
 // rows of S and D once from memory as operands, and shares E, dR, dY in LDS.
 // Z and X tiles go through LDS into operand order once per chunk.
 
-#include "gdr_device.h"
+#include "gdr_factor.h"
 
 namespace wkv7 {
 namespace gdr {
@@ -45,9 +45,9 @@ struct GradLds {
         struct {
             T dy[64 * LT], dr[P * 64 * LT], e[P * 64 * LT];
         } in;
-        T w[4][P * kFragElems];   // W1, W2 (for dq, A), then transposed (for F)
+        T w[4][P * kTri];   // W1, W2 (for dq, A), then transposed (for F)
     } u;
-    float tab[8 * 64], gam[64], eh[64];
+    float tab[kTableFloats], gam[64], eh[64];
     float red[4][4][64];       // per wave: q.dq, k.A, k.F, k.M3
     float ip[4];               // <S, D>
     float tq[64], tk[64];      // over the group: q.dq, k.dk
@@ -56,17 +56,10 @@ struct GradLds {
 template <typename T, int P>
 __device__ __forceinline__ void put(T *dst, int at, f32x4 x)   // 4 consecutive elements
 {
-    typename Num<T>::Quad z;
+    typename Num<T>::Quad q[P];
+    split_quad<T, P>(x, q);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            z = x;
-        } else {
-            z = __builtin_convertvector(x, bf16x4);
-            x -= __builtin_convertvector(z, f32x4);
-        }
-        *reinterpret_cast<typename Num<T>::Quad *>(dst + i * kFragElems + at) = z;
-    }
+    for (int i = 0; i < P; ++i) *reinterpret_cast<typename Num<T>::Quad *>(dst + i * kTri + at) = q[i];
 }
 
 template <typename T, int P>
@@ -75,7 +68,7 @@ __device__ __forceinline__ void put1(T *dst, int at, float x)
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const T z = (T)x;
-        dst[i * kFragElems + at] = z;
+        dst[i * kTri + at] = z;
         x -= (float)z;
     }
 }
@@ -144,20 +137,13 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
                 }
                 const int at = t * LT + kpos(v);
                 *reinterpret_cast<Quad *>(s.u.in.dy + at) = x;
+                Quad rz[P], ez[P];
+                split_quad<T, P>(r, rz);
+                split_quad<T, P>(e, ez);
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    Quad rz, ez;
-                    if constexpr (sizeof(T) == 4) {
-                        rz = r;
-                        ez = e;
-                    } else {
-                        rz = __builtin_convertvector(r, bf16x4);
-                        r -= __builtin_convertvector(rz, f32x4);
-                        ez = __builtin_convertvector(e, bf16x4);
-                        e -= __builtin_convertvector(ez, f32x4);
-                    }
-                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * LT + at) = rz;
-                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * LT + at) = ez;
+                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * LT + at) = rz[p];
+                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * LT + at) = ez[p];
                 }
             }
             __syncthreads();
@@ -207,8 +193,8 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
             }
         }
         if (tid < 64) {
-            const float G = s.tab[4 * 64 + tid] + s.tab[5 * 64 + tid];
-            const float dhi = s.tab[4 * 64 + 63] - s.tab[4 * 64 + tid], dlo = s.tab[5 * 64 + 63] - s.tab[5 * 64 + tid];
+            const float G = s.tab[tid] + s.tab[64 + tid];
+            const float dhi = s.tab[63] - s.tab[tid], dlo = s.tab[64 + 63] - s.tab[64 + tid];
             s.gam[tid] = __builtin_amdgcn_exp2f(G);
             s.eh[tid] = __builtin_amdgcn_exp2f(dhi + dlo);
         }
@@ -219,8 +205,8 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
 #pragma unroll
         for (int zx = 0; zx < 2; ++zx) {
             const int jt = zx ? 3 - w : w, j = 16 * jt + l16;
-            const float Ghj = s.tab[4 * 64 + j], Glj = s.tab[5 * 64 + j];
-            const float cj = s.tab[3 * 64 + j] * s.tab[6 * 64 + j];   // beta rk
+            const float Ghj = s.tab[j], Glj = s.tab[64 + j];
+            const float cj = s.tab[2 * 64 + j] * s.tab[3 * 64 + j];   // beta rk
             T *wa = s.u.w[zx], *wt = s.u.w[2 + zx];
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
@@ -231,22 +217,15 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
                     const int i = 16 * it + 4 * lg + r;
                     float v = 0.f;
                     if (zx ? i > j : i >= j) {
-                        const float gd = __builtin_amdgcn_exp2f((s.tab[4 * 64 + i] - Ghj) + (s.tab[5 * 64 + i] - Glj));
+                        const float gd = __builtin_amdgcn_exp2f((s.tab[i] - Ghj) + (s.tab[64 + i] - Glj));
                         v = gd * (zx ? -X[it][r] : Z[it][r]);
                     }
                     // row i, k = j
-                    put1<T, P>(wa, (low_frag(it, jt >> 1) * 64 + (l16 >> 2) * 16 + 4 * lg + r) * 8 + (jt & 1) * 4 + (l16 & 3),
-                               v * cj);
-                    x[r] = v * s.tab[(zx ? 6 : 7) * 64 + i];
+                    put1<T, P>(wa, (tile_id(it, jt) * 64 + (l16 >> 2) * 16 + 4 * lg + r) * 4 + (l16 & 3), v * cj);
+                    x[r] = v * s.tab[(zx ? 3 : 4) * 64 + i];
                 }
                 // row j, k = i
-                put<T, P>(wt, (up_frag(jt, it >> 1) * 64 + lane) * 8 + (it & 1) * 4, x);
-                if (it == jt) {   // the half of a fragment beyond the diagonal
-                    if (jt & 1)
-                        put<T, P>(wt, (up_frag(jt, it >> 1) * 64 + lane) * 8, zero4());
-                    else
-                        put<T, P>(wa, (low_frag(it, jt >> 1) * 64 + lane) * 8 + 4, zero4());
-                }
+                put<T, P>(wt, (tile_id(it, jt) * 64 + lane) * 4, x);
             }
         }
         __syncthreads();
@@ -266,18 +245,18 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
             for (int it = 0; it < 4; ++it) {
                 const f32x4 gam = *reinterpret_cast<const f32x4 *>(s.gam + 16 * it + 4 * lg);
                 const f32x4 eh = *reinterpret_cast<const f32x4 *>(s.eh + 16 * it + 4 * lg);
-                const f32x4 be = row4(s.tab, 3, 16 * it + 4 * lg);
-                const f32x4 rk = row4(s.tab, 6, 16 * it + 4 * lg), rq = row4(s.tab, 7, 16 * it + 4 * lg);
+                const f32x4 be = row4(s.tab, 2, 16 * it + 4 * lg);
+                const f32x4 rk = row4(s.tab, 3, 16 * it + 4 * lg), rq = row4(s.tab, 4, 16 * it + 4 * lg);
                 f32x4 q1 = gam * M1[it][n], A = -gam * M2[it][n], m3 = eh * M3[it][n], F = m3;
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks) {
-                    q1 = mma(q1, load_packed<T, P>(s.u.w[0], low_frag(it, ks), lane), kf2[ks]);
-                    A = mma(A, load_packed<T, P>(s.u.w[1], low_frag(it, ks), lane), kf2[ks]);
+                    q1 = mma(q1, load_tri<T, P, false>(s.u.w[0], it, ks, lane), kf2[ks]);
+                    A = mma(A, load_tri<T, P, false>(s.u.w[1], it, ks, lane), kf2[ks]);
                 }
 #pragma unroll
                 for (int ks = it / 2; ks < 2; ++ks) {
-                    F = mma(F, load_packed<T, P>(s.u.w[2], up_frag(it, ks), lane), qf2[ks]);
-                    F = mma(F, load_packed<T, P>(s.u.w[3], up_frag(it, ks), lane), kf2[ks]);
+                    F = mma(F, load_tri<T, P, true>(s.u.w[2], it, ks, lane), qf2[ks]);
+                    F = mma(F, load_tri<T, P, true>(s.u.w[3], it, ks, lane), kf2[ks]);
                 }
                 // this lane's q, k of the tile: rows 16 it + 4 lg + r
                 f32x4 kv, qv;
@@ -317,11 +296,11 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 x[i] = (s.red[0][i][lane] + s.red[1][i][lane]) + (s.red[2][i][lane] + s.red[3][i][lane]);
-            const float be = s.tab[3 * 64 + lane];
+            const float be = s.tab[2 * 64 + lane];
             double dG = (double)x[0] + x[1] - (double)be * x[2];
             const double end = wave_sum((double)be * x[3]);
             if (lane == 63)
-                dG += end + (double)__builtin_amdgcn_exp2f(s.tab[4 * 64 + 63]) * ((double)s.ip[0] + s.ip[1] + ((double)s.ip[2] + s.ip[3]));
+                dG += end + (double)__builtin_amdgcn_exp2f(s.tab[63]) * ((double)s.ip[0] + s.ip[1] + ((double)s.ip[2] + s.ip[3]));
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double dn = __shfl_down(dG, d);
@@ -347,7 +326,7 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
             for (int r = 0; r < 4; ++r) {
                 const int t = 16 * it + 4 * lg + r;
                 if (t >= c.len) continue;
-                const float rq = s.tab[7 * 64 + t], rk = s.tab[6 * 64 + t];
+                const float rq = s.tab[4 * 64 + t], rk = s.tab[3 * 64 + t];
                 float x = dq[it][n][r] * rq, z = dk[it][n][r] * rk;
                 if (a.norm) {
                     const float nq = rq / a.scale;   // 1 / |q|

@@ -14,13 +14,12 @@ namespace wkv7 {
 namespace gdr {
 
 constexpr int kChunk = 64;   // tokens of a chunk
-// A chunk's triangular factors are kept in fragment order: 6 fragments (the
-// 16 x 32 blocks that touch the triangle) of 64 lanes x 8 values, per part.
-constexpr int kFragElems = 6 * 64 * 8;
 // bf16 parts that stand for an fp32 value as a matrix operand.
 constexpr int kParts = 3;
-// Per chunk and value head: 8 rows of 64 floats (gdr_prep.hip).
-constexpr int kTableFloats = 8 * 64;
+// Per chunk and value head, from the reverse scan to the gradients, per
+// token: the inclusive sum of g log2(e) as a sum of two floats, beta, and the
+// reciprocal lengths of k and (times the scale) q.
+constexpr int kTableFloats = 5 * 64;
 
 // Where the chunks of the sequences lie.
 struct Map {
@@ -28,6 +27,22 @@ struct Map {
     int64_t T, nseq, nck;    // tokens of a row, sequences, chunks per row (unpacked)
     int64_t slots;           // chunk slots in the workspace
 };
+
+// Whether the scans' workgroups make the chunks' triangular factors themselves
+// (gdr_scan.hip) or find them in memory, made by a kernel before (gdr_prep.hip).
+// In memory they cost 26 KB (forward) and 31 KB (reverse) per chunk and head,
+// written and read, against 32 KB of inputs and outputs at K = V = 64 in bf16:
+// there the scan at 8 x 4096 x 32 takes 313 us instead of 394 us and 186 us for
+// the kernel before it.  With wider heads or fp32 the making of a chunk's
+// factors takes longer than its slabs do (fp32, same shape: 820 us against
+// 459 + 264; K = V = 128, 4 x 4096 x 16: 474 against 420 + 43), and with few
+// workgroups the waves that make them would idle the chip.
+inline bool scan_makes_factors(int dtype, int64_t K, int64_t V, int64_t units)
+{
+    return dtype == WKV7_BF16 && K == 64 && V <= 64 && units >= 128;
+}
+// Bytes of a chunk's factors in memory.
+size_t factor_bytes(int dtype, bool transposed);
 
 struct Launch {
     Map map;
@@ -45,17 +60,15 @@ struct Launch {
     void *dq = nullptr, *dk = nullptr, *dv = nullptr;
     float *dg = nullptr, *dbeta = nullptr, *ds0 = nullptr;
     float *ws_ds = nullptr, *ws_dr = nullptr;   // [slots][Hv][K][V], [slots][Hv][64][V]
-    // both
-    float *table = nullptr;                     // [slots][Hv][8][64]
-    void *tfrag = nullptr, *pfrag = nullptr;    // [slots][Hv][parts][6][64][8]
+    float *table = nullptr;                     // [slots][Hv][5][64]
+    void *factors = nullptr;                    // [slots][Hv][factor_bytes], or null
 };
 
-// Triangular factors and decay tables of every chunk; transposed ones for
-// the backward.
+// The factors of every chunk; transposed ones, and the tables, for the backward.
 hipError_t launch_prep(const Launch &a, bool transposed, hipStream_t stream);
 // The forward scan over the chunks: y, sT and the record, each where asked for.
 hipError_t launch_scan(const Launch &a, hipStream_t stream);
-// The reverse scan: dv, ds0, and the chunks' state gradients and dR rows.
+// The reverse scan: dv, ds0, and the chunks' state gradients, dR rows and tables.
 hipError_t launch_reverse(const Launch &a, hipStream_t stream);
 // dq, dk, dg, dbeta of every chunk.
 hipError_t launch_grads(const Launch &a, hipStream_t stream);

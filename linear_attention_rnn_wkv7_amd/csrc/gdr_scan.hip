@@ -1,12 +1,13 @@
 // The scans over the chunks, forward and reverse (the mathematics and the
-// operand layouts: gdr_device.h).
+// operand layouts: gdr_device.h, gdr_factor.h).
 //
 // One wave owns 16 value columns of one sequence's head: its K x 16 slab of
 // the state stays in registers as result tiles, and every product of the
 // chain takes its other operand from LDS, so that a chunk needs no exchange
-// between waves.  The waves of a workgroup share that operand: K and Q by
-// rows, K (and in the reverse scan Q) transposed, and the chunk's triangular
-// factors.
+// between waves.  The waves of a workgroup share that operand: K and Q, by
+// rows and, through transposing reads, by columns, and the chunk's triangular
+// factors.  Those come from memory, or (scan_makes_factors) are made ahead of
+// the slabs by waves of their own in the same workgroup and never leave LDS.
 //
 // Reverse, from the gradient D of the state behind the chunk:
 //     dE = P^T dY + w * (K D),  w_j = (gamma_C / gamma_j) beta_j
@@ -14,7 +15,7 @@
 //     D0 = gamma_C D + (gamma Q)^T dY - (gamma K)^T dR
 // It leaves D (per chunk) and dR for gdr_grads.hip.
 
-#include "gdr_device.h"
+#include "gdr_factor.h"
 
 namespace wkv7 {
 namespace gdr {
@@ -28,19 +29,13 @@ struct ScanArgs {
     T *y, *dv;
     float *sT, *ds0;
     float *st, *rows;    // record: states and E; reverse: D and dR
-    const float *table;
-    const T *tfrag, *pfrag;
+    float *table;        // reverse
+    const float *g, *beta;
+    const char *factors;
     int64_t Hk, Hv, V;
-    int group;
+    int group, norm;
+    float scale;
 };
-
-// The lane's first row and column in a wave's tiles, fresh to the compiler at
-// each use: otherwise it keeps every offset made from it in a register.
-__device__ __forceinline__ uint32_t fresh(uint32_t x)
-{
-    asm volatile("" : "+v"(x));
-    return x;
-}
 
 // A wave's 64 x 16 tiles of a chunk of a [tokens][Hv][V] tensor, by buffer
 // accesses: rows behind the chunk's last read as zero and are not written.
@@ -55,19 +50,25 @@ struct Cols {
     {
     }
     __device__ __forceinline__ uint32_t off(int i) const { return at + (16 * (i >> 2) + (i & 3)) * step; }
-    __device__ __forceinline__ T load(int i) const
+    // The bits, one register to a value: as 16-bit values the compiler would
+    // pack them in pairs, and wait for the loads to do so.
+    __device__ __forceinline__ uint32_t load(int i) const
     {
         if constexpr (sizeof(T) == 4)
-            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off(i), 0, 0));
+            return __builtin_amdgcn_raw_buffer_load_b32(buf, (int)off(i), 0, 0);
         else
-            return __builtin_bit_cast(T, (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(buf, (int)off(i), 0, 0));
+            return __builtin_amdgcn_raw_buffer_load_b16(buf, (int)off(i), 0, 0);
+    }
+    __device__ static __forceinline__ float value(uint32_t u)
+    {
+        return sizeof(T) == 4 ? __builtin_bit_cast(float, u) : bf16_lo(u);
     }
     __device__ __forceinline__ void store(int i, float x) const
     {
         if constexpr (sizeof(T) == 4)
             bstore(buf, off(i), x);
         else
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (T)x), buf, (int)off(i), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)pack_bf16(x, x), buf, (int)off(i), 0, 0);
     }
 };
 
@@ -98,38 +99,21 @@ __device__ __forceinline__ Pos chunk_at(int64_t lo, int64_t hi, int64_t slot0, i
     return {tok, (slot0 + c) * Hv + hv, hi - tok < kChunk ? (int)(hi - tok) : kChunk};
 }
 
-// One chunk's operands in LDS.  The copies of the next chunk run while this
-// one is computed, into a second set, where two fit into 160 KB (all but
-// fp32 with K = 128).
+// A workgroup's LDS.  kMake: two sets of K and Q, so that the next chunk's
+// copies run while one is computed, two of factors, one read and one being
+// written, and the scratch of the waves that write them.  Else: two sets of
+// all, or one where two do not fit (fp32 with K = 128).
+constexpr int kMakers = 4;
 template <typename T, int K, int PP>
-struct Operands {
+struct ScanLds {
     static constexpr int kMat = Swizzled<T, K>::kBytes;
-    static constexpr int kT = Num<T>::kPlanes * kFragElems * (int)sizeof(T), kP = PP * kFragElems * (int)sizeof(T);
-    static constexpr int kTab = kTableFloats * 4;
-    static constexpr int kBytes = 2 * kMat + kT + kP + kTab;
-    static constexpr int kSets = 2 * kBytes <= 160 * 1024 ? 2 : 1;
-    char *base;
-
-    __device__ __forceinline__ char *k() const { return base; }
-    __device__ __forceinline__ char *q() const { return base + kMat; }
-    __device__ __forceinline__ const T *t() const { return reinterpret_cast<const T *>(base + 2 * kMat); }
-    __device__ __forceinline__ const T *p() const { return reinterpret_cast<const T *>(base + 2 * kMat + kT); }
-    __device__ __forceinline__ const float *tab() const
-    {
-        return reinterpret_cast<const float *>(base + 2 * kMat + kT + kP);
-    }
-    template <bool kAll>
-    __device__ __forceinline__ void copy(const ScanArgs<T> &a, const Pos &at, int64_t hk, int lane) const
-    {
-        const int64_t o = (at.tok * a.Hk + hk) * K;
-        dma_rows<T, K>(k(), a.k + o, a.Hk * K, at.len, lane);
-        dma_flat<kT>(base + 2 * kMat, a.tfrag + at.ch * (kT / (int)sizeof(T)), lane);
-        dma_flat<kTab>(base + 2 * kMat + kT + kP, a.table + at.ch * kTableFloats, lane);
-        if constexpr (kAll) {
-            dma_rows<T, K>(q(), a.q + o, a.Hk * K, at.len, lane);
-            dma_flat<kP>(base + 2 * kMat + kT, a.pfrag + at.ch * (kP / (int)sizeof(T)), lane);
-        }
-    }
+    static constexpr int kSets = 2 * (2 * kMat + (int)sizeof(Factor<T, PP>)) <= 160 * 1024 ? 2 : 1;
+    char k[kSets][kMat], q[kSets][kMat];
+    Factor<T, PP> f[kSets];
+};
+template <typename T, int K, int PP>
+struct MakeLds : ScanLds<T, K, PP> {
+    FactorLds scratch[kMakers];
 };
 
 template <typename T, int P, int Q>
@@ -141,45 +125,136 @@ __device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
     return g;
 }
 
-// The last wave of a workgroup copies the operands, chunk by chunk, one ahead
-// of the others: issuing copies stalls whenever the memory system has no room
-// for more, and would stall the products with it.  One barrier per chunk: the
-// copies for it have landed, and the set of the chunk before is free.
-template <typename T, int K, int PP, bool kAll>
-__device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, char *buf, int64_t lo, int64_t hi, int64_t slot0,
-                                          int64_t hv, int64_t hk, int64_t first, int64_t step, int64_t nc, int lane)
+// The waves of a workgroup run in steps, one chunk of the slabs to a step,
+// with a barrier between two steps: the slabs take chunk c in step c (the c-th
+// chunk of their direction), its operands arrive in step c - 1.
+
+// One wave copies them from memory: issuing copies stalls whenever the memory
+// system has no room for more, and would stall the products with it.
+template <typename T, int K, int PP, bool kTrans>
+__device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K, PP> &s, int64_t lo, int64_t hi, int64_t slot0,
+                                          int64_t hv, int64_t hk, int64_t nc, int lane)
 {
-    using Op = Operands<T, K, PP>;
+    using L = ScanLds<T, K, PP>;
+    using F = Factor<T, PP>;
     __builtin_amdgcn_s_setprio(2);
-    for (int64_t i = 0, c = first; i < nc; ++i, c += step) {
-        if (Op::kSets == 1 && i > 0) __syncthreads();   // the only set is free
-        Op{buf + (Op::kSets == 2 ? (i & 1) * Op::kBytes : 0)}.template copy<kAll>(
-            a, chunk_at(lo, hi, slot0, c, a.Hv, hv), hk, lane);
+    for (int64_t i = 0; i < nc; ++i) {
+        const Pos at = chunk_at(lo, hi, slot0, kTrans ? nc - 1 - i : i, a.Hv, hv);
+        const int64_t o = (at.tok * a.Hk + hk) * K;
+        const int set = L::kSets == 2 ? (int)(i & 1) : 0;
+        if (L::kSets == 1 && i > 0) __syncthreads();   // the only set is free
+        dma_rows<T, K>(s.k[set], a.k + o, a.Hk * K, at.len, lane);
+        dma_flat<sizeof(F)>(&s.f[set], a.factors + at.ch * sizeof(F), lane);
+        dma_rows<T, K>(s.q[set], a.q + o, a.Hk * K, at.len, lane);
         wait_dma();
         __syncthreads();
     }
 }
 
-constexpr int kMaxThreads = 64 * 9;   // 8 slabs and the copies
+// kMakers waves take turns at the factors: wave c % kMakers makes those of
+// chunk c in steps c - kMakers to c - 1, a stage to a step, and writes them in
+// the last.  The wave in its first stage, which waits for memory in any case,
+// also copies K and Q for the next step.
+template <typename T, int K, int PP, bool kTrans>
+__device__ __forceinline__ void make_loop(const ScanArgs<T> &a, MakeLds<T, K, PP> &s, int maker, bool tables, int64_t lo,
+                                          int64_t hi, int64_t slot0, int64_t hv, int64_t hk, int64_t nc, int lane)
+{
+    static_assert(MakeLds<T, K, PP>::kSets == 2, "two sets");
+    int64_t steps = nc + kMakers - 1;   // barriers still to come
+    auto next = [&]() {
+        if (steps > 0) __syncthreads();
+        --steps;
+    };
+    for (int i = 0; i < maker; ++i) next();
+    for (int64_t i = maker;; i += kMakers) {
+        if (steps <= 0) break;
+        const int64_t j = i - kMakers + 1;   // the next step's chunk
+        const bool made = i < nc;
+        const Pos at = chunk_at(lo, hi, slot0, kTrans ? nc - 1 - i : i, a.Hv, hv);
+        if (j >= 0 && j < nc) {
+            const Pos to = chunk_at(lo, hi, slot0, kTrans ? nc - 1 - j : j, a.Hv, hv);
+            const int64_t o = (to.tok * a.Hk + hk) * K;
+            dma_rows<T, K>(s.k[j & 1], a.k + o, a.Hk * K, to.len, lane);
+            dma_rows<T, K>(s.q[j & 1], a.q + o, a.Hk * K, to.len, lane);
+        }
+        Factors<T, K, kTrans> f;
+        if (made) {
+            const int64_t o = (at.tok * a.Hk + hk) * K, og = at.tok * a.Hv + hv;
+            f.products(s.scratch[maker], a.k + o, a.q + o, a.g + og, a.beta + og, a.Hk, a.Hv, at.len, a.norm, a.scale,
+                       (int)fresh(lane));
+        }
+        wait_dma();
+        next();
+        if (made)
+            f.decays(s.scratch[maker], kTrans && tables ? a.table + at.ch * kTableFloats : nullptr, at.len, (int)fresh(lane));
+        next();
+        if (made) f.solve(s.scratch[maker], (int)fresh(lane));
+        next();
+        Factor<T, PP> &to = s.f[i & 1];
+        if (made) f.template finish<PP>(to.t, to.p, to.w, (int)fresh(lane));
+        next();
+    }
+}
 
-template <typename T, int K, bool kY>
-__global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
+// The waves besides the slabs': returns false in a slab's wave.
+template <typename T, int K, int PP, bool kTrans, bool kMake>
+__device__ __forceinline__ bool feed(const ScanArgs<T> &a, char *buf, int wave, int slabs, bool tables, int64_t lo,
+                                     int64_t hi, int64_t slot0, int64_t hv, int64_t hk, int64_t nc, int lane)
+{
+    if constexpr (kMake) {
+        if (wave >= slabs) {
+            if (nc > 0)
+                make_loop<T, K, PP, kTrans>(a, *reinterpret_cast<MakeLds<T, K, PP> *>(buf), wave - slabs, tables, lo, hi,
+                                            slot0, hv, hk, nc, lane);
+            return true;
+        }
+    } else {
+        if (wave == slabs) {
+            copy_loop<T, K, PP, kTrans>(a, *reinterpret_cast<ScanLds<T, K, PP> *>(buf), lo, hi, slot0, hv, hk, nc, lane);
+            return true;
+        }
+    }
+    return false;
+}
+
+// Before a slab's first step.
+template <bool kMake>
+__device__ __forceinline__ void first_step()
+{
+    for (int i = 0; i < (kMake ? kMakers : 1); ++i) __syncthreads();
+}
+
+// Between two steps of a slab.
+template <int kSets>
+__device__ __forceinline__ void step_end()
+{
+    if (kSets == 1) __syncthreads();   // the only set is free: the next copies follow
+    __syncthreads();
+}
+
+template <typename T, int K, int PP, bool kMake>
+constexpr int kScanLds = kMake ? (int)sizeof(MakeLds<T, K, PP>) : (int)sizeof(ScanLds<T, K, PP>);
+// The most waves: 8 slabs and the copies, or 4 slabs and the makers.
+template <bool kMake>
+constexpr int kMaxThreads = 64 * (kMake ? 4 + kMakers : 8 + 1);
+
+template <typename T, int K, bool kMake, bool kY>
+__global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes, PY = kYParts<T>;
     constexpr int KT = K / 16, KS = K / 32;
-    using Op = Operands<T, K, PY>;
+    using L = ScanLds<T, K, PY>;
     using Sw = Swizzled<T, K>;
-    __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
+    __shared__ __align__(16) char buf[kScanLds<T, K, PY, kMake>];
+    L &s = *reinterpret_cast<L *>(buf);
     const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), slabs = (blockDim.x >> 6) - 1;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int slabs = (int)(blockDim.x >> 6) - (kMake ? kMakers : 1);
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (wave == slabs) {
-        copy_loop<T, K, PY, kY>(a, buf, lo, hi, slot0, hv, hk, 0, 1, nc, lane);
-        return;
-    }
+    if (feed<T, K, PY, false, kMake>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
 
@@ -189,7 +264,7 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
     for (int i = 0; i < KT; ++i)
         S[i] = a.s0 && own ? *reinterpret_cast<const f32x4 *>(a.s0 + so + 16 * i) : zero4();
 
-    T vn[16];
+    uint32_t vn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const Cols<T> v(a.v + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
@@ -197,14 +272,15 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
         for (int i = 0; i < 16; ++i) vn[i] = v.load(i);
     };
     if (own && nc > 0) fetch(0);
+    if (nc > 0) first_step<kMake>();
     for (int64_t c = 0; c < nc; ++c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
-        const Op s{buf + (Op::kSets == 2 ? (c & 1) * Op::kBytes : 0)};
-        __syncthreads();
+        const int set = L::kSets == 2 ? (int)(c & 1) : 0;
+        const Factor<T, PY> &f = s.f[set];
         if (own) {
             f32x4 R[4], Y[4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = to_f32(vn[i]);
+            for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = Cols<T>::value(vn[i]);
             if (c + 1 < nc) fetch(c + 1);
             if (a.st) {
                 const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
@@ -220,13 +296,13 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
                     const Frag<T, P> Sf = make_frag<T, P>(S[2 * ks], S[2 * ks + 1]);
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
-                        acc[it] = mma(acc[it], Sw::rows(s.k(), it, ks, lg, l16), Sf);
+                        acc[it] = mma(acc[it], Sw::rows(s.k[set], it, ks, lg, l16), Sf);
                         if constexpr (kY)
-                            Y[it] = mma<PY>(Y[it], Sw::rows(s.q(), it, ks, lg, l16), first_parts<T, P, PY>(Sf));
+                            Y[it] = mma<PY>(Y[it], Sw::rows(s.q[set], it, ks, lg, l16), first_parts<T, P, PY>(Sf));
                     }
                 }
 #pragma unroll
-                for (int it = 0; it < 4; ++it) R[it] -= row4(s.tab(), 0, 16 * it + 4 * lg) * acc[it];
+                for (int it = 0; it < 4; ++it) R[it] -= row4(f.w, 0, 16 * it + 4 * lg) * acc[it];
             }
             const Frag<T, P> Rf[2] = {make_frag<T, P>(R[0], R[1]), make_frag<T, P>(R[2], R[3])};
             f32x4 E[4];
@@ -235,7 +311,7 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
                 E[it] = zero4();
 #pragma unroll
                 for (int ks = 0; ks <= it / 2; ++ks)
-                    E[it] = mma(E[it], load_packed<T, P>(s.t(), low_frag(it, ks), lane), Rf[ks]);
+                    E[it] = mma(E[it], load_tri<T, P, false>(f.t, it, ks, lane), Rf[ks]);
             }
             if (a.rows) {
                 const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
@@ -247,26 +323,26 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
                 const Cols<T> y(a.y + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    Y[it] *= row4(s.tab(), 1, 16 * it + 4 * lg);
+                    Y[it] *= row4(f.w, 1, 16 * it + 4 * lg);
 #pragma unroll
                     for (int ks = 0; ks <= it / 2; ++ks)
-                        Y[it] = mma<PY>(Y[it], load_packed<T, PY>(s.p(), low_frag(it, ks), lane), Ef[ks]);
+                        Y[it] = mma<PY>(Y[it], load_tri<T, PY, false>(f.p, it, ks, lane), Ef[ks]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y.store(4 * it + r, Y[it][r]);
                 }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) E[it] *= row4(s.tab(), 2, 16 * it + 4 * lg);
+            for (int it = 0; it < 4; ++it) E[it] *= row4(f.w, 2, 16 * it + 4 * lg);
             const Frag<T, P> Wf[2] = {make_frag<T, P>(E[0], E[1]), make_frag<T, P>(E[2], E[3])};
-            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
+            const float last = f.w[192];
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 S[i] *= last;
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) S[i] = mma(S[i], Sw::cols(s.k(), i, ks, lg, l16), Wf[ks]);
+                for (int ks = 0; ks < 2; ++ks) S[i] = mma(S[i], Sw::cols(s.k[set], i, ks, lg, l16), Wf[ks]);
             }
         }
-        if (Op::kSets == 1 && c + 1 < nc) __syncthreads();
+        if (c + 1 < nc) step_end<L::kSets>();
     }
     if (a.sT && own) {
 #pragma unroll
@@ -274,24 +350,23 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_scan_kernel(ScanArgs<T> a)
     }
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
+template <typename T, int K, bool kMake>
+__global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes;
     constexpr int KT = K / 16, KS = K / 32;
-    using Op = Operands<T, K, P>;
+    using L = ScanLds<T, K, P>;
     using Sw = Swizzled<T, K>;
-    __shared__ __align__(16) char buf[Op::kSets * Op::kBytes];
+    __shared__ __align__(16) char buf[kScanLds<T, K, P, kMake>];
+    L &s = *reinterpret_cast<L *>(buf);
     const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), slabs = (blockDim.x >> 6) - 1;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int slabs = (int)(blockDim.x >> 6) - (kMake ? kMakers : 1);
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (wave == slabs) {
-        copy_loop<T, K, P, true>(a, buf, lo, hi, slot0, hv, hk, nc - 1, -1, nc, lane);
-        return;
-    }
+    if (feed<T, K, P, true, kMake>(a, buf, wave, slabs, blockIdx.x == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
 
@@ -301,7 +376,7 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
     for (int i = 0; i < KT; ++i)
         D[i] = a.dsT && own ? *reinterpret_cast<const f32x4 *>(a.dsT + so + 16 * i) : zero4();
 
-    T yn[16];
+    uint32_t yn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const Cols<T> y(a.dy + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
@@ -309,15 +384,16 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
         for (int i = 0; i < 16; ++i) yn[i] = y.load(i);
     };
     if (own && nc > 0) fetch(nc - 1);
+    if (nc > 0) first_step<kMake>();
     for (int64_t i = 0; i < nc; ++i) {
         const int64_t c = nc - 1 - i;
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
-        const Op s{buf + (Op::kSets == 2 ? (i & 1) * Op::kBytes : 0)};
-        __syncthreads();
+        const int set = L::kSets == 2 ? (int)(i & 1) : 0;
+        const Factor<T, P> &f = s.f[set];
         if (own) {
             f32x4 dY[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = to_f32(yn[j]);
+            for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = Cols<T>::value(yn[j]);
             if (c > 0) fetch(c - 1);
             const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
@@ -329,16 +405,16 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
             for (int ks = 0; ks < KS; ++ks) {
                 const Frag<T, P> Df = make_frag<T, P>(D[2 * ks], D[2 * ks + 1]);
 #pragma unroll
-                for (int jt = 0; jt < 4; ++jt) dE[jt] = mma(dE[jt], Sw::rows(s.k(), jt, ks, lg, l16), Df);
+                for (int jt = 0; jt < 4; ++jt) dE[jt] = mma(dE[jt], Sw::rows(s.k[set], jt, ks, lg, l16), Df);
             }
             {
                 const Frag<T, 1> dYf[2] = {make_frag<T, 1>(dY[0], dY[1]), make_frag<T, 1>(dY[2], dY[3])};
 #pragma unroll
                 for (int jt = 0; jt < 4; ++jt) {
-                    dE[jt] *= row4(s.tab(), 2, 16 * jt + 4 * lg);
+                    dE[jt] *= row4(f.w, 2, 16 * jt + 4 * lg);
 #pragma unroll
                     for (int ks = jt / 2; ks < 2; ++ks)
-                        dE[jt] = mma(dE[jt], load_packed<T, P>(s.p(), up_frag(jt, ks), lane), dYf[ks]);
+                        dE[jt] = mma(dE[jt], load_tri<T, P, true>(f.p, jt, ks, lane), dYf[ks]);
                 }
             }
             f32x4 dR[4];
@@ -351,19 +427,19 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
                     dR[jt] = zero4();
 #pragma unroll
                     for (int ks = jt / 2; ks < 2; ++ks)
-                        dR[jt] = mma(dR[jt], load_packed<T, P>(s.t(), up_frag(jt, ks), lane), dEf[ks]);
+                        dR[jt] = mma(dR[jt], load_tri<T, P, true>(f.t, jt, ks, lane), dEf[ks]);
                     rows.store(jt, dR[jt]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dv.store(4 * jt + r, dR[jt][r]);
                 }
             }
-            const float last = __builtin_amdgcn_exp2f(s.tab()[4 * 64 + 63]);
+            const float last = f.w[192];
 #pragma unroll
             for (int j = 0; j < KT; ++j) D[j] *= last;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
-                dY[jt] *= row4(s.tab(), 1, 16 * jt + 4 * lg);
-                dR[jt] *= -row4(s.tab(), 0, 16 * jt + 4 * lg);
+                dY[jt] *= row4(f.w, 1, 16 * jt + 4 * lg);
+                dR[jt] *= -row4(f.w, 0, 16 * jt + 4 * lg);
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -371,12 +447,12 @@ __global__ void __launch_bounds__(kMaxThreads) gdr_reverse_kernel(ScanArgs<T> a)
                 const Frag<T, P> Rf = make_frag<T, P>(dR[2 * ks], dR[2 * ks + 1]);
 #pragma unroll
                 for (int j = 0; j < KT; ++j) {
-                    D[j] = mma(D[j], Sw::cols(s.q(), j, ks, lg, l16), Yf);
-                    D[j] = mma(D[j], Sw::cols(s.k(), j, ks, lg, l16), Rf);
+                    D[j] = mma(D[j], Sw::cols(s.q[set], j, ks, lg, l16), Yf);
+                    D[j] = mma(D[j], Sw::cols(s.k[set], j, ks, lg, l16), Rf);
                 }
             }
         }
-        if (Op::kSets == 1 && c > 0) __syncthreads();
+        if (c > 0) step_end<L::kSets>();
     }
     if (a.ds0 && own) {
 #pragma unroll
@@ -402,8 +478,11 @@ ScanArgs<T> scan_args(const Launch &a)
     p.st = a.rec_s;
     p.rows = a.rec_e;
     p.table = a.table;
-    p.tfrag = static_cast<const T *>(a.tfrag);
-    p.pfrag = static_cast<const T *>(a.pfrag);
+    p.g = a.g;
+    p.beta = a.beta;
+    p.norm = a.norm;
+    p.scale = a.scale;
+    p.factors = static_cast<const char *>(a.factors);
     p.Hk = a.Hk;
     p.Hv = a.Hv;
     p.V = a.V;
@@ -411,41 +490,45 @@ ScanArgs<T> scan_args(const Launch &a)
     return p;
 }
 
-// Slabs per workgroup, a wave each: as many as there are (8 at most), fewer
-// while that leaves compute units without a workgroup.
-void scan_grid(const Launch &a, dim3 *grid, dim3 *block)
+// Slabs per workgroup, a wave each: as many as there are (`most` at most),
+// fewer while that leaves compute units without a workgroup.
+int scan_grid(const Launch &a, int most, dim3 *grid)
 {
     const int64_t slabs = a.V / 16, units = a.map.nseq * a.Hv;
-    int64_t groups = (slabs + 7) / 8;
+    int64_t groups = (slabs + most - 1) / most;
     while (units * groups < 256 && groups < slabs) ++groups;
     const int64_t per = (slabs + groups - 1) / groups;
     *grid = dim3((unsigned)((slabs + per - 1) / per), (unsigned)a.Hv, (unsigned)a.map.nseq);
-    *block = dim3((unsigned)(64 * (per + 1)));   // and the copies'
+    return (int)per;
 }
 
-template <typename T, int K>
+template <typename T, int K, bool kMake>
 hipError_t scan_t(const Launch &a, bool reverse, hipStream_t stream)
 {
     ScanArgs<T> p = scan_args<T>(a);
-    dim3 grid, block;
-    scan_grid(a, &grid, &block);
+    dim3 grid;
+    const int slabs = scan_grid(a, kMake ? 4 : 8, &grid);
+    const dim3 block(64 * (slabs + (kMake ? kMakers : 1)));
     if (reverse) {
         p.st = a.ws_ds;
         p.rows = a.ws_dr;
-        hipLaunchKernelGGL((gdr_reverse_kernel<T, K>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_reverse_kernel<T, K, kMake>), grid, block, 0, stream, p);
     } else if (a.y) {
-        hipLaunchKernelGGL((gdr_scan_kernel<T, K, true>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, true>), grid, block, 0, stream, p);
     } else {
-        hipLaunchKernelGGL((gdr_scan_kernel<T, K, false>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, false>), grid, block, 0, stream, p);
     }
     return hipGetLastError();
 }
 
 hipError_t scan_any(const Launch &a, bool reverse, hipStream_t stream)
 {
+    if (!a.factors) return scan_t<bf16, 64, true>(a, reverse, stream);
+    const hipError_t e = launch_prep(a, reverse, stream);
+    if (e != hipSuccess) return e;
     if (a.dtype == WKV7_F32)
-        return a.K == 64 ? scan_t<float, 64>(a, reverse, stream) : scan_t<float, 128>(a, reverse, stream);
-    return a.K == 64 ? scan_t<bf16, 64>(a, reverse, stream) : scan_t<bf16, 128>(a, reverse, stream);
+        return a.K == 64 ? scan_t<float, 64, false>(a, reverse, stream) : scan_t<float, 128, false>(a, reverse, stream);
+    return a.K == 64 ? scan_t<bf16, 64, false>(a, reverse, stream) : scan_t<bf16, 128, false>(a, reverse, stream);
 }
 
 }  // namespace

@@ -227,11 +227,13 @@ def test_rule_other_stream_and_workspace():
     for n in want:
         assert torch.equal(got[n], want[n]), n
     a = [d[n] for n in IN]
-    need = api.gdr_forward_workspace_bytes(1, 140, 1, 2, 64, 32, BF16)
+    need = api.gdr_backward_workspace_bytes(1, 140, 1, 2, 64, 32, BF16, ckpt_provided=False)
     ws = torch.empty(need, device="cuda", dtype=torch.uint8)
-    assert torch.equal(api.gdr_forward(*a, d["s0"], workspace=ws)[0], want["y"])
+    got = api.gdr_backward(*a, d["dy"], d["s0"], d["dsT"], workspace=ws)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
     with pytest.raises(Exception, match="workspace"):
-        api.gdr_forward(*a, d["s0"], workspace=ws[:need - 256])
+        api.gdr_backward(*a, d["dy"], d["s0"], d["dsT"], workspace=ws[:need - 256])
 
 
 def test_rule_captured_twice():
