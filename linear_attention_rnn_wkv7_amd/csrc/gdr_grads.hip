@@ -14,10 +14,11 @@
 // enter is a row dot of what dq, dk are made of, so no C x C array besides Z
 // and X is needed.)
 //
-// One workgroup of four waves per chunk and key head; it adds up the group's
-// value heads in registers.  Each wave owns K / 4 key columns: it reads its
-// rows of S and D once from memory as operands, and shares E, dR, dY in LDS.
-// Z and X tiles go through LDS into operand order once per chunk.
+// One workgroup per chunk and key head; it adds up the group's value heads in
+// registers.  Each of its K / 16 waves owns 16 key columns: it reads its rows
+// of S and D once from memory as operands.  E, dR, dY pass through LDS 32
+// values at a time, then Z and X, in operand order; so that two workgroups
+// share a compute unit and cover each other's waits.
 
 #include "gdr_factor.h"
 
@@ -37,19 +38,21 @@ struct GradArgs {
     float scale;
 };
 
+constexpr int kVB = 32;   // values of E, dR, dY in LDS at a time
+
 template <typename T, int K>
 struct GradLds {
-    static constexpr int P = Num<T>::kPlanes, LT = 64 + kPad<T>;
-    T kt[K * LT], qt[K * LT];
+    static constexpr int P = Num<T>::kPlanes, LV = kVB + kPad<T>, W = K / 16;
+    char k[Swizzled<T, K>::kBytes], q[Swizzled<T, K>::kBytes];
     union {
         struct {
-            T dy[64 * LT], dr[P * 64 * LT], e[P * 64 * LT];
+            T dy[64 * LV], dr[P * 64 * LV], e[P * 64 * LV];
         } in;
-        T w[4][P * kTri];   // W1, W2 (for dq, A), then transposed (for F)
+        T w[2][P * kTri];   // of Z, then of X: by rows, and transposed
     } u;
     float tab[kTableFloats], gam[64], eh[64];
-    float red[4][4][64];       // per wave: q.dq, k.A, k.F, k.M3
-    float ip[4];               // <S, D>
+    float red[4][W][64];       // q.dq, k.A, k.F, k.M3 of each wave's columns
+    float ip[W];               // <S, D>
     float tq[64], tk[64];      // over the group: q.dq, k.dk
 };
 
@@ -73,234 +76,210 @@ __device__ __forceinline__ void put1(T *dst, int at, float x)
     }
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
+// Row and column of triangle tile t.
+__device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
+
+// Row sums over the wave's 16 columns of x * y, into red.
+__device__ __forceinline__ void row_dots(float *red, int it, int lg, int l16, f32x4 x, f32x4 y)
+{
+    const f32x4 xy = x * y;
+    f32x4 z;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) z[r] = group_allreduce<16>(xy[r]);
+    if (l16 == 0) *reinterpret_cast<f32x4 *>(red + 16 * it + 4 * lg) = z;
+}
+
+template <typename T, int K, bool kShared>
+__global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
 {
     using L = GradLds<T, K>;
     using Quad = typename Num<T>::Quad;
-    constexpr int P = L::P, LT = L::LT, NT = K / 64;   // 16-column tiles per wave
+    using Sw = Swizzled<T, K>;
+    constexpr int P = L::P, LV = L::LV, W = L::W, NZ = (10 + W - 1) / W;   // tiles of Z, X per wave
     __shared__ __align__(16) char buf[sizeof(L)];
     L &s = *reinterpret_cast<L *>(buf);
     const int64_t slot = blockIdx.x, hk = blockIdx.y;
     const Chunk c = locate(a.map, slot);
     if (c.len == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, lg = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    for (int b = tid; b < 2 * 16 * (K / 4); b += 256) {
-        const int which = b / (16 * (K / 4)), i0 = b % (16 * (K / 4));
-        const int col = 4 * (i0 % (K / 4)), t0 = 4 * (i0 / (K / 4));
-        const T *src = (which ? a.k : a.q) + ((c.tok + t0) * a.Hk + hk) * K + col;
-        T *dst = which ? s.kt : s.qt;
-        Quad x[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            x[r] = Quad{};
-            if (t0 + r < c.len) x[r] = *reinterpret_cast<const Quad *>(src + r * a.Hk * K);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<Quad *>(dst + (col + i) * LT + kpos(t0)) = Quad{x[0][i], x[1][i], x[2][i], x[3][i]};
+    if (w < 2) {
+        dma_rows<T, K>(w ? s.q : s.k, (w ? a.q : a.k) + (c.tok * a.Hk + hk) * K, a.Hk * K, c.len, lane);
+        wait_dma();
     }
     if (tid < 64) s.tq[tid] = s.tk[tid] = 0.f;
 
-    f32x4 dq[4][NT], dk[4][NT];
+    f32x4 dq[4], dk[4];
+    if constexpr (kShared) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) dq[it][n] = dk[it][n] = zero4();
-
-    for (int gi = 0; gi < a.group; ++gi) {
+        for (int it = 0; it < 4; ++it) dq[it] = dk[it] = zero4();
+    }
+    for (int gi = 0; gi < (kShared ? a.group : 1); ++gi) {
         const int64_t hv = hk * a.group + gi, ch = slot * a.Hv + hv;
         __syncthreads();
-        for (int i = tid; i < kTableFloats / 4; i += 256)
+        for (int i = tid; i < kTableFloats / 4; i += 64 * W)
             reinterpret_cast<f32x4 *>(s.tab)[i] = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[i];
-        f32x4 M1[4][NT], M2[4][NT], M3[4][NT], Z[4], X[4];
+        f32x4 M1[4], M2[4], M3[4], Z[NZ], X[NZ];
         float ip = 0.f;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            Z[it] = X[it] = zero4();
+        for (int it = 0; it < 4; ++it) M1[it] = M2[it] = M3[it] = zero4();
 #pragma unroll
-            for (int n = 0; n < NT; ++n) M1[it][n] = M2[it][n] = M3[it][n] = zero4();
-        }
-        for (int64_t v0 = 0; v0 < a.V; v0 += 64) {
-            __syncthreads();
-            for (int b = tid; b < 64 * 16; b += 256) {
-                const int t = b >> 4, v = 4 * (b & 15);
-                const bool in = v0 + v < a.V;
-                Quad x = {};
-                f32x4 r = zero4(), e = zero4();
-                if (in) {
-                    if (t < c.len)
-                        x = *reinterpret_cast<const Quad *>(a.dy + ((c.tok + t) * a.Hv + hv) * a.V + v0 + v);
-                    r = *reinterpret_cast<const f32x4 *>(a.dR + (ch * 64 + t) * a.V + v0 + v);
-                    e = *reinterpret_cast<const f32x4 *>(a.E + (ch * 64 + t) * a.V + v0 + v);
-                }
-                const int at = t * LT + kpos(v);
-                *reinterpret_cast<Quad *>(s.u.in.dy + at) = x;
-                Quad rz[P], ez[P];
-                split_quad<T, P>(r, rz);
-                split_quad<T, P>(e, ez);
+        for (int i = 0; i < NZ; ++i) Z[i] = X[i] = zero4();
+        const float *Sr = a.S + (ch * K + 16 * w + l16) * a.V + 4 * lg, *Dr = a.D + (ch * K + 16 * w + l16) * a.V + 4 * lg;
+        for (int v0 = 0; v0 < (int)a.V; v0 += kVB) {
+            // V is a multiple of 16: the second half of the block may be beyond it
+            const bool half = v0 + 16 < (int)a.V;
+            f32x4 x[2] = {zero4(), zero4()}, d[2] = {zero4(), zero4()};
+            x[0] = *reinterpret_cast<const f32x4 *>(Sr + v0);
+            d[0] = *reinterpret_cast<const f32x4 *>(Dr + v0);
+            if (half) {
+                x[1] = *reinterpret_cast<const f32x4 *>(Sr + v0 + 16);
+                d[1] = *reinterpret_cast<const f32x4 *>(Dr + v0 + 16);
+            }
+            Quad yq[8 / W];
+            f32x4 rq[8 / W], eq[8 / W];
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * LT + at) = rz[p];
-                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * LT + at) = ez[p];
+            for (int n = 0; n < 8 / W; ++n) {
+                const int t = (tid + n * 64 * W) >> 3, v = v0 + 4 * (tid & 7);
+                yq[n] = Quad{};
+                rq[n] = eq[n] = zero4();
+                if (v < (int)a.V) {
+                    if (t < c.len) yq[n] = *reinterpret_cast<const Quad *>(a.dy + ((c.tok + t) * a.Hv + hv) * a.V + v);
+                    rq[n] = *reinterpret_cast<const f32x4 *>(a.dR + (ch * 64 + t) * a.V + v);
+                    eq[n] = *reinterpret_cast<const f32x4 *>(a.E + (ch * 64 + t) * a.V + v);
                 }
             }
+            if (v0 > 0) __syncthreads();   // the block before is done with
+#pragma unroll
+            for (int n = 0; n < 8 / W; ++n) {
+                const int at = ((tid + n * 64 * W) >> 3) * LV + kpos(4 * (tid & 7));
+                Quad rz[P], ez[P];
+                split_quad<T, P>(rq[n], rz);
+                split_quad<T, P>(eq[n], ez);
+                *reinterpret_cast<Quad *>(s.u.in.dy + at) = yq[n];
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * LV + at) = rz[p];
+                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * LV + at) = ez[p];
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 xd = x[h] * d[h];
+                ip += (xd[0] + xd[1]) + (xd[2] + xd[3]);
+            }
+            const Frag<T, P> Sf = make_frag<T, P>(x[0], x[1]), Df = make_frag<T, P>(d[0], d[1]);
             __syncthreads();
 #pragma unroll
-            for (int vs = 0; vs < 2; ++vs) {
-                Frag<T, P> Sf[NT], Df[NT];
+            for (int it = 0; it < 4; ++it) {
+                M1[it] = mma(M1[it], load_frag<T, 1>(s.u.in.dy, 16 * it + l16, LV, 0, lg, 0), Sf);
+                M2[it] = mma(M2[it], load_frag<T, P>(s.u.in.dr, 16 * it + l16, LV, 0, lg, 64 * LV), Sf);
+                M3[it] = mma(M3[it], load_frag<T, P>(s.u.in.e, 16 * it + l16, LV, 0, lg, 64 * LV), Df);
+            }
+            // tiles w, w + W, .. of Z, and from the other end of X
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 x[2], d[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        x[h] = d[h] = zero4();
-                        const int64_t v = v0 + 32 * vs + 16 * h + 4 * lg;
-                        const int64_t o = (ch * K + 16 * (NT * w + n) + l16) * a.V + v;
-                        if (v < a.V) {
-                            x[h] = *reinterpret_cast<const f32x4 *>(a.S + o);
-                            d[h] = *reinterpret_cast<const f32x4 *>(a.D + o);
-                        }
-                        const f32x4 xd = x[h] * d[h];
-                        ip += (xd[0] + xd[1]) + (xd[2] + xd[3]);
-                    }
-                    Sf[n] = make_frag<T, P>(x[0], x[1]);
-                    Df[n] = make_frag<T, P>(d[0], d[1]);
-                }
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag<T, 1> y = load_frag<T, 1>(s.u.in.dy, 16 * it + l16, LT, vs, lg, 0);
-                    const Frag<T, P> r = load_frag<T, P>(s.u.in.dr, 16 * it + l16, LT, vs, lg, 64 * LT);
-                    const Frag<T, P> e = load_frag<T, P>(s.u.in.e, 16 * it + l16, LT, vs, lg, 64 * LT);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        M1[it][n] = mma(M1[it][n], y, Sf[n]);
-                        M2[it][n] = mma(M2[it][n], r, Sf[n]);
-                        M3[it][n] = mma(M3[it][n], e, Df[n]);
-                    }
-                }
-                // Z column tile w, X column tile 3 - w: five tiles per wave
-                const Frag<T, P> ez = load_frag<T, P>(s.u.in.e, 16 * w + l16, LT, vs, lg, 64 * LT);
-                const Frag<T, P> ex = load_frag<T, P>(s.u.in.e, 16 * (3 - w) + l16, LT, vs, lg, 64 * LT);
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    if (it >= w)
-                        Z[it] = mma(Z[it], load_frag<T, 1>(s.u.in.dy, 16 * it + l16, LT, vs, lg, 0), ez);
-                    if (it >= 3 - w)
-                        X[it] = mma(X[it], load_frag<T, P>(s.u.in.dr, 16 * it + l16, LT, vs, lg, 64 * LT), ex);
-                }
+            for (int i = 0; i < NZ; ++i) {
+                const int tz = w + i * W, tx = 9 - tz;
+                if (tz >= 10) continue;
+                const int zi = tile_row(tz), zj = tz - tile_id(zi, 0), xi = tile_row(tx), xj = tx - tile_id(xi, 0);
+                Z[i] = mma(Z[i], load_frag<T, 1>(s.u.in.dy, 16 * zi + l16, LV, 0, lg, 0),
+                           load_frag<T, P>(s.u.in.e, 16 * zj + l16, LV, 0, lg, 64 * LV));
+                X[i] = mma(X[i], load_frag<T, P>(s.u.in.dr, 16 * xi + l16, LV, 0, lg, 64 * LV),
+                           load_frag<T, P>(s.u.in.e, 16 * xj + l16, LV, 0, lg, 64 * LV));
             }
         }
         if (tid < 64) {
-            const float G = s.tab[tid] + s.tab[64 + tid];
-            const float dhi = s.tab[63] - s.tab[tid], dlo = s.tab[64 + 63] - s.tab[64 + tid];
-            s.gam[tid] = __builtin_amdgcn_exp2f(G);
-            s.eh[tid] = __builtin_amdgcn_exp2f(dhi + dlo);
+            s.gam[tid] = __builtin_amdgcn_exp2f(s.tab[tid] + s.tab[64 + tid]);
+            s.eh[tid] = __builtin_amdgcn_exp2f((s.tab[63] - s.tab[tid]) + (s.tab[64 + 63] - s.tab[64 + tid]));
         }
         ip = wave_sum(ip);
         if (lane == 0) s.ip[w] = ip;
-        __syncthreads();   // E, dR, dY are done with; the table is there
-        // Z and X with their decays, as operands
+        // this wave's columns of q and k as operands; position 4 (it & 1) + r of
+        // step it / 2 is row 16 it + 4 lg + r
+        Frag<T, 1> kf[2], qf[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            kf[ks] = Sw::cols(s.k, w, ks, lg, l16);
+            qf[ks] = Sw::cols(s.q, w, ks, lg, l16);
+        }
+        auto value = [&](const Frag<T, 1> (&f)[2], int it, int kind) {
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = to_f32(f[it >> 1].p[0][(it & 1) * 4 + r]);
+            return x * row4(s.tab, kind, 16 * it + 4 * lg);
+        };
+        __syncthreads();   // E, dR, dY are done with; gam and eh are there
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {   // now M1, M2, M3 become dq, A, F
+            const f32x4 gam = row4(s.gam, 0, 16 * it + 4 * lg);
+            M1[it] *= gam;
+            M2[it] *= -gam;
+            M3[it] *= row4(s.eh, 0, 16 * it + 4 * lg);
+            row_dots(s.red[3][w], it, lg, l16, value(kf, it, 3), M3[it]);
+        }
 #pragma unroll
         for (int zx = 0; zx < 2; ++zx) {
-            const int jt = zx ? 3 - w : w, j = 16 * jt + l16;
-            const float Ghj = s.tab[j], Glj = s.tab[64 + j];
-            const float cj = s.tab[2 * 64 + j] * s.tab[3 * 64 + j];   // beta rk
-            T *wa = s.u.w[zx], *wt = s.u.w[2 + zx];
+            if (zx) __syncthreads();   // Z's operands are done with
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                if (it < jt) continue;
+            for (int n = 0; n < NZ; ++n) {   // with their decays, as operands
+                const int t = zx ? 9 - (w + n * W) : w + n * W;
+                if (w + n * W >= 10) continue;
+                const int it = tile_row(t), jt = t - tile_id(it, 0), j = 16 * jt + l16, i0 = 16 * it + 4 * lg;
+                const float Ghj = s.tab[j], Glj = s.tab[64 + j], cj = s.tab[2 * 64 + j] * s.tab[3 * 64 + j];   // beta rk
+                const f32x4 gh = row4(s.tab, 0, i0), gl = row4(s.tab, 1, i0);
                 f32x4 x;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * it + 4 * lg + r;
-                    float v = 0.f;
-                    if (zx ? i > j : i >= j) {
-                        const float gd = __builtin_amdgcn_exp2f((s.tab[i] - Ghj) + (s.tab[64 + i] - Glj));
-                        v = gd * (zx ? -X[it][r] : Z[it][r]);
-                    }
+                    const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj));
+                    x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -X[n][r] : Z[n][r]) : 0.f;
                     // row i, k = j
-                    put1<T, P>(wa, (tile_id(it, jt) * 64 + (l16 >> 2) * 16 + 4 * lg + r) * 4 + (l16 & 3), v * cj);
-                    x[r] = v * s.tab[(zx ? 3 : 4) * 64 + i];
+                    put1<T, P>(s.u.w[0], (t * 64 + (l16 >> 2) * 16 + 4 * lg + r) * 4 + (l16 & 3), x[r] * cj);
                 }
-                // row j, k = i
-                put<T, P>(wt, (tile_id(it, jt) * 64 + lane) * 4, x);
+                put<T, P>(s.u.w[1], (t * 64 + lane) * 4, x * row4(s.tab, zx ? 3 : 4, i0));   // row j, k = i
             }
-        }
-        __syncthreads();
-        float qd[16], ka[16], kf[16], km[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) qd[i] = ka[i] = kf[i] = km[i] = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int kc = 16 * (NT * w + n) + l16;   // this lane's key column
-            Frag<T, 1> kf2[2], qf2[2];
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                kf2[ks] = load_frag<T, 1>(s.kt, kc, LT, ks, lg, 0);
-                qf2[ks] = load_frag<T, 1>(s.qt, kc, LT, ks, lg, 0);
-            }
+            __syncthreads();
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
-                const f32x4 gam = *reinterpret_cast<const f32x4 *>(s.gam + 16 * it + 4 * lg);
-                const f32x4 eh = *reinterpret_cast<const f32x4 *>(s.eh + 16 * it + 4 * lg);
-                const f32x4 be = row4(s.tab, 2, 16 * it + 4 * lg);
-                const f32x4 rk = row4(s.tab, 3, 16 * it + 4 * lg), rq = row4(s.tab, 4, 16 * it + 4 * lg);
-                f32x4 q1 = gam * M1[it][n], A = -gam * M2[it][n], m3 = eh * M3[it][n], F = m3;
+                f32x4 &m = zx ? M2[it] : M1[it];
 #pragma unroll
-                for (int ks = 0; ks <= it / 2; ++ks) {
-                    q1 = mma(q1, load_tri<T, P, false>(s.u.w[0], it, ks, lane), kf2[ks]);
-                    A = mma(A, load_tri<T, P, false>(s.u.w[1], it, ks, lane), kf2[ks]);
-                }
+                for (int ks = 0; ks <= it / 2; ++ks) m = mma(m, load_tri<T, P, false>(s.u.w[0], it, ks, lane), kf[ks]);
 #pragma unroll
-                for (int ks = it / 2; ks < 2; ++ks) {
-                    F = mma(F, load_tri<T, P, true>(s.u.w[2], it, ks, lane), qf2[ks]);
-                    F = mma(F, load_tri<T, P, true>(s.u.w[3], it, ks, lane), kf2[ks]);
-                }
-                // this lane's q, k of the tile: rows 16 it + 4 lg + r
-                f32x4 kv, qv;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    kv[r] = to_f32(kf2[it >> 1].p[0][(it & 1) * 4 + r]);
-                    qv[r] = to_f32(qf2[it >> 1].p[0][(it & 1) * 4 + r]);
-                }
-                kv *= rk;
-                qv *= rq;
-                dq[it][n] += q1;
-                dk[it][n] += A + be * F;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    qd[4 * it + r] += qv[r] * q1[r];
-                    ka[4 * it + r] += kv[r] * A[r];
-                    kf[4 * it + r] += kv[r] * F[r];
-                    km[4 * it + r] += kv[r] * m3[r];
-                }
+                for (int ks = it / 2; ks < 2; ++ks)
+                    M3[it] = mma(M3[it], load_tri<T, P, true>(s.u.w[1], it, ks, lane), zx ? kf[ks] : qf[ks]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = 16 * (i >> 2) + 4 * lg + (i & 3);
-            const float x0 = group_allreduce<16>(qd[i]), x1 = group_allreduce<16>(ka[i]);
-            const float x2 = group_allreduce<16>(kf[i]), x3 = group_allreduce<16>(km[i]);
-            if (l16 == 0) {
-                s.red[w][0][row] = x0;
-                s.red[w][1][row] = x1;
-                s.red[w][2][row] = x2;
-                s.red[w][3][row] = x3;
+        for (int it = 0; it < 4; ++it) {
+            const f32x4 kv = value(kf, it, 3);
+            row_dots(s.red[0][w], it, lg, l16, value(qf, it, 4), M1[it]);
+            row_dots(s.red[1][w], it, lg, l16, kv, M2[it]);
+            row_dots(s.red[2][w], it, lg, l16, kv, M3[it]);
+            M2[it] += row4(s.tab, 2, 16 * it + 4 * lg) * M3[it];
+            if constexpr (kShared) {
+                dq[it] += M1[it];
+                dk[it] += M2[it];
+            } else {
+                dq[it] = M1[it];
+                dk[it] = M2[it];
             }
         }
         __syncthreads();
         if (w == 0) {
             float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = (s.red[0][i][lane] + s.red[1][i][lane]) + (s.red[2][i][lane] + s.red[3][i][lane]);
+            for (int i = 0; i < 4; ++i) {
+                x[i] = 0.f;
+#pragma unroll
+                for (int n = 0; n < W; ++n) x[i] += s.red[i][n][lane];
+            }
             const float be = s.tab[2 * 64 + lane];
             double dG = (double)x[0] + x[1] - (double)be * x[2];
-            const double end = wave_sum((double)be * x[3]);
-            if (lane == 63)
-                dG += end + (double)__builtin_amdgcn_exp2f(s.tab[63]) * ((double)s.ip[0] + s.ip[1] + ((double)s.ip[2] + s.ip[3]));
+            double end = wave_sum((double)be * x[3]), sd = 0.;
+#pragma unroll
+            for (int n = 0; n < W; ++n) sd += s.ip[n];
+            end += (double)__builtin_amdgcn_exp2f(s.tab[63]) * sd;
+            if (lane == 63) dG += end;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double dn = __shfl_down(dG, d);
@@ -315,28 +294,29 @@ __global__ void __launch_bounds__(256) gdr_grads_kernel(GradArgs<T> a)
             s.tk[lane] += x[1] + be * x[2];
         }
     }
-    __syncthreads();
+    if (a.norm) __syncthreads();
     // with q = n scale and n = x rq / scale: dx = rq (dq - q (q . dq) / scale^2)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int kc = 16 * (NT * w + n) + l16;
-#pragma unroll
-        for (int it = 0; it < 4; ++it)
+    for (int it = 0; it < 4; ++it) {
+        const int t0 = 16 * it + 4 * lg;
+        const f32x4 rq = row4(s.tab, 4, t0), rk = row4(s.tab, 3, t0);
+        f32x4 x = dq[it] * rq, z = dk[it] * rk;
+        if (a.norm) {
+            const f32x4 nq = rq / a.scale, tq = row4(s.tq, 0, t0), tk = row4(s.tk, 0, t0);   // nq = 1 / |q|
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int t = 16 * it + 4 * lg + r;
-                if (t >= c.len) continue;
-                const float rq = s.tab[4 * 64 + t], rk = s.tab[3 * 64 + t];
-                float x = dq[it][n][r] * rq, z = dk[it][n][r] * rk;
-                if (a.norm) {
-                    const float nq = rq / a.scale;   // 1 / |q|
-                    x -= nq * nq * to_f32(s.qt[kc * LT + kpos(t)]) * s.tq[t];
-                    z -= rk * rk * to_f32(s.kt[kc * LT + kpos(t)]) * s.tk[t];
-                }
-                const int64_t o = ((c.tok + t) * a.Hk + hk) * K + kc;
-                a.dq[o] = (T)x;
-                a.dk[o] = (T)z;
+                const int b = (16 * w + l16) * (int)sizeof(T);
+                x[r] -= nq[r] * nq[r] * to_f32(*reinterpret_cast<const T *>(s.q + Sw::at(t0 + r, b))) * tq[r];
+                z[r] -= rk[r] * rk[r] * to_f32(*reinterpret_cast<const T *>(s.k + Sw::at(t0 + r, b))) * tk[r];
             }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (t0 + r >= c.len) continue;
+            const int64_t o = ((c.tok + t0 + r) * a.Hk + hk) * K + 16 * w + l16;
+            a.dq[o] = (T)x[r];
+            a.dk[o] = (T)z[r];
+        }
     }
 }
 
@@ -363,7 +343,11 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.group = (int)(a.Hv / a.Hk);
     p.norm = a.norm;
     p.scale = a.scale;
-    hipLaunchKernelGGL((gdr_grads_kernel<T, K>), dim3((unsigned)a.map.slots, (unsigned)a.Hk), dim3(256), 0, stream, p);
+    const dim3 grid((unsigned)a.map.slots, (unsigned)a.Hk);
+    if (p.group > 1)
+        hipLaunchKernelGGL((gdr_grads_kernel<T, K, true>), grid, dim3(4 * K), 0, stream, p);
+    else
+        hipLaunchKernelGGL((gdr_grads_kernel<T, K, false>), grid, dim3(4 * K), 0, stream, p);
     return hipGetLastError();
 }
 
