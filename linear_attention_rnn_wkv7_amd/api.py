@@ -5,6 +5,7 @@ stream; every step of the recurrence runs in the library's HIP kernels.
 Names mirror the C entry points (include/wkv7.h).
 """
 import ctypes
+import functools
 
 import torch
 
@@ -302,55 +303,71 @@ def rwkv8_backward(q, v, decay, dy, rho0=None, norm0=None, drhoT=None, dnormT=No
 
 # ------------------------------------------------------ the gated delta rule
 
-class _At:
-    """The device of a call's tensors as the current one, and the stream its
-    kernels run on (``stream``, or that device's current stream)."""
+# The calls below are also made for single tokens, where their own host time is
+# what a step waits for: plain integers for pointers, one look-up per shape and
+# no context managers unless the caller's device or stream is not the current one.
 
-    def __init__(self, name, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on {device}")
-        self.device, self.stream = torch.cuda.device(device), stream
-
-    def __enter__(self):
-        self.device.__enter__()
-        self.on = _on(self.stream)
-        self.on.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        self.on.__exit__(*exc)
-        self.device.__exit__(*exc)
-        return False
+def _raw_stream(index):
+    """The handle of a device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _check_like(name, t, shape, dtype, device, optional=False):
+def _launch(name, index, stream, call):
+    """call(stream handle) with the device of the tensors as the current one and
+    ``stream``, if given, as its stream (also for what it allocates)."""
+    if stream is None and index == torch.cuda.current_device():
+        return call(_raw_stream(index))
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.device(index), _on(stream):
+        return call(_raw_stream(index))
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_like(name, t, shape, dtype, index, optional=False):
     if t is None and optional:
         return
-    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+    if t is None or t.shape != shape or t.dtype != dtype or not t.is_cuda or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
 
 
-def _workspace(name, workspace, need, device):
-    """The workspace to pass on: the caller's, or one of `need` bytes."""
+def _workspace(name, workspace, need, index):
+    """The workspace to pass on (the caller's, or one of `need` bytes), its
+    address and its size."""
     if workspace is None:
-        workspace = torch.empty(need, device=device, dtype=torch.uint8) if need > 0 else None
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{name}: workspace must be a contiguous tensor on {device}")
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, device=index, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_cuda or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"{name}: workspace must be a contiguous tensor on cuda:{index}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _output(name, t, shape, dtype, device):
+def _output(name, t, shape, dtype, index):
     """A caller's output, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, device=device, dtype=dtype)
-    _check_like(name, t, shape, dtype, device)
+        return torch.empty(shape, device=index, dtype=dtype)
+    _check_like(name, t, shape, dtype, index)
     return t
 
 
 def gdr_shape(B, T, Hk, Hv, K, V, dtype=torch.float32, nseq=0, norm_qk=False, scale=None):
     return _lib.GdrShape(B, T, Hk, Hv, K, V, nseq, _VEC_DTYPES[dtype],
                          _lib.GDR_NORM_QK if norm_qk else 0, K ** -0.5 if scale is None else scale)
+
+
+@functools.lru_cache(maxsize=256)
+def _gdr_sizes(*key):
+    """A shape for the library, and the bytes of its record and workspaces."""
+    L, sh = _lib.lib(), gdr_shape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, L.gdr_checkpoint_bytes(r), L.gdr_forward_workspace_bytes(r), \
+        (L.gdr_backward_workspace_bytes(r, 0), L.gdr_backward_workspace_bytes(r, 1))
 
 
 def gdr_checkpoint_bytes(B, T, Hk, Hv, K, V, dtype=torch.float32, nseq=0):
@@ -370,25 +387,29 @@ def gdr_backward_workspace_bytes(B, T, Hk, Hv, K, V, dtype=torch.float32, nseq=0
 def _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk):
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q must be [B, T, Hk, K] and v [B, T, Hv, V]")
-    if q.dtype not in _VEC_DTYPES:
-        raise ValueError(f"q: dtype {q.dtype} not supported")
+    dt = q.dtype
+    if dt not in _VEC_DTYPES:
+        raise ValueError(f"q: dtype {dt} not supported")
     if not q.is_cuda:
         raise ValueError("q must be a device tensor")
-    (B, T, Hk, K), (Hv, V) = q.shape, v.shape[2:]
+    qs, ys, at = q.shape, v.shape, q.get_device()
+    B, T, Hk, K = qs
+    Hv, V = ys[2], ys[3]
     if Hk == 0 or Hv % Hk != 0:
         raise ValueError(f"v has {Hv} heads: not a multiple of q's {Hk}")
-    for n, t, shp, dt in (("q", q, (B, T, Hk, K), q.dtype), ("k", k, (B, T, Hk, K), q.dtype),
-                          ("v", v, (B, T, Hv, V), q.dtype), ("g", g, (B, T, Hv), torch.float32),
-                          ("beta", beta, (B, T, Hv), torch.float32)):
-        _check_like(n, t, shp, dt, q.device)
+    gs = (B, T, Hv)
+    _check_like("q", q, qs, dt, at)
+    _check_like("k", k, qs, dt, at)
+    _check_like("v", v, (B, T, Hv, V), dt, at)
+    _check_like("g", g, gs, torch.float32, at)
+    _check_like("beta", beta, gs, torch.float32, at)
     nseq = 0
     if seq_starts is not None:
         nseq = seq_starts.numel() - 1
         if B != 1 or nseq < 1:
             raise ValueError("seq_starts needs B = 1 and at least two entries")
-        _check_like("seq_starts", seq_starts, (nseq + 1,), torch.int32, q.device)
-    sh = gdr_shape(B, T, Hk, Hv, K, V, q.dtype, nseq, norm_qk, scale)
-    return sh, (B, T, Hv, V), (nseq or B, Hv, V, K)
+        _check_like("seq_starts", seq_starts, (nseq + 1,), torch.int32, at)
+    return (B, T, Hk, Hv, K, V, dt, nseq, bool(norm_qk), scale), ys, (nseq or B, Hv, V, K), at
 
 
 def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_qk=False, want_y=True,
@@ -407,21 +428,22 @@ def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_
 
     ckpt is the record gdr_backward consumes.  ``out`` may supply (y, sT,
     ckpt) tensors (None entries are allocated when wanted)."""
-    sh, ys, ss = _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk)
-    dev, L, f32 = q.device, _lib.lib(), torch.float32
-    _check_like("s0", s0, ss, f32, dev, optional=True)
+    key, ys, ss, at = _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk)
+    _, sh, ck_bytes, need, _ = _gdr_sizes(*key)
+    f32 = torch.float32
+    _check_like("s0", s0, ss, f32, at, optional=True)
     y, sT, ckpt = out if out is not None else (None, None, None)
-    with _At("gdr_forward", dev, stream) as st:
-        y = _output("y", y, ys, q.dtype, dev) if want_y else None
-        sT = _output("sT", sT, ss, f32, dev) if want_sT else None
-        ckpt = _output("ckpt", ckpt, (L.gdr_checkpoint_bytes(ctypes.byref(sh)) // 4,), f32,
-                       dev) if want_ckpt else None
-        workspace, ws_bytes = _workspace("gdr_forward", workspace,
-                                         L.gdr_forward_workspace_bytes(ctypes.byref(sh)), dev)
-        rc = L.gdr_forward(ctypes.byref(sh), *map(_ptr, (q, k, v, g, beta, s0, seq_starts, y, sT, ckpt)),
-                           _ptr(workspace), ws_bytes, st)
-    _lib.check("gdr_forward", rc)
-    return y, sT, ckpt
+
+    def call(st):
+        y_ = _output("y", y, ys, q.dtype, at) if want_y else None
+        sT_ = _output("sT", sT, ss, f32, at) if want_sT else None
+        ckpt_ = _output("ckpt", ckpt, (ck_bytes // 4,), f32, at) if want_ckpt else None
+        ws, wp, wb = _workspace("gdr_forward", workspace, need, at)
+        rc = _lib.lib().gdr_forward(sh, *map(_at, (q, k, v, g, beta, s0, seq_starts, y_, sT_, ckpt_)), wp, wb, st)
+        _lib.check("gdr_forward", rc)
+        return y_, sT_, ckpt_
+
+    return _launch("gdr_forward", at, stream, call)
 
 
 def gdr_backward(q, k, v, g, beta, dy, s0=None, dsT=None, ckpt=None, *, seq_starts=None, scale=None,
@@ -429,26 +451,27 @@ def gdr_backward(q, k, v, g, beta, dy, s0=None, dsT=None, ckpt=None, *, seq_star
     """The gradients of gdr_forward (gdr_backward), with the same inputs and
     options.  Returns dict(dq, dk, dv, dg, dbeta, ds0): dq, dk, dv in the
     inputs' type, the others fp32; ds0 None when not wanted."""
-    sh, ys, ss = _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk)
-    dev, L, f32 = q.device, _lib.lib(), torch.float32
-    _check_like("dy", dy, ys, q.dtype, dev)
-    for n, t in (("s0", s0), ("dsT", dsT)):
-        _check_like(n, t, ss, f32, dev, optional=True)
-    _check_like("ckpt", ckpt, (L.gdr_checkpoint_bytes(ctypes.byref(sh)) // 4,), f32, dev, optional=True)
+    key, ys, ss, at = _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk)
+    _, sh, ck_bytes, _, need = _gdr_sizes(*key)
+    f32 = torch.float32
+    _check_like("dy", dy, ys, q.dtype, at)
+    _check_like("s0", s0, ss, f32, at, optional=True)
+    _check_like("dsT", dsT, ss, f32, at, optional=True)
+    _check_like("ckpt", ckpt, (ck_bytes // 4,), f32, at, optional=True)
     grads = dict(out) if out is not None else {}
-    with _At("gdr_backward", dev, stream) as st:
+
+    def call(st):
         for n, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
-            grads[n] = _output(n, grads.get(n), like.shape, like.dtype, dev)
-        grads["ds0"] = _output("ds0", grads.get("ds0"), ss, f32, dev) if want_ds0 else None
-        workspace, ws_bytes = _workspace(
-            "gdr_backward", workspace,
-            L.gdr_backward_workspace_bytes(ctypes.byref(sh), int(ckpt is not None)), dev)
-        rc = L.gdr_backward(
-            ctypes.byref(sh), *map(_ptr, (q, k, v, g, beta, s0, seq_starts, dy, dsT, ckpt)),
-            *map(_ptr, (grads[n] for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0"))),
-            _ptr(workspace), ws_bytes, st)
-    _lib.check("gdr_backward", rc)
-    return grads
+            grads[n] = _output(n, grads.get(n), like.shape, like.dtype, at)
+        grads["ds0"] = _output("ds0", grads.get("ds0"), ss, f32, at) if want_ds0 else None
+        ws, wp, wb = _workspace("gdr_backward", workspace, need[ckpt is not None], at)
+        rc = _lib.lib().gdr_backward(
+            sh, *map(_at, (q, k, v, g, beta, s0, seq_starts, dy, dsT, ckpt)),
+            *(_at(grads[n]) for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0")), wp, wb, st)
+        _lib.check("gdr_backward", rc)
+        return grads
+
+    return _launch("gdr_backward", at, stream, call)
 
 
 def gdr_decode(q, k, v, g, beta, state, slots=None, *, scale=None, norm_qk=False, stream=None, out=None):
@@ -457,70 +480,94 @@ def gdr_decode(q, k, v, g, beta, state, slots=None, *, scale=None, norm_qk=False
     returns y [B, T, Hv, V].  slots (int32 [B], on the device) names each
     row's state, None is row b = state b.  A row with a slot outside the pool,
     or with an earlier row's slot, is skipped: its y is left as it was."""
-    sh, ys, ss = _gdr_dims(q, k, v, g, beta, None, scale, norm_qk)
-    dev = q.device
+    key, ys, ss, at = _gdr_dims(q, k, v, g, beta, None, scale, norm_qk)
     if state.dim() != 4:
         raise ValueError("state must be [pool, Hv, V, K]")
-    _check_like("state", state, (state.shape[0],) + ss[1:], torch.float32, dev)
+    pool = state.shape[0]
+    _check_like("state", state, (pool,) + ss[1:], torch.float32, at)
     if slots is not None:
-        _check_like("slots", slots, (ys[0],), torch.int32, dev)
-    elif state.shape[0] < ys[0]:
-        raise ValueError(f"state holds {state.shape[0]} states for {ys[0]} rows")
-    with _At("gdr_decode", dev, stream) as st:
-        y = _output("y", out, ys, q.dtype, dev)
-        rc = _lib.lib().gdr_decode(ctypes.byref(sh), *map(_ptr, (q, k, v, g, beta, state)),
-                                   state.shape[0], *map(_ptr, (slots, y)), st)
-    _lib.check("gdr_decode", rc)
-    return y
+        _check_like("slots", slots, (ys[0],), torch.int32, at)
+    elif pool < ys[0]:
+        raise ValueError(f"state holds {pool} states for {ys[0]} rows")
+    sh = _gdr_sizes(*key)[1]
+
+    def call(st):
+        y = _output("y", out, ys, q.dtype, at)
+        rc = _lib.lib().gdr_decode(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                   state.data_ptr(), pool, _at(slots), y.data_ptr(), st)
+        _lib.check("gdr_decode", rc)
+        return y
+
+    return _launch("gdr_decode", at, stream, call)
+
+
+@functools.lru_cache(maxsize=256)
+def _epilogue_sizes(*key):
+    sh = _lib.GdrEpilogueShape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, _lib.lib().gdr_epilogue_workspace_bytes(r)
 
 
 def _gdr_epilogue_dims(y, gate, w, eps):
     if y.dim() != 4 or w.dim() != 2:
         raise ValueError("y must be [B, T, H, N] and w [1 or H, N]")
-    if y.dtype not in _VEC_DTYPES:
-        raise ValueError(f"y: dtype {y.dtype} not supported")
+    dt = y.dtype
+    if dt not in _VEC_DTYPES:
+        raise ValueError(f"y: dtype {dt} not supported")
     if not y.is_cuda:
         raise ValueError("y must be a device tensor")
-    B, T, H, N = y.shape
-    if w.shape[0] not in (1, H):
-        raise ValueError(f"w has {w.shape[0]} heads: 1 or {H}")
-    _check_like("y", y, y.shape, y.dtype, y.device)
-    _check_like("gate", gate, y.shape, y.dtype, y.device)
-    _check_like("w", w, (w.shape[0], N), torch.float32, y.device)
-    return _lib.GdrEpilogueShape(B * T, H, N, w.shape[0], _VEC_DTYPES[y.dtype], 0, eps)
+    ys, at = y.shape, y.get_device()
+    B, T, H, N = ys
+    Hw = w.shape[0]
+    if Hw not in (1, H):
+        raise ValueError(f"w has {Hw} heads: 1 or {H}")
+    _check_like("y", y, ys, dt, at)
+    _check_like("gate", gate, ys, dt, at)
+    _check_like("w", w, (Hw, N), torch.float32, at)
+    return _epilogue_sizes(B * T, H, N, Hw, _VEC_DTYPES[dt], 0, eps), ys, at
 
 
 def gdr_epilogue_forward(y, gate, w, *, eps=1e-6, stream=None, out=None):
     """The gated norm after the scan (gdr_epilogue_forward), per head:
     z = y / sqrt(mean(y^2) + eps) * w * gate * sigmoid(gate).
     y, gate [B, T, H, N] fp32 or bf16, w [1 or H, N] fp32."""
-    sh = _gdr_epilogue_dims(y, gate, w, eps)
-    with _At("gdr_epilogue_forward", y.device, stream) as st:
-        z = _output("z", out, y.shape, y.dtype, y.device)
-        rc = _lib.lib().gdr_epilogue_forward(ctypes.byref(sh), *map(_ptr, (y, gate, w, z)), st)
-    _lib.check("gdr_epilogue_forward", rc)
-    return z
+    (_, sh, _), ys, at = _gdr_epilogue_dims(y, gate, w, eps)
+
+    def call(st):
+        z = _output("z", out, ys, y.dtype, at)
+        rc = _lib.lib().gdr_epilogue_forward(sh, y.data_ptr(), gate.data_ptr(), w.data_ptr(), z.data_ptr(), st)
+        _lib.check("gdr_epilogue_forward", rc)
+        return z
+
+    return _launch("gdr_epilogue_forward", at, stream, call)
 
 
 def gdr_epilogue_backward(dz, y, gate, w, *, eps=1e-6, workspace=None, stream=None, out=None):
     """The epilogue's gradients: dict(dy, dgate, dw), dw fp32 like w."""
-    sh = _gdr_epilogue_dims(y, gate, w, eps)
-    dev, L = y.device, _lib.lib()
-    _check_like("dz", dz, y.shape, y.dtype, dev)
+    (_, sh, need), ys, at = _gdr_epilogue_dims(y, gate, w, eps)
+    _check_like("dz", dz, ys, y.dtype, at)
     grads = dict(out) if out is not None else {}
-    with _At("gdr_epilogue_backward", dev, stream) as st:
+
+    def call(st):
         for n, like in (("dy", y), ("dgate", gate), ("dw", w)):
-            grads[n] = _output(n, grads.get(n), like.shape, like.dtype, dev)
-        workspace, ws_bytes = _workspace("gdr_epilogue_backward", workspace,
-                                         L.gdr_epilogue_workspace_bytes(ctypes.byref(sh)), dev)
-        rc = L.gdr_epilogue_backward(ctypes.byref(sh), *map(_ptr, (dz, y, gate, w)),
-                                     *map(_ptr, (grads[n] for n in ("dy", "dgate", "dw"))),
-                                     _ptr(workspace), ws_bytes, st)
-    _lib.check("gdr_epilogue_backward", rc)
-    return grads
+            grads[n] = _output(n, grads.get(n), like.shape, like.dtype, at)
+        ws, wp, wb = _workspace("gdr_epilogue_backward", workspace, need, at)
+        rc = _lib.lib().gdr_epilogue_backward(sh, *map(_at, (dz, y, gate, w)),
+                                              *(_at(grads[n]) for n in ("dy", "dgate", "dw")), wp, wb, st)
+        _lib.check("gdr_epilogue_backward", rc)
+        return grads
+
+    return _launch("gdr_epilogue_backward", at, stream, call)
 
 
 # --------------------------------------------------------- the residual norm
+
+@functools.lru_cache(maxsize=256)
+def _norm_sizes(*key):
+    sh = _lib.ResidualNormShape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, _lib.lib().residual_norm_workspace_bytes(r)
+
 
 def _norm_dims(x, eps):
     if x.dim() < 1 or x.dtype not in _VEC_DTYPES or not x.is_cuda or not x.is_contiguous():
@@ -528,7 +575,7 @@ def _norm_dims(x, eps):
     D = x.shape[-1]
     if D == 0:
         raise ValueError("the residual stream has rows of no entries")
-    return _lib.ResidualNormShape(x.numel() // D, D, _VEC_DTYPES[x.dtype], 0, eps), D
+    return _norm_sizes(x.numel() // D, D, _VEC_DTYPES[x.dtype], 0, eps), D, x.get_device()
 
 
 def residual_norm_forward(x, y, w, scale=None, *, eps=1e-6, want_x_out=True, stream=None, out=None):
@@ -537,20 +584,24 @@ def residual_norm_forward(x, y, w, scale=None, *, eps=1e-6, want_x_out=True, str
     sqrt(mean(x_out^2) + eps) * w over the last axis.  Returns (x_out, h).
     x, y [..., D] fp32 or bf16 (y None: x_out = x); w, scale [D] fp32.
     ``out`` may supply (x_out, h); x_out may be x itself."""
-    sh, D = _norm_dims(x, eps)
-    dev, f32 = x.device, torch.float32
-    _check_like("y", y, x.shape, x.dtype, dev, optional=True)
-    _check_like("w", w, (D,), f32, dev)
-    _check_like("scale", scale, (D,), f32, dev, optional=True)
+    (_, sh, _), D, at = _norm_dims(x, eps)
+    f32, xs, dt = torch.float32, x.shape, x.dtype
+    _check_like("y", y, xs, dt, at, optional=True)
+    _check_like("w", w, (D,), f32, at)
+    _check_like("scale", scale, (D,), f32, at, optional=True)
     if scale is not None and y is None:
         raise ValueError("scale needs y")
     xo, h = out if out is not None else (None, None)
-    with _At("residual_norm_forward", dev, stream) as st:
-        xo = _output("x_out", xo, x.shape, x.dtype, dev) if want_x_out else None
-        h = _output("h", h, x.shape, x.dtype, dev)
-        rc = _lib.lib().residual_norm_forward(ctypes.byref(sh), *map(_ptr, (x, y, scale, w, xo, h)), st)
-    _lib.check("residual_norm_forward", rc)
-    return xo, h
+
+    def call(st):
+        xo_ = _output("x_out", xo, xs, dt, at) if want_x_out else None
+        h_ = _output("h", h, xs, dt, at)
+        rc = _lib.lib().residual_norm_forward(sh, x.data_ptr(), _at(y), _at(scale), w.data_ptr(), _at(xo_),
+                                              h_.data_ptr(), st)
+        _lib.check("residual_norm_forward", rc)
+        return xo_, h_
+
+    return _launch("residual_norm_forward", at, stream, call)
 
 
 def residual_norm_backward(dh, dx_out, x_out, w, y=None, scale=None, *, eps=1e-6, workspace=None,
@@ -559,27 +610,28 @@ def residual_norm_backward(dh, dx_out, x_out, w, y=None, scale=None, *, eps=1e-6
     (dx_out None: zeros), with x_out as it was stored: dict(dx, dy, dw,
     dscale).  Without a scale, dx is the gradient of y too, and dy and dscale
     are None; with one, y is needed as well.  dx may be dx_out itself."""
-    sh, D = _norm_dims(x_out, eps)
-    dev, dt, f32, L = x_out.device, x_out.dtype, torch.float32, _lib.lib()
-    _check_like("dh", dh, x_out.shape, dt, dev)
-    _check_like("dx_out", dx_out, x_out.shape, dt, dev, optional=True)
-    _check_like("w", w, (D,), f32, dev)
+    (_, sh, need), D, at = _norm_dims(x_out, eps)
+    dt, f32, xs = x_out.dtype, torch.float32, x_out.shape
+    _check_like("dh", dh, xs, dt, at)
+    _check_like("dx_out", dx_out, xs, dt, at, optional=True)
+    _check_like("w", w, (D,), f32, at)
     if (scale is None) != (y is None):
         raise ValueError("y and scale come together")
-    _check_like("scale", scale, (D,), f32, dev, optional=True)
-    _check_like("y", y, x_out.shape, dt, dev, optional=True)
+    scaled = scale is not None
+    _check_like("scale", scale, (D,), f32, at, optional=True)
+    _check_like("y", y, xs, dt, at, optional=True)
     grads = dict(out) if out is not None else {}
-    with _At("residual_norm_backward", dev, stream) as st:
-        grads["dx"] = _output("dx", grads.get("dx"), x_out.shape, dt, dev)
-        grads["dw"] = _output("dw", grads.get("dw"), (D,), f32, dev)
-        scaled = scale is not None
-        grads["dy"] = _output("dy", grads.get("dy"), x_out.shape, dt, dev) if scaled else None
-        grads["dscale"] = _output("dscale", grads.get("dscale"), (D,), f32, dev) if scaled else None
-        workspace, ws_bytes = _workspace("residual_norm_backward", workspace,
-                                         L.residual_norm_workspace_bytes(ctypes.byref(sh)), dev)
-        rc = L.residual_norm_backward(
-            ctypes.byref(sh), *map(_ptr, (dh, dx_out, x_out, y, scale, w)),
-            *map(_ptr, (grads[n] for n in ("dx", "dy", "dw", "dscale"))),
-            _ptr(workspace), ws_bytes, st)
-    _lib.check("residual_norm_backward", rc)
-    return grads
+
+    def call(st):
+        grads["dx"] = _output("dx", grads.get("dx"), xs, dt, at)
+        grads["dw"] = _output("dw", grads.get("dw"), (D,), f32, at)
+        grads["dy"] = _output("dy", grads.get("dy"), xs, dt, at) if scaled else None
+        grads["dscale"] = _output("dscale", grads.get("dscale"), (D,), f32, at) if scaled else None
+        ws, wp, wb = _workspace("residual_norm_backward", workspace, need, at)
+        rc = _lib.lib().residual_norm_backward(
+            sh, *map(_at, (dh, dx_out, x_out, y, scale, w)),
+            *(_at(grads[n]) for n in ("dx", "dy", "dw", "dscale")), wp, wb, st)
+        _lib.check("residual_norm_backward", rc)
+        return grads
+
+    return _launch("residual_norm_backward", at, stream, call)
