@@ -23,11 +23,33 @@ struct Dims {
     float scale;
     size_t states, rows, table;       // bytes: chunk states, chunk rows, tables
     size_t factors, factors_t;        // of the forward's and the backward's factors, or 0
+    int64_t nseg, nckseg;             // segments of a row
+    size_t seg_map, carry;            // of the segments, or 0
     bool empty() const { return Hv == 0 || (packed ? seqs == 0 : B == 0); }
     bool tokens() const { return !empty() && B * T > 0; }
 };
 
 bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
+
+size_t round_up(size_t x);
+
+// Few, long rows run in segments: as many as fill 256 compute units with a
+// workgroup each, 16 at most, of at least 4 chunks, where one slab to a
+// workgroup would leave units idle (or just fill them).  A chunk then takes two
+// steps, one of them with K more columns: fewer than 4 segments do not pay.
+void plan_segments(Dims *d)
+{
+    d->nseg = 1;
+    d->nckseg = d->nck;
+    const int64_t units = d->B * d->Hv;
+    if (d->packed || units == 0 || units * (d->V / 16) > 256) return;
+    int64_t n = 256 / units;
+    if (n > 16) n = 16;
+    if (n > d->nck / 4) n = d->nck / 4;
+    if (n < 4) return;
+    d->nckseg = (d->nck + n - 1) / n;
+    d->nseg = (d->nck + d->nckseg - 1) / d->nckseg;
+}
 
 size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -70,6 +92,10 @@ int check(const gdr_shape *s, Dims *d)
     if (d->slots > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
     if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 2 * 4096), &x))
         return WKV7_ERR_INVALID;   // any sum of the workspace's parts
+    plan_segments(d);
+    const size_t segs = d->nseg > 1 ? (size_t)(s->B * s->Hv * d->nseg) : 0;
+    d->seg_map = segs * (size_t)(s->K * (s->V + s->K) * 4);
+    d->carry = segs * (size_t)(s->V * s->K * 4);
     d->states = (size_t)(per * s->K * s->V * 4);
     d->rows = (size_t)(per * 64 * s->V * 4);
     const bool makes = wkv7::gdr::scan_makes_factors(d->dtype, s->K, s->V, d->seqs * s->Hv);
@@ -79,20 +105,21 @@ int check(const gdr_shape *s, Dims *d)
     return WKV7_OK;
 }
 
-size_t forward_bytes(const Dims &d) { return round_up(d.factors); }
+size_t segment_bytes(const Dims &d) { return round_up(d.seg_map) + round_up(d.carry); }
+size_t forward_bytes(const Dims &d) { return round_up(d.factors) + segment_bytes(d); }
 size_t record_bytes(const Dims &d) { return round_up(d.states) + round_up(d.rows); }
-// the tables, the factors, D and dR (sized as the record), and the record if it
+// the tables, the factors, the segments, D and dR (sized as the record), and the record if it
 // is not given
 size_t backward_bytes(const Dims &d, bool ckpt_provided)
 {
-    return round_up(d.table) + round_up(d.factors_t) + record_bytes(d) * (ckpt_provided ? 1 : 2);
+    return round_up(d.table) + round_up(d.factors_t) + segment_bytes(d) + record_bytes(d) * (ckpt_provided ? 1 : 2);
 }
 
 wkv7::gdr::Launch base(const Dims &d, const void *q, const void *k, const void *v, const float *g,
                        const float *beta, const float *s0, const int32_t *starts)
 {
     wkv7::gdr::Launch L;
-    L.map = {d.packed ? starts : nullptr, d.T, d.seqs, d.nck, d.slots};
+    L.map = {d.packed ? starts : nullptr, d.T, d.seqs, d.nck, d.slots, d.nseg, d.nckseg};
     L.B = d.B;
     L.Hk = d.Hk;
     L.Hv = d.Hv;
@@ -108,6 +135,13 @@ wkv7::gdr::Launch base(const Dims &d, const void *q, const void *k, const void *
     L.beta = beta;
     L.s0 = s0;
     return L;
+}
+
+void set_segments(wkv7::gdr::Launch *L, const Dims &d, char *at)
+{
+    if (d.nseg == 1) return;
+    L->seg_map = reinterpret_cast<float *>(at);
+    L->carry = reinterpret_cast<float *>(at + round_up(d.seg_map));
 }
 
 void set_record(wkv7::gdr::Launch *L, const Dims &d, const float *rec)
@@ -227,6 +261,7 @@ int gdr_forward(const gdr_shape *shape, const void *q, const void *k, const void
     if (rc != WKV7_OK) return rc;
     wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts);
     L.factors = d.factors ? workspace : nullptr;
+    set_segments(&L, d, static_cast<char *>(workspace) + round_up(d.factors));
     L.y = y;
     L.sT = sT;
     set_record(&L, d, ckpt);
@@ -252,10 +287,12 @@ int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const voi
     }
     rc = check_workspace(workspace, workspace_bytes, backward_bytes(d, ckpt != nullptr));
     if (rc != WKV7_OK) return rc;
-    char *ws = static_cast<char *>(workspace), *grads = ws + round_up(d.table) + round_up(d.factors_t);
+    char *ws = static_cast<char *>(workspace), *segs = ws + round_up(d.table) + round_up(d.factors_t),
+         *grads = segs + segment_bytes(d);
     wkv7::gdr::Launch L = base(d, q, k, v, g, beta, s0, seq_starts);
     L.table = static_cast<float *>(workspace);
     L.factors = d.factors_t ? ws + round_up(d.table) : nullptr;   // at least the forward's
+    set_segments(&L, d, segs);
     L.ws_ds = reinterpret_cast<float *>(grads);
     L.ws_dr = reinterpret_cast<float *>(grads + round_up(d.states));
     if (ckpt) {

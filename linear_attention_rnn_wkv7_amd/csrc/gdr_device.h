@@ -272,18 +272,18 @@ __device__ __forceinline__ float to_f32(bf16 x) { return (float)x; }
 __device__ __forceinline__ f32x4 quad_f32(f32x4 x) { return x; }
 __device__ __forceinline__ f32x4 quad_f32(bf16x4 x) { return __builtin_convertvector(x, f32x4); }
 
-// A chunk slot's sequence, its first token (in the [B * T] token list), its
-// length, and whether it is the sequence's last chunk.
+// A chunk slot's first token (in the [B * T] token list) and its length.
 struct Chunk {
-    int64_t seq, tok;
+    int64_t tok;
     int len;
 };
 
 __device__ __forceinline__ void seq_range(const Map &m, int64_t s, int64_t &lo, int64_t &hi)
 {
-    if (!m.starts) {
-        lo = s * m.T;
-        hi = lo + m.T;
+    if (!m.starts) {   // a row, or a segment of one
+        const int64_t row = s / m.nseg, at = s % m.nseg * m.nckseg * kChunk;
+        lo = row * m.T + at;
+        hi = at + m.nckseg * kChunk < m.T ? lo + m.nckseg * kChunk : (row + 1) * m.T;
         return;
     }
     lo = m.starts[s];
@@ -298,7 +298,7 @@ __device__ __forceinline__ void seq_range(const Map &m, int64_t s, int64_t &lo, 
 // over the sequences before.
 __device__ __forceinline__ int64_t first_slot(const Map &m, int64_t s, int64_t lo)
 {
-    return m.starts ? lo / kChunk + s : s * m.nck;
+    return m.starts ? lo / kChunk + s : s / m.nseg * m.nck + s % m.nseg * m.nckseg;
 }
 
 __device__ __forceinline__ Chunk locate(const Map &m, int64_t slot)
@@ -306,9 +306,10 @@ __device__ __forceinline__ Chunk locate(const Map &m, int64_t slot)
     Chunk c;
     int64_t lo, hi, at;
     if (!m.starts) {
-        c.seq = slot / m.nck;
-        seq_range(m, c.seq, lo, hi);
-        at = slot - c.seq * m.nck;
+        const int64_t row = slot / m.nck;
+        lo = row * m.T;
+        hi = lo + m.T;
+        at = slot - row * m.nck;
     } else {
         int64_t a = 0, b = m.nseq - 1;   // the last sequence whose first slot is <= slot
         while (a < b) {
@@ -319,7 +320,6 @@ __device__ __forceinline__ Chunk locate(const Map &m, int64_t slot)
             else
                 b = mid - 1;
         }
-        c.seq = a;
         seq_range(m, a, lo, hi);
         at = slot - first_slot(m, a, lo);
     }

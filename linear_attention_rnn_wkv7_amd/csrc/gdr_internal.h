@@ -21,11 +21,13 @@ constexpr int kParts = 3;
 // reciprocal lengths of k and (times the scale) q.
 constexpr int kTableFloats = 5 * 64;
 
-// Where the chunks of the sequences lie.
+// Where the chunks of the sequences lie.  Rows that are not packed may be cut
+// into nseg segments of nckseg chunks; the scans take those as sequences.
 struct Map {
     const int32_t *starts;   // packed: [nseq + 1]; else null
     int64_t T, nseq, nck;    // tokens of a row, sequences, chunks per row (unpacked)
     int64_t slots;           // chunk slots in the workspace
+    int64_t nseg, nckseg;
 };
 
 // Whether the scans' workgroups make the chunks' triangular factors themselves
@@ -62,6 +64,9 @@ struct Launch {
     float *ws_ds = nullptr, *ws_dr = nullptr;   // [slots][Hv][K][V], [slots][Hv][64][V]
     float *table = nullptr;                     // [slots][Hv][5][64]
     void *factors = nullptr;                    // [slots][Hv][factor_bytes], or null
+    // segments: how each takes its state on, and the states they start from
+    float *seg_map = nullptr;                   // [nseq * nseg][Hv][K][V + K]
+    float *carry = nullptr;                     // [nseq * nseg][Hv][V][K]
 };
 
 // The factors of every chunk; transposed ones, and the tables, for the backward.

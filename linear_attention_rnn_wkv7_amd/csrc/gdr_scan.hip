@@ -14,6 +14,12 @@
 //     dR = T^T dE  (= dV)
 //     D0 = gamma_C D + (gamma Q)^T dY - (gamma K)^T dR
 // It leaves D (per chunk) and dR for gdr_grads.hip.
+//
+// Few, long rows run in segments.  A chunk takes its state on linearly, S1 =
+// M S0 + L; a first pass runs every segment from a zero state, and beside it
+// K columns that start as the identity and see no values, which gives the
+// segment's L and M; a small kernel runs through the segments of a row; the
+// second pass starts each from its own state.  (Reverse the same way.)
 
 #include "gdr_factor.h"
 
@@ -27,7 +33,7 @@ struct ScanArgs {
     const T *q, *k, *v, *dy;
     const float *s0, *dsT;
     T *y, *dv;
-    float *sT, *ds0;
+    float *sT, *ds0, *seg_map;
     float *st, *rows;    // record: states and E; reverse: D and dR
     float *table;        // reverse
     const float *g, *beta;
@@ -238,7 +244,8 @@ constexpr int kScanLds = kMake ? (int)sizeof(MakeLds<T, K, PP>) : (int)sizeof(Sc
 template <bool kMake>
 constexpr int kMaxThreads = 64 * (kMake ? 4 + kMakers : 8 + 1);
 
-template <typename T, int K, bool kMake, bool kY>
+// kMap: the first pass over segments.
+template <typename T, int K, bool kMake, bool kY, bool kMap>
 __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes, PY = kYParts<T>;
@@ -251,25 +258,34 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int slabs = (int)(blockDim.x >> 6) - (kMake ? kMakers : 1);
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
+    const int64_t row = seq / a.map.nseg, seg = seq % a.map.nseg, Vc = kMap ? a.V + K : a.V;   // columns
+    if (kMap && seg == a.map.nseg - 1) return;   // nothing follows it
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
     if (feed<T, K, PY, false, kMake>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
-    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
+    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < Vc;
+    const bool extra = kMap && 16 * ((int64_t)blockIdx.x * slabs + wave) >= a.V;   // of the identity
 
     f32x4 S[KT];
     const int64_t so = ((seq * a.Hv + hv) * a.V + col) * K + 4 * lg;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
-        S[i] = a.s0 && own ? *reinterpret_cast<const f32x4 *>(a.s0 + so + 16 * i) : zero4();
+        S[i] = !kMap && a.s0 && own ? *reinterpret_cast<const f32x4 *>(a.s0 + so + 16 * i) : zero4();
+    if (extra) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[i][r] = 16 * i + 4 * lg + r == col - a.V ? 1.f : 0.f;
+    }
 
     uint32_t vn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const Cols<T> v(a.v + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) vn[i] = v.load(i);
+        for (int i = 0; i < 16; ++i) vn[i] = extra ? 0u : v.load(i);
     };
     if (own && nc > 0) fetch(0);
     if (nc > 0) first_step<kMake>();
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
 #pragma unroll
             for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = Cols<T>::value(vn[i]);
             if (c + 1 < nc) fetch(c + 1);
-            if (a.st) {
+            if (!kMap && a.st) {
                 const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
                 for (int i = 0; i < KT; ++i) st.store(i, S[i]);
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
                 for (int ks = 0; ks <= it / 2; ++ks)
                     E[it] = mma(E[it], load_tri<T, P, false>(f.t, it, ks, lane), Rf[ks]);
             }
-            if (a.rows) {
+            if (!kMap && a.rows) {
                 const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rows.store(i, E[i]);
@@ -344,13 +360,20 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
         }
         if (c + 1 < nc) step_end<L::kSets>();
     }
-    if (a.sT && own) {
+    if constexpr (kMap) {
+        const Tiles out(a.seg_map + (seq * a.Hv + hv) * K * Vc, K, Vc, col, lg);
+        if (own) {
 #pragma unroll
-        for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(a.sT + so + 16 * i) = S[i];
+            for (int i = 0; i < KT; ++i) out.store(i, S[i]);
+        }
+    } else if (a.sT && own && seg == a.map.nseg - 1) {
+        float *to = a.sT + ((row * a.Hv + hv) * a.V + col) * K + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(to + 16 * i) = S[i];
     }
 }
 
-template <typename T, int K, bool kMake>
+template <typename T, int K, bool kMake, bool kMap>
 __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArgs<T> a)
 {
     constexpr int P = Num<T>::kPlanes;
@@ -363,25 +386,34 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int slabs = (int)(blockDim.x >> 6) - (kMake ? kMakers : 1);
     const int64_t seq = blockIdx.z, hv = blockIdx.y, hk = hv / a.group;
+    const int64_t row = seq / a.map.nseg, seg = seq % a.map.nseg, Vc = kMap ? a.V + K : a.V;   // columns
+    if (kMap && seg == 0) return;   // nothing follows it
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
     if (feed<T, K, P, true, kMake>(a, buf, wave, slabs, blockIdx.x == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
-    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < a.V;
+    const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < Vc;
+    const bool extra = kMap && 16 * ((int64_t)blockIdx.x * slabs + wave) >= a.V;   // of the identity
 
     f32x4 D[KT];
     const int64_t so = ((seq * a.Hv + hv) * a.V + col) * K + 4 * lg;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
-        D[i] = a.dsT && own ? *reinterpret_cast<const f32x4 *>(a.dsT + so + 16 * i) : zero4();
+        D[i] = !kMap && a.dsT && own ? *reinterpret_cast<const f32x4 *>(a.dsT + so + 16 * i) : zero4();
+    if (extra) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) D[i][r] = 16 * i + 4 * lg + r == col - a.V ? 1.f : 0.f;
+    }
 
     uint32_t yn[16];
     auto fetch = [&](int64_t c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const Cols<T> y(a.dy + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) yn[i] = y.load(i);
+        for (int i = 0; i < 16; ++i) yn[i] = extra ? 0u : y.load(i);
     };
     if (own && nc > 0) fetch(nc - 1);
     if (nc > 0) first_step<kMake>();
@@ -395,9 +427,11 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
 #pragma unroll
             for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = Cols<T>::value(yn[j]);
             if (c > 0) fetch(c - 1);
-            const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
+            if constexpr (!kMap) {
+                const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
-            for (int j = 0; j < KT; ++j) st.store(j, D[j]);
+                for (int j = 0; j < KT; ++j) st.store(j, D[j]);
+            }
             f32x4 dE[4];
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) dE[jt] = zero4();
@@ -428,9 +462,11 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
 #pragma unroll
                     for (int ks = jt / 2; ks < 2; ++ks)
                         dR[jt] = mma(dR[jt], load_tri<T, P, true>(f.t, jt, ks, lane), dEf[ks]);
-                    rows.store(jt, dR[jt]);
+                    if constexpr (!kMap) {
+                        rows.store(jt, dR[jt]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) dv.store(4 * jt + r, dR[jt][r]);
+                        for (int r = 0; r < 4; ++r) dv.store(4 * jt + r, dR[jt][r]);
+                    }
                 }
             }
             const float last = f.w[192];
@@ -454,9 +490,51 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
         }
         if (c > 0) step_end<L::kSets>();
     }
-    if (a.ds0 && own) {
+    if constexpr (kMap) {
+        const Tiles out(a.seg_map + (seq * a.Hv + hv) * K * Vc, K, Vc, col, lg);
+        if (own) {
 #pragma unroll
-        for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(a.ds0 + so + 16 * i) = D[i];
+            for (int i = 0; i < KT; ++i) out.store(i, D[i]);
+        }
+    } else if (a.ds0 && own && seg == 0) {
+        float *to = a.ds0 + ((row * a.Hv + hv) * a.V + col) * K + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(to + 16 * i) = D[i];
+    }
+}
+
+// The states the segments of a row start from: S behind a segment is L + M S,
+// of the state before it.  One wave per 16 columns of a row's head; kReverse:
+// from the last segment to the first.
+template <int K, bool kReverse>
+__global__ void __launch_bounds__(64) gdr_carry_kernel(const float *from, const float *seg_map, float *carry, int nseg,
+                                                       int64_t Hv, int64_t V)
+{
+    constexpr int KT = K / 16;
+    const int lane = threadIdx.x, lg = lane >> 4, l16 = lane & 15;
+    const int64_t row = blockIdx.z, hv = blockIdx.y, col = 16 * (int64_t)blockIdx.x + l16, Vc = V + K;
+    f32x4 S[KT];
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+        S[i] = from ? *reinterpret_cast<const f32x4 *>(from + ((row * Hv + hv) * V + col) * K + 16 * i + 4 * lg) : zero4();
+    for (int n = 0; n < nseg; ++n) {
+        const int64_t seq = row * nseg + (kReverse ? nseg - 1 - n : n);
+        float *to = carry + ((seq * Hv + hv) * V + col) * K + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(to + 16 * i) = S[i];
+        if (n + 1 == nseg) break;
+        const float *m = seg_map + (seq * Hv + hv) * K * Vc;
+        f32x4 N[KT];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) N[i][r] = m[(16 * i + 4 * lg + r) * Vc + col];
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+                N[i] = mma16(N[i], *reinterpret_cast<const f32x4 *>(m + (16 * i + l16) * Vc + V + 16 * k + 4 * lg), S[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < KT; ++i) S[i] = N[i];
     }
 }
 
@@ -483,6 +561,7 @@ ScanArgs<T> scan_args(const Launch &a)
     p.norm = a.norm;
     p.scale = a.scale;
     p.factors = static_cast<const char *>(a.factors);
+    p.seg_map = a.seg_map;
     p.Hk = a.Hk;
     p.Hv = a.Hv;
     p.V = a.V;
@@ -492,13 +571,13 @@ ScanArgs<T> scan_args(const Launch &a)
 
 // Slabs per workgroup, a wave each: as many as there are (`most` at most),
 // fewer while that leaves compute units without a workgroup.
-int scan_grid(const Launch &a, int most, dim3 *grid)
+int scan_grid(const Launch &a, int64_t columns, int most, dim3 *grid)
 {
-    const int64_t slabs = a.V / 16, units = a.map.nseq * a.Hv;
+    const int64_t slabs = columns / 16, seqs = a.map.nseq * a.map.nseg, units = seqs * a.Hv;
     int64_t groups = (slabs + most - 1) / most;
     while (units * groups < 256 && groups < slabs) ++groups;
     const int64_t per = (slabs + groups - 1) / groups;
-    *grid = dim3((unsigned)((slabs + per - 1) / per), (unsigned)a.Hv, (unsigned)a.map.nseq);
+    *grid = dim3((unsigned)((slabs + per - 1) / per), (unsigned)a.Hv, (unsigned)seqs);
     return (int)per;
 }
 
@@ -507,16 +586,35 @@ hipError_t scan_t(const Launch &a, bool reverse, hipStream_t stream)
 {
     ScanArgs<T> p = scan_args<T>(a);
     dim3 grid;
-    const int slabs = scan_grid(a, kMake ? 4 : 8, &grid);
+    if constexpr (!kMake) {
+        if (a.map.nseg > 1) {
+            const dim3 block(64 * (scan_grid(a, a.V + K, 8, &grid) + 1));
+            const dim3 rows((unsigned)(a.V / 16), (unsigned)a.Hv, (unsigned)a.map.nseq);
+            if (reverse) {
+                hipLaunchKernelGGL((gdr_reverse_kernel<T, K, false, true>), grid, block, 0, stream, p);
+                hipLaunchKernelGGL((gdr_carry_kernel<K, true>), rows, dim3(64), 0, stream, a.dsT, a.seg_map, a.carry,
+                                   (int)a.map.nseg, a.Hv, a.V);
+                p.dsT = a.carry;
+            } else {
+                hipLaunchKernelGGL((gdr_scan_kernel<T, K, false, false, true>), grid, block, 0, stream, p);
+                hipLaunchKernelGGL((gdr_carry_kernel<K, false>), rows, dim3(64), 0, stream, a.s0, a.seg_map, a.carry,
+                                   (int)a.map.nseg, a.Hv, a.V);
+                p.s0 = a.carry;
+            }
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+    }
+    const int slabs = scan_grid(a, a.V, kMake ? 4 : 8, &grid);
     const dim3 block(64 * (slabs + (kMake ? kMakers : 1)));
     if (reverse) {
         p.st = a.ws_ds;
         p.rows = a.ws_dr;
-        hipLaunchKernelGGL((gdr_reverse_kernel<T, K, kMake>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_reverse_kernel<T, K, kMake, false>), grid, block, 0, stream, p);
     } else if (a.y) {
-        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, true>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, true, false>), grid, block, 0, stream, p);
     } else {
-        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, false>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((gdr_scan_kernel<T, K, kMake, false, false>), grid, block, 0, stream, p);
     }
     return hipGetLastError();
 }

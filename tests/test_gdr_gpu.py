@@ -105,6 +105,20 @@ def test_rule(case):
     check(run(d, norm=norm, record=record), reference(d, norm=norm), str(case))
 
 
+SEGMENTS = [   # rows of 16 chunks and more with few heads run in segments
+    (1, 1024, 1, 1, 64, 16, F32, True, True, True, True),
+    (1, 1030, 1, 2, 64, 48, BF16, False, True, True, False),
+    (2, 1500, 1, 3, 128, 64, BF16, True, True, True, True),
+    (1, 1217, 2, 2, 128, 32, F32, False, False, False, True),
+    (1, 2100, 1, 1, 64, 64, BF16, True, False, True, True),
+]
+
+
+@pytest.mark.parametrize("case", SEGMENTS, ids=["-".join(map(str, c)).replace("torch.", "") for c in SEGMENTS])
+def test_rule_segments(case):
+    test_rule(case)
+
+
 PACKED = [
     [0, 5],
     [0, 0, 1, 65, 65, 130, 131],
