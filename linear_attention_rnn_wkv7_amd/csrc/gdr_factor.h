@@ -27,10 +27,23 @@ namespace gdr {
 // A triangle's ten 16 x 16 tiles, row by row.
 __device__ __forceinline__ constexpr int tile_id(int i, int j) { return i * (i + 1) / 2 + j; }
 
-// As operands (kTri elements per part): for a tile, each lane's four
-// values, row l16 and columns 4 lg .. 4 lg + 3 of the tile or, kTrans, of
-// its transpose.
+// As operands (kTri elements per part): for a tile, each lane's four values,
+// row l16 and columns 4 lg .. 4 lg + 3 of the tile or, kTrans, of its
+// transpose.  In bf16, tiles that make up one 32-deep step of an operand lie
+// side by side in a lane's 16 bytes; the two that stand alone in theirs share
+// the last place.
 constexpr int kTri = 10 * 64 * 4;
+template <bool kTrans>
+__device__ __forceinline__ constexpr int tri_place(int tile)
+{
+    return (int)((kTrans ? 0x9753642810ull : 0x7654932108ull) >> (4 * tile)) & 15;
+}
+template <typename T, bool kTrans>
+__device__ __forceinline__ constexpr int tri_at(int tile, int lane)
+{
+    if (sizeof(T) == 4) return (tile * 64 + lane) * 4;
+    return ((tri_place<kTrans>(tile) >> 1) * 64 + lane) * 8 + (tri_place<kTrans>(tile) & 1) * 4;
+}
 
 // Row tile `it` of a lower triangle (steps 0 .. it / 2), or of a transposed
 // one (steps it / 2 .. 1), as the left operand of step ks.
@@ -39,17 +52,21 @@ __device__ __forceinline__ Frag<T, P> load_tri(const T *base, int it, int ks, in
 {
     using Quad = typename Num<T>::Quad;
     Frag<T, P> f;
+    const bool lo = kTrans ? 2 * ks >= it : true, hi = kTrans ? true : 2 * ks + 1 <= it;   // tiles of the triangle
+    const int a = kTrans ? tile_id(2 * ks, it) : tile_id(it, 2 * ks), b = kTrans ? tile_id(2 * ks + 1, it) : tile_id(it, 2 * ks + 1);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        Quad h[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = 2 * ks + i;
-            h[i] = Quad{};
-            if (kTrans ? k >= it : k <= it)
-                h[i] = *reinterpret_cast<const Quad *>(base + p * kTri + ((kTrans ? tile_id(k < it ? it : k, it) : tile_id(it, k > it ? it : k)) * 64 + lane) * 4);
+        if (lo && hi && sizeof(T) == 4) {
+            f.p[p] = __builtin_shufflevector(*reinterpret_cast<const Quad *>(base + p * kTri + tri_at<T, kTrans>(a, lane)),
+                                             *reinterpret_cast<const Quad *>(base + p * kTri + tri_at<T, kTrans>(b, lane)),
+                                             0, 1, 2, 3, 4, 5, 6, 7);
+        } else if (lo && hi) {
+            f.p[p] = *reinterpret_cast<const typename Num<T>::Oct *>(base + p * kTri + tri_at<T, kTrans>(a, lane));
+        } else {
+            const Quad x = *reinterpret_cast<const Quad *>(base + p * kTri + tri_at<T, kTrans>(lo ? a : b, lane));
+            f.p[p] = lo ? __builtin_shufflevector(x, Quad{}, 0, 1, 2, 3, 4, 5, 6, 7)
+                        : __builtin_shufflevector(Quad{}, x, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-        f.p[p] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return f;
 }
@@ -87,16 +104,26 @@ __device__ __forceinline__ f32x4 mma16(f32x4 c, f32x4 a, f32x4 b)
 }
 
 // Tiles in D layout as left operands of their transposes, in P parts.
-template <typename T, int P>
+template <typename T, int P, bool kTrans>
 __device__ __forceinline__ void write_tri(T *out, const f32x4 (&X)[10], int lane)
 {
-    using Quad = typename Num<T>::Quad;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        Quad q[P];
-        split_quad<T, P>(X[i], q);
+        for (int t = 0; t < 10; ++t) *reinterpret_cast<f32x4 *>(out + tri_at<T, kTrans>(t, lane)) = X[t];
+        return;
+    }
 #pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<Quad *>(out + p * kTri + (i * 64 + lane) * 4) = q[p];
+    for (int i = 0; i < 10; i += 2) {   // places i, i + 1
+        f32x4 x[2];
+#pragma unroll
+        for (int t = 0; t < 10; ++t) {
+            if (tri_place<kTrans>(t) == i) x[0] = X[t];
+            if (tri_place<kTrans>(t) == i + 1) x[1] = X[t];
+        }
+        const Frag<T, P> f = make_frag<T, P>(x[0], x[1]);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            *reinterpret_cast<typename Num<T>::Oct *>(out + p * kTri + (i / 2 * 64 + lane) * 8) = f.p[p];
     }
 }
 
@@ -305,8 +332,8 @@ struct Factors {
     template <int PP>
     __device__ __forceinline__ void finish(T *t, T *p, float *weights, int lane)
     {
-        write_tri<T, Num<T>::kPlanes>(t, kk, lane);
-        write_tri<T, PP>(p, qk, lane);
+        write_tri<T, Num<T>::kPlanes, kTrans>(t, kk, lane);
+        write_tri<T, PP, kTrans>(p, qk, lane);
         weights[lane] = wa;
         weights[64 + lane] = wb;
         weights[128 + lane] = we;

@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
                     const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj));
                     x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -X[n][r] : Z[n][r]) : 0.f;
                     // row i, k = j
-                    put1<T, P>(s.u.w[0], (t * 64 + (l16 >> 2) * 16 + 4 * lg + r) * 4 + (l16 & 3), x[r] * cj);
+                    put1<T, P>(s.u.w[0], tri_at<T, false>(t, (l16 >> 2) * 16 + 4 * lg + r) + (l16 & 3), x[r] * cj);
                 }
-                put<T, P>(s.u.w[1], (t * 64 + lane) * 4, x * row4(s.tab, zx ? 3 : 4, i0));   // row j, k = i
+                put<T, P>(s.u.w[1], tri_at<T, true>(t, lane), x * row4(s.tab, zx ? 3 : 4, i0));   // row j, k = i
             }
             __syncthreads();
 #pragma unroll

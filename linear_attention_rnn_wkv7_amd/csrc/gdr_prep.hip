@@ -27,7 +27,11 @@ __global__ void __launch_bounds__(256, 2) gdr_prep_kernel(PrepArgs<T> a)
     constexpr int PP = kTrans ? Num<T>::kPlanes : kYParts<T>;
     __shared__ __align__(16) FactorLds lds[4];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t slot = (int64_t)blockIdx.x * 4 + w, hv = blockIdx.y, hk = hv / a.group, ch = slot * a.Hv + hv;
+    // Workgroups go round the 8 dies; those of one die take the heads of one
+    // set of chunks before the next, so that g and beta, a few bytes of each
+    // line to a head, are fetched once.
+    const int64_t at = blockIdx.x >> 3;
+    const int64_t slot = (at / a.Hv * 8 + (blockIdx.x & 7)) * 4 + w, hv = at % a.Hv, hk = hv / a.group, ch = slot * a.Hv + hv;
     if (slot >= a.map.slots) return;
     const Chunk c = locate(a.map, slot);
     if (c.len == 0) return;
@@ -56,7 +60,7 @@ hipError_t launch_t(const Launch &a, bool transposed, hipStream_t stream)
     p.group = (int)(a.Hv / a.Hk);
     p.norm = a.norm;
     p.scale = a.scale;
-    const dim3 grid((unsigned)((a.map.slots + 3) / 4), (unsigned)a.Hv);
+    const dim3 grid((unsigned)((a.map.slots + 31) / 32 * 8 * a.Hv));
     if (transposed)
         hipLaunchKernelGGL((gdr_prep_kernel<T, K, true>), grid, dim3(256), 0, stream, p);
     else

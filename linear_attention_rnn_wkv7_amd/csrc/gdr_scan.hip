@@ -135,9 +135,9 @@ __device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
 // with a barrier between two steps: the slabs take chunk c in step c (the c-th
 // chunk of their direction), its operands arrive in step c - 1.
 
-// One wave copies them from memory: issuing copies stalls whenever the memory
+// One wave copies them from memory (kAll: with Q and P): issuing copies stalls whenever the memory
 // system has no room for more, and would stall the products with it.
-template <typename T, int K, int PP, bool kTrans>
+template <typename T, int K, int PP, bool kTrans, bool kAll>
 __device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K, PP> &s, int64_t lo, int64_t hi, int64_t slot0,
                                           int64_t hv, int64_t hk, int64_t nc, int lane)
 {
@@ -150,8 +150,14 @@ __device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K, PP
         const int set = L::kSets == 2 ? (int)(i & 1) : 0;
         if (L::kSets == 1 && i > 0) __syncthreads();   // the only set is free
         dma_rows<T, K>(s.k[set], a.k + o, a.Hk * K, at.len, lane);
-        dma_flat<sizeof(F)>(&s.f[set], a.factors + at.ch * sizeof(F), lane);
-        dma_rows<T, K>(s.q[set], a.q + o, a.Hk * K, at.len, lane);
+        const F *f = reinterpret_cast<const F *>(a.factors) + at.ch;
+        if constexpr (kAll) {
+            dma_flat<sizeof(F)>(&s.f[set], f, lane);
+            dma_rows<T, K>(s.q[set], a.q + o, a.Hk * K, at.len, lane);
+        } else {
+            dma_flat<sizeof(F::t)>(s.f[set].t, f->t, lane);
+            dma_flat<sizeof(F::w)>(s.f[set].w, f->w, lane);
+        }
         wait_dma();
         __syncthreads();
     }
@@ -203,7 +209,7 @@ __device__ __forceinline__ void make_loop(const ScanArgs<T> &a, MakeLds<T, K, PP
 }
 
 // The waves besides the slabs': returns false in a slab's wave.
-template <typename T, int K, int PP, bool kTrans, bool kMake>
+template <typename T, int K, int PP, bool kTrans, bool kMake, bool kAll>
 __device__ __forceinline__ bool feed(const ScanArgs<T> &a, char *buf, int wave, int slabs, bool tables, int64_t lo,
                                      int64_t hi, int64_t slot0, int64_t hv, int64_t hk, int64_t nc, int lane)
 {
@@ -216,7 +222,7 @@ __device__ __forceinline__ bool feed(const ScanArgs<T> &a, char *buf, int wave, 
         }
     } else {
         if (wave == slabs) {
-            copy_loop<T, K, PP, kTrans>(a, *reinterpret_cast<ScanLds<T, K, PP> *>(buf), lo, hi, slot0, hv, hk, nc, lane);
+            copy_loop<T, K, PP, kTrans, kAll>(a, *reinterpret_cast<ScanLds<T, K, PP> *>(buf), lo, hi, slot0, hv, hk, nc, lane);
             return true;
         }
     }
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (feed<T, K, PY, false, kMake>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
+    if (feed<T, K, PY, false, kMake, kY>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < Vc;
     const bool extra = kMap && 16 * ((int64_t)blockIdx.x * slabs + wave) >= a.V;   // of the identity
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (feed<T, K, P, true, kMake>(a, buf, wave, slabs, blockIdx.x == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
+    if (feed<T, K, P, true, kMake, true>(a, buf, wave, slabs, blockIdx.x == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)blockIdx.x * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)blockIdx.x * slabs + wave) < Vc;
     const bool extra = kMap && 16 * ((int64_t)blockIdx.x * slabs + wave) >= a.V;   // of the identity
