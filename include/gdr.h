@@ -38,7 +38,7 @@
  * leading 24 bits, with fp32 sums.  y and the gradients of q, k, v are rounded once, to the
  * inputs' type.  Results are the same bit for bit from run to run.
  *
- * Sizes.  At most 65535 sequences and value heads, and 2^25 chunks of 64
+ * Sizes.  At most 65535 sequences and value heads, and 2^22 chunks of 64
  * tokens times value heads (WKV7_ERR_UNSUPPORTED beyond).
  *
  * Ownership, execution and errors as for wkv7.h: device pointers owned by the

@@ -92,7 +92,7 @@ int check(const gdr_shape *s, Dims *d)
     if (d->slots > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
     if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 2 * 4096), &x))
         return WKV7_ERR_INVALID;   // any sum of the workspace's parts
-    if (per > (int64_t(1) << 25)) return WKV7_ERR_UNSUPPORTED;   // a workgroup for every four
+    if (per > (int64_t(1) << 22)) return WKV7_ERR_UNSUPPORTED;   // a workgroup of 512 for each
     plan_segments(d);
     const size_t segs = d->nseg > 1 ? (size_t)(s->B * s->Hv * d->nseg) : 0;
     d->seg_map = segs * (size_t)(s->K * (s->V + s->K) * 4);

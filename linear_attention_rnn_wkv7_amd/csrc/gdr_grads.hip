@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
     constexpr int P = L::P, LV = L::LV, W = L::W, NZ = (10 + W - 1) / W;   // tiles of Z, X per wave
     __shared__ __align__(16) char buf[sizeof(L)];
     L &s = *reinterpret_cast<L *>(buf);
-    const int64_t slot = blockIdx.x, hk = blockIdx.y;
+    // the heads of a chunk together on one of the 8 dies, as in gdr_prep.hip: dg
+    // and dbeta are a few bytes of each line to a head
+    const int64_t at = blockIdx.x >> 3, slot = at / a.Hk * 8 + (blockIdx.x & 7), hk = at % a.Hk;
+    if (slot >= a.map.slots) return;
     const Chunk c = locate(a.map, slot);
     if (c.len == 0) return;
     const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
@@ -343,7 +346,7 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.group = (int)(a.Hv / a.Hk);
     p.norm = a.norm;
     p.scale = a.scale;
-    const dim3 grid((unsigned)a.map.slots, (unsigned)a.Hk);
+    const dim3 grid((unsigned)((a.map.slots + 7) / 8 * 8 * a.Hk));
     if (p.group > 1)
         hipLaunchKernelGGL((gdr_grads_kernel<T, K, true>), grid, dim3(4 * K), 0, stream, p);
     else
