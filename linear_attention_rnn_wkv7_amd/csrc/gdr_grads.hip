@@ -17,8 +17,11 @@
 // One workgroup per chunk and key head; it adds up the group's value heads in
 // registers.  Each of its K / 16 waves owns 16 key columns: it reads its rows
 // of S and D once from memory as operands.  E, dR, dY pass through LDS 32
-// values at a time, then Z and X, in operand order; so that two workgroups
-// share a compute unit and cover each other's waits.
+// values at a time; then one copy each of the C x C arrays
+//     U_ij = rq_i Gamma_ij Z_ij,   V_ij = -rk_i Gamma_ij X_ij
+// (rq, rk: what q, k as passed are multiplied by), which serves by rows for F
+// and, through transposing reads, by columns for dq and A, whose other operand
+// is k_j beta_j rk_j and whose rows are divided by rq_i, rk_i again.
 
 #include "gdr_factor.h"
 
@@ -40,62 +43,115 @@ struct GradArgs {
 
 constexpr int kVB = 32;   // values of E, dR, dY in LDS at a time
 
+// Rows of kVB values, their 16-byte pieces permuted so that 16 rows' reads of
+// one piece meet all banks.
+template <typename T>
+__device__ __forceinline__ int in_row(int row, int k)   // of four values from k
+{
+    constexpr int kPer = 16 / (int)sizeof(T);   // values of a piece
+    const int pos = kpos(k), piece = pos / kPer;
+    return row * kVB + (piece ^ (sizeof(T) == 2 ? (row >> 2) & 3 : (row >> 1) & 7)) * kPer + pos % kPer;
+}
+template <typename T, int P>
+__device__ __forceinline__ Frag<T, P> load_in(const T *base, int it, int lg, int l16)
+{
+    Frag<T, P> f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const T *b = base + p * 64 * kVB;
+        if constexpr (sizeof(T) == 2)
+            f.p[p] = *reinterpret_cast<const typename Num<T>::Oct *>(b + in_row<T>(16 * it + l16, 4 * lg));
+        else
+            f.p[p] = __builtin_shufflevector(*reinterpret_cast<const f32x4 *>(b + in_row<T>(16 * it + l16, 4 * lg)),
+                                             *reinterpret_cast<const f32x4 *>(b + in_row<T>(16 * it + l16, 16 + 4 * lg)),
+                                             0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+
+// A lower triangle's tiles, each stored by columns ([j][i], 16 x 16) per part.
+constexpr int kTri16 = 10 * 256;
+// Step ks of row tile `it` of the triangle itself (rows i, k = j).
+template <typename T, int P>
+__device__ __forceinline__ Frag<T, P> tri_rows(const T *base, int it, int ks, int lg, int l16)
+{
+    Frag<T, P> f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        typename Num<T>::Quad h[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int jt = 2 * ks + n;
+            h[n] = typename Num<T>::Quad{};
+            if (jt > it) continue;
+            const T *t = base + p * kTri16 + tile_id(it, jt) * 256;
+            if constexpr (sizeof(T) == 2) {   // row j = 4 lg + l16 / 4, columns 4 (l16 % 4) .. to a lane
+                const T *a = t + (4 * lg + (l16 >> 2)) * 16 + 4 * (l16 & 3);
+                h[n] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                    (__attribute__((address_space(3))) bf16x4 *)(const __attribute__((address_space(3))) T *)a);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[n][r] = t[(4 * lg + r) * 16 + l16];
+            }
+        }
+        f.p[p] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+// Step ks of row tile jt of its transpose (rows j, k = i).
+template <typename T, int P>
+__device__ __forceinline__ Frag<T, P> tri_cols(const T *base, int jt, int ks, int lg, int l16)
+{
+    Frag<T, P> f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        typename Num<T>::Quad h[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int it = 2 * ks + n;
+            h[n] = typename Num<T>::Quad{};
+            if (it >= jt)
+                h[n] = *reinterpret_cast<const typename Num<T>::Quad *>(base + p * kTri16 + tile_id(it, jt) * 256 + l16 * 16 + 4 * lg);
+        }
+        f.p[p] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+
 template <typename T, int K>
 struct GradLds {
-    static constexpr int P = Num<T>::kPlanes, LV = kVB + kPad<T>, W = K / 16;
+    static constexpr int P = Num<T>::kPlanes, W = K / 16;
     char k[Swizzled<T, K>::kBytes], q[Swizzled<T, K>::kBytes];
     union {
         struct {
-            T dy[64 * LV], dr[P * 64 * LV], e[P * 64 * LV];
+            T dy[64 * kVB], dr[P * 64 * kVB], e[P * 64 * kVB];
         } in;
-        T w[2][P * kTri];   // of Z, then of X: by rows, and transposed
+        T w[2][P * kTri16];   // U, V
     } u;
     float tab[kTableFloats], gam[64], eh[64];
-    float red[4][W][64];       // q.dq, k.A, k.F, k.M3 of each wave's columns
-    float ip[W];               // <S, D>
+    float red[3][W][64];       // of each wave's columns: all of dG's dots, k.F; with norm k.A, k.F, q.dq
+    float ip[W];               // gamma_C <S, D> + sum_j beta_j e_j k_j . M3_j
     float tq[64], tk[64];      // over the group: q.dq, k.dk
 };
 
-template <typename T, int P>
-__device__ __forceinline__ void put(T *dst, int at, f32x4 x)   // 4 consecutive elements
+// Row sums over the wave's 16 columns, into red.
+__device__ __forceinline__ void row_sums(float *red, int it, int lg, int l16, f32x4 x)
 {
-    typename Num<T>::Quad q[P];
-    split_quad<T, P>(x, q);
-#pragma unroll
-    for (int i = 0; i < P; ++i) *reinterpret_cast<typename Num<T>::Quad *>(dst + i * kTri + at) = q[i];
-}
-
-template <typename T, int P>
-__device__ __forceinline__ void put1(T *dst, int at, float x)
-{
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const T z = (T)x;
-        dst[i * kTri + at] = z;
-        x -= (float)z;
-    }
-}
-
-// Row and column of triangle tile t.
-__device__ __forceinline__ int tile_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
-
-// Row sums over the wave's 16 columns of x * y, into red.
-__device__ __forceinline__ void row_dots(float *red, int it, int lg, int l16, f32x4 x, f32x4 y)
-{
-    const f32x4 xy = x * y;
     f32x4 z;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z[r] = group_allreduce<16>(xy[r]);
+    for (int r = 0; r < 4; ++r) z[r] = group_allreduce<16>(x[r]);
     if (l16 == 0) *reinterpret_cast<f32x4 *>(red + 16 * it + 4 * lg) = z;
 }
 
+// Registers for three workgroups of four waves on a compute unit (LDS holds as
+// many), or two where the sums over a group need them.
 template <typename T, int K, bool kShared>
-__global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
+__global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ? 3 : 2) gdr_grads_kernel(GradArgs<T> a)
 {
     using L = GradLds<T, K>;
     using Quad = typename Num<T>::Quad;
     using Sw = Swizzled<T, K>;
-    constexpr int P = L::P, LV = L::LV, W = L::W, NZ = (10 + W - 1) / W;   // tiles of Z, X per wave
+    constexpr int P = L::P, W = L::W;
     __shared__ __align__(16) char buf[sizeof(L)];
     L &s = *reinterpret_cast<L *>(buf);
     // the heads of a chunk together on one of the 8 dies, as in gdr_prep.hip: dg
@@ -104,12 +160,17 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
     if (slot >= a.map.slots) return;
     const Chunk c = locate(a.map, slot);
     if (c.len == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // column tile w % 4 of Z and 3 - w % 4 of X is this wave's, five tiles; of
+    // eight waves, two have every other row tile
+    constexpr int kHalf = W / 4;
+    constexpr bool kAhead = W == 8;   // loads of the next block before this one's products
+    const int zcol = w & 3, xcol = 3 - zcol;
+    auto mine = [&](int it, int jt) { return it >= jt && (kHalf == 1 || ((it ^ w ^ (w >> 2)) & 1) == 0); };
 
     if (w < 2) {
         dma_rows<T, K>(w ? s.q : s.k, (w ? a.q : a.k) + (c.tok * a.Hk + hk) * K, a.Hk * K, c.len, lane);
-        wait_dma();
     }
     if (tid < 64) s.tq[tid] = s.tk[tid] = 0.f;
 
@@ -120,51 +181,62 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
     }
     for (int gi = 0; gi < (kShared ? a.group : 1); ++gi) {
         const int64_t hv = hk * a.group + gi, ch = slot * a.Hv + hv;
-        __syncthreads();
-        for (int i = tid; i < kTableFloats / 4; i += 64 * W)
-            reinterpret_cast<f32x4 *>(s.tab)[i] = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[i];
-        f32x4 M1[4], M2[4], M3[4], Z[NZ], X[NZ];
+        f32x4 M1[4], M2[4], M3[4], Z[2][4 / kHalf];
         float ip = 0.f;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) M1[it] = M2[it] = M3[it] = zero4();
-#pragma unroll
-        for (int i = 0; i < NZ; ++i) Z[i] = X[i] = zero4();
-        const float *Sr = a.S + (ch * K + 16 * w + l16) * a.V + 4 * lg, *Dr = a.D + (ch * K + 16 * w + l16) * a.V + 4 * lg;
-        for (int v0 = 0; v0 < (int)a.V; v0 += kVB) {
+        for (int it = 0; it < 4; ++it) M1[it] = M2[it] = M3[it] = Z[0][it / kHalf] = Z[1][it / kHalf] = zero4();
+        // addresses as a uniform base and 32-bit offsets
+        const uint32_t V = (uint32_t)a.V;
+        const float *Sb = a.S + ch * K * a.V, *Db = a.D + ch * K * a.V, *Rb = a.dR + ch * 64 * a.V, *Eb = a.E + ch * 64 * a.V;
+        const T *yb = a.dy + (c.tok * a.Hv + hv) * a.V;
+        const uint32_t ys = (uint32_t)(a.Hv * a.V);
+        f32x4 x[2], d[2], rq[8 / W], eq[8 / W];
+        Quad yq[8 / W];
+        auto fetch = [&](uint32_t v0) {
+            const uint32_t tid = fresh(threadIdx.x), lg = tid >> 4 & 3, l16 = tid & 15;   // addresses formed anew, not kept
             // V is a multiple of 16: the second half of the block may be beyond it
-            const bool half = v0 + 16 < (int)a.V;
-            f32x4 x[2] = {zero4(), zero4()}, d[2] = {zero4(), zero4()};
-            x[0] = *reinterpret_cast<const f32x4 *>(Sr + v0);
-            d[0] = *reinterpret_cast<const f32x4 *>(Dr + v0);
-            if (half) {
-                x[1] = *reinterpret_cast<const f32x4 *>(Sr + v0 + 16);
-                d[1] = *reinterpret_cast<const f32x4 *>(Dr + v0 + 16);
-            }
-            Quad yq[8 / W];
-            f32x4 rq[8 / W], eq[8 / W];
+            const uint32_t so = (uint32_t)(16 * w + l16) * V + v0 + 4 * lg;
 #pragma unroll
-            for (int n = 0; n < 8 / W; ++n) {
-                const int t = (tid + n * 64 * W) >> 3, v = v0 + 4 * (tid & 7);
-                yq[n] = Quad{};
-                rq[n] = eq[n] = zero4();
-                if (v < (int)a.V) {
-                    if (t < c.len) yq[n] = *reinterpret_cast<const Quad *>(a.dy + ((c.tok + t) * a.Hv + hv) * a.V + v);
-                    rq[n] = *reinterpret_cast<const f32x4 *>(a.dR + (ch * 64 + t) * a.V + v);
-                    eq[n] = *reinterpret_cast<const f32x4 *>(a.E + (ch * 64 + t) * a.V + v);
+            for (int h = 0; h < 2; ++h) {
+                x[h] = d[h] = zero4();
+                if (v0 + 16 * h < V) {
+                    x[h] = *reinterpret_cast<const f32x4 *>(Sb + so + 16 * h);
+                    d[h] = *reinterpret_cast<const f32x4 *>(Db + so + 16 * h);
                 }
             }
-            if (v0 > 0) __syncthreads();   // the block before is done with
 #pragma unroll
             for (int n = 0; n < 8 / W; ++n) {
-                const int at = ((tid + n * 64 * W) >> 3) * LV + kpos(4 * (tid & 7));
+                const uint32_t t = (tid + n * 64 * W) >> 3, v = v0 + 4 * (tid & 7);
+                yq[n] = Quad{};
+                rq[n] = eq[n] = zero4();
+                if (v < V) {
+                    if ((int)t < c.len) yq[n] = *reinterpret_cast<const Quad *>(yb + t * ys + v);
+                    rq[n] = *reinterpret_cast<const f32x4 *>(Rb + t * V + v);
+                    eq[n] = *reinterpret_cast<const f32x4 *>(Eb + t * V + v);
+                }
+            }
+        };
+        if constexpr (kAhead) fetch(0);
+        const f32x4 tv = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[tid < kTableFloats / 4 ? tid : 0];
+        if (gi > 0) __syncthreads();   // the table of the head before is done with
+        for (uint32_t v0 = 0; v0 < V; v0 += kVB) {
+            if constexpr (!kAhead) fetch(v0);
+            const int ft = (int)fresh(tid), lane = ft & 63, lg = lane >> 4, l16 = lane & 15;
+            if (v0 > 0)
+                __syncthreads();   // the block before is done with
+            else if (tid < kTableFloats / 4)
+                reinterpret_cast<f32x4 *>(s.tab)[tid] = tv;
+#pragma unroll
+            for (int n = 0; n < 8 / W; ++n) {
+                const int to = in_row<T>((ft + n * 64 * W) >> 3, 4 * (ft & 7));
                 Quad rz[P], ez[P];
                 split_quad<T, P>(rq[n], rz);
                 split_quad<T, P>(eq[n], ez);
-                *reinterpret_cast<Quad *>(s.u.in.dy + at) = yq[n];
+                *reinterpret_cast<Quad *>(s.u.in.dy + to) = yq[n];
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * LV + at) = rz[p];
-                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * LV + at) = ez[p];
+                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * kVB + to) = rz[p];
+                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * kVB + to) = ez[p];
                 }
             }
 #pragma unroll
@@ -173,31 +245,40 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
                 ip += (xd[0] + xd[1]) + (xd[2] + xd[3]);
             }
             const Frag<T, P> Sf = make_frag<T, P>(x[0], x[1]), Df = make_frag<T, P>(d[0], d[1]);
+            if constexpr (kAhead) {
+                if (v0 + kVB < V) fetch(v0 + kVB);
+            }
+            if (v0 == 0 && gi == 0) wait_dma();   // of k, q, older than the block's loads
             __syncthreads();
+            // one array of rows after the other: registers for few operands at a time
+            {
+                const Frag<T, P> E = load_in<T, P>(s.u.in.e, zcol, lg, l16);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                M1[it] = mma(M1[it], load_frag<T, 1>(s.u.in.dy, 16 * it + l16, LV, 0, lg, 0), Sf);
-                M2[it] = mma(M2[it], load_frag<T, P>(s.u.in.dr, 16 * it + l16, LV, 0, lg, 64 * LV), Sf);
-                M3[it] = mma(M3[it], load_frag<T, P>(s.u.in.e, 16 * it + l16, LV, 0, lg, 64 * LV), Df);
+                for (int it = 0; it < 4; ++it) {
+                    const Frag<T, 1> y = load_in<T, 1>(s.u.in.dy, it, lg, l16);
+                    M1[it] = mma(M1[it], y, Sf);
+                    if (mine(it, zcol)) Z[0][it / kHalf] = mma(Z[0][it / kHalf], y, E);
+                }
             }
-            // tiles w, w + W, .. of Z, and from the other end of X
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                const Frag<T, P> E = load_in<T, P>(s.u.in.e, xcol, lg, l16);
 #pragma unroll
-            for (int i = 0; i < NZ; ++i) {
-                const int tz = w + i * W, tx = 9 - tz;
-                if (tz >= 10) continue;
-                const int zi = tile_row(tz), zj = tz - tile_id(zi, 0), xi = tile_row(tx), xj = tx - tile_id(xi, 0);
-                Z[i] = mma(Z[i], load_frag<T, 1>(s.u.in.dy, 16 * zi + l16, LV, 0, lg, 0),
-                           load_frag<T, P>(s.u.in.e, 16 * zj + l16, LV, 0, lg, 64 * LV));
-                X[i] = mma(X[i], load_frag<T, P>(s.u.in.dr, 16 * xi + l16, LV, 0, lg, 64 * LV),
-                           load_frag<T, P>(s.u.in.e, 16 * xj + l16, LV, 0, lg, 64 * LV));
+                for (int it = 0; it < 4; ++it) {
+                    const Frag<T, P> r = load_in<T, P>(s.u.in.dr, it, lg, l16);
+                    M2[it] = mma(M2[it], r, Sf);
+                    if (mine(it, xcol)) Z[1][it / kHalf] = mma(Z[1][it / kHalf], r, E);
+                }
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) M3[it] = mma(M3[it], load_in<T, P>(s.u.in.e, it, lg, l16), Df);
         }
+        const int ln = (int)fresh(lane), lg = ln >> 4, l16 = ln & 15;
         if (tid < 64) {
             s.gam[tid] = __builtin_amdgcn_exp2f(s.tab[tid] + s.tab[64 + tid]);
             s.eh[tid] = __builtin_amdgcn_exp2f((s.tab[63] - s.tab[tid]) + (s.tab[64 + 63] - s.tab[64 + tid]));
         }
-        ip = wave_sum(ip);
-        if (lane == 0) s.ip[w] = ip;
         // this wave's columns of q and k as operands; position 4 (it & 1) + r of
         // step it / 2 is row 16 it + 4 lg + r
         Frag<T, 1> kf[2], qf[2];
@@ -206,59 +287,85 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
             kf[ks] = Sw::cols(s.k, w, ks, lg, l16);
             qf[ks] = Sw::cols(s.q, w, ks, lg, l16);
         }
-        auto value = [&](const Frag<T, 1> (&f)[2], int it, int kind) {
+        auto value = [&](const Frag<T, 1> (&f)[2], int it) {
             f32x4 x;
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[r] = to_f32(f[it >> 1].p[0][(it & 1) * 4 + r]);
-            return x * row4(s.tab, kind, 16 * it + 4 * lg);
+            return x;
         };
         __syncthreads();   // E, dR, dY are done with; gam and eh are there
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {   // now M1, M2, M3 become dq, A, F
-            const f32x4 gam = row4(s.gam, 0, 16 * it + 4 * lg);
-            M1[it] *= gam;
-            M2[it] *= -gam;
-            M3[it] *= row4(s.eh, 0, 16 * it + 4 * lg);
-            row_dots(s.red[3][w], it, lg, l16, value(kf, it, 3), M3[it]);
-        }
+        for (int zx = 0; zx < 2; ++zx) {   // U and V
+            const int jt = zx ? xcol : zcol, j = 16 * jt + l16;
+            const float Ghj = s.tab[j], Glj = s.tab[64 + j];
 #pragma unroll
-        for (int zx = 0; zx < 2; ++zx) {
-            if (zx) __syncthreads();   // Z's operands are done with
-#pragma unroll
-            for (int n = 0; n < NZ; ++n) {   // with their decays, as operands
-                const int t = zx ? 9 - (w + n * W) : w + n * W;
-                if (w + n * W >= 10) continue;
-                const int it = tile_row(t), jt = t - tile_id(it, 0), j = 16 * jt + l16, i0 = 16 * it + 4 * lg;
-                const float Ghj = s.tab[j], Glj = s.tab[64 + j], cj = s.tab[2 * 64 + j] * s.tab[3 * 64 + j];   // beta rk
-                const f32x4 gh = row4(s.tab, 0, i0), gl = row4(s.tab, 1, i0);
+            for (int it = 0; it < 4; ++it) {
+                if (!mine(it, jt)) continue;
+                const int i0 = 16 * it + 4 * lg;
+                const f32x4 gh = row4(s.tab, 0, i0), gl = row4(s.tab, 1, i0), f = row4(s.tab, zx ? 3 : 4, i0);
                 f32x4 x;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj));
-                    x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -X[n][r] : Z[n][r]) : 0.f;
-                    // row i, k = j
-                    put1<T, P>(s.u.w[0], tri_at<T, false>(t, (l16 >> 2) * 16 + 4 * lg + r) + (l16 & 3), x[r] * cj);
+                    const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj)) * f[r];
+                    x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -Z[1][it / kHalf][r] : Z[0][it / kHalf][r]) : 0.f;
                 }
-                put<T, P>(s.u.w[1], tri_at<T, true>(t, lane), x * row4(s.tab, zx ? 3 : 4, i0));   // row j, k = i
-            }
-            __syncthreads();
+                Quad q[P];
+                split_quad<T, P>(x, q);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                f32x4 &m = zx ? M2[it] : M1[it];
-#pragma unroll
-                for (int ks = 0; ks <= it / 2; ++ks) m = mma(m, load_tri<T, P, false>(s.u.w[0], it, ks, lane), kf[ks]);
-#pragma unroll
-                for (int ks = it / 2; ks < 2; ++ks)
-                    M3[it] = mma(M3[it], load_tri<T, P, true>(s.u.w[1], it, ks, lane), zx ? kf[ks] : qf[ks]);
+                for (int p = 0; p < P; ++p)
+                    *reinterpret_cast<Quad *>(s.u.w[zx] + p * kTri16 + tile_id(it, jt) * 256 + l16 * 16 + 4 * lg) = q[p];
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        // M1, M2, M3 become dq rq, A rk, F
+        f32x4 ck[4];
+        float end = 0.f;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-            const f32x4 kv = value(kf, it, 3);
-            row_dots(s.red[0][w], it, lg, l16, value(qf, it, 4), M1[it]);
-            row_dots(s.red[1][w], it, lg, l16, kv, M2[it]);
-            row_dots(s.red[2][w], it, lg, l16, kv, M3[it]);
-            M2[it] += row4(s.tab, 2, 16 * it + 4 * lg) * M3[it];
+            const int i0 = 16 * it + 4 * lg;
+            const f32x4 gam = row4(s.gam, 0, i0), be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0);
+            M1[it] *= gam * row4(s.tab, 4, i0);
+            M2[it] *= -gam * rk;
+            M3[it] *= row4(s.eh, 0, i0);
+            ck[it] = value(kf, it) * (be * rk);
+            const f32x4 e = ck[it] * M3[it];
+            end += (e[0] + e[1]) + (e[2] + e[3]);
+        }
+        const Frag<T, P> cf[2] = {make_frag<T, P>(ck[0], ck[1]), make_frag<T, P>(ck[2], ck[3])};
+        end = wave_sum(fmaf(ip, __builtin_amdgcn_exp2f(s.tab[63]), end));
+        if (lane == 0) s.ip[w] = end;
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks <= it / 2; ++ks) {
+                M1[it] = mma(M1[it], tri_rows<T, P>(s.u.w[0], it, ks, lg, l16), cf[ks]);
+                M2[it] = mma(M2[it], tri_rows<T, P>(s.u.w[1], it, ks, lg, l16), cf[ks]);
+            }
+#pragma unroll
+            for (int ks = it / 2; ks < 2; ++ks) {
+                M3[it] = mma(M3[it], tri_cols<T, P>(s.u.w[0], it, ks, lg, l16), qf[ks]);
+                M3[it] = mma(M3[it], tri_cols<T, P>(s.u.w[1], it, ks, lg, l16), kf[ks]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int i0 = 16 * it + 4 * lg;
+            const f32x4 be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0), rq = row4(s.tab, 4, i0);
+            const f32x4 kv = value(kf, it), qd = value(qf, it) * M1[it];   // q rq . M1 / rq
+            f32x4 kF = kv * rk * M3[it];
+            const f32x4 kA = kv * M2[it];
+            row_sums(s.red[0][w], it, lg, l16, a.norm ? kA : qd + kA - be * kF);
+            row_sums(s.red[1][w], it, lg, l16, kF);
+            if (a.norm) row_sums(s.red[2][w], it, lg, l16, qd);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                M1[it][r] *= __builtin_amdgcn_rcpf(rq[r]);
+                M2[it][r] *= __builtin_amdgcn_rcpf(rk[r]);
+            }
+            M2[it] += be * M3[it];
             if constexpr (kShared) {
                 dq[it] += M1[it];
                 dk[it] += M2[it];
@@ -269,20 +376,18 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
         }
         __syncthreads();
         if (w == 0) {
-            float x[4];
+            float x[3];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 3; ++i) {
                 x[i] = 0.f;
 #pragma unroll
-                for (int n = 0; n < W; ++n) x[i] += s.red[i][n][lane];
+                for (int n = 0; n < W; ++n) x[i] += i == 2 && !a.norm ? 0.f : s.red[i][n][lane];
             }
             const float be = s.tab[2 * 64 + lane];
-            double dG = (double)x[0] + x[1] - (double)be * x[2];
-            double end = wave_sum((double)be * x[3]), sd = 0.;
+            double dG = a.norm ? (double)x[0] + x[2] - (double)be * x[1] : x[0], last = 0.;
 #pragma unroll
-            for (int n = 0; n < W; ++n) sd += s.ip[n];
-            end += (double)__builtin_amdgcn_exp2f(s.tab[63]) * sd;
-            if (lane == 63) dG += end;
+            for (int n = 0; n < W; ++n) last += s.ip[n];
+            if (lane == 63) dG += last;
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) {
                 const double dn = __shfl_down(dG, d);
@@ -291,35 +396,47 @@ __global__ void __launch_bounds__(4 * K, 2) gdr_grads_kernel(GradArgs<T> a)
             if (lane < c.len) {
                 const int64_t o = (c.tok + lane) * a.Hv + hv;
                 a.dg[o] = (float)dG;
-                a.dbeta[o] = x[2];
+                a.dbeta[o] = x[1];
             }
-            s.tq[lane] += x[0];
-            s.tk[lane] += x[1] + be * x[2];
+            s.tq[lane] += x[2];
+            s.tk[lane] += x[0] + be * x[1];
         }
     }
-    if (a.norm) __syncthreads();
-    // with q = n scale and n = x rq / scale: dx = rq (dq - q (q . dq) / scale^2)
+    __syncthreads();
+    const int ln = (int)fresh(lane), lg = ln >> 4, l16 = ln & 15;
+    // with q = n scale and n = x rq / scale: dx = rq (dq - q (q . dq) / scale^2),
+    // each value in the place of the q or k that it needs, then out by whole rows
+    const float is = 1.f / a.scale;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int t0 = 16 * it + 4 * lg;
         const f32x4 rq = row4(s.tab, 4, t0), rk = row4(s.tab, 3, t0);
         f32x4 x = dq[it] * rq, z = dk[it] * rk;
-        if (a.norm) {
-            const f32x4 nq = rq / a.scale, tq = row4(s.tq, 0, t0), tk = row4(s.tk, 0, t0);   // nq = 1 / |q|
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int b = (16 * w + l16) * (int)sizeof(T);
-                x[r] -= nq[r] * nq[r] * to_f32(*reinterpret_cast<const T *>(s.q + Sw::at(t0 + r, b))) * tq[r];
-                z[r] -= rk[r] * rk[r] * to_f32(*reinterpret_cast<const T *>(s.k + Sw::at(t0 + r, b))) * tk[r];
-            }
-        }
+        f32x4 nq = rq * is, nk = rk;   // 1 / |q|, 1 / |k|
+        nq *= nq * row4(s.tq, 0, t0);
+        nk *= nk * row4(s.tk, 0, t0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (t0 + r >= c.len) continue;
-            const int64_t o = ((c.tok + t0 + r) * a.Hk + hk) * K + 16 * w + l16;
-            a.dq[o] = (T)x[r];
-            a.dk[o] = (T)z[r];
+            const int o = Sw::at(t0 + r, (16 * w + l16) * (int)sizeof(T));
+            T *qs = reinterpret_cast<T *>(s.q + o), *ks = reinterpret_cast<T *>(s.k + o);
+            if (a.norm) {
+                x[r] -= nq[r] * to_f32(*qs);
+                z[r] -= nk[r] * to_f32(*ks);
+            }
+            *qs = (T)x[r];
+            *ks = (T)z[r];
         }
+    }
+    __syncthreads();
+    T *dqb = a.dq + (c.tok * a.Hk + hk) * K, *dkb = a.dk + (c.tok * a.Hk + hk) * K;
+    constexpr int kRow = K * (int)sizeof(T) / 16;   // 16-byte pieces of a row
+#pragma unroll
+    for (int n = 0; n < 64 * kRow / (64 * W); ++n) {
+        const int i = tid + n * 64 * W, t = i / kRow, b = i % kRow * 16;
+        if (t >= c.len) continue;
+        const uint32_t o = (uint32_t)t * (uint32_t)(a.Hk * K) + b / sizeof(T);
+        *reinterpret_cast<f32x4 *>(dqb + o) = *reinterpret_cast<const f32x4 *>(s.q + Sw::at(t, b));
+        *reinterpret_cast<f32x4 *>(dkb + o) = *reinterpret_cast<const f32x4 *>(s.k + Sw::at(t, b));
     }
 }
 
