@@ -16,12 +16,21 @@
 //
 // One workgroup per chunk and key head; it adds up the group's value heads in
 // registers.  Each of its K / 16 waves owns 16 key columns: it reads its rows
-// of S and D once from memory as operands.  E, dR, dY pass through LDS 32
+// of S and D once from memory as operands.  E, dR, dY pass through LDS K / 2
 // values at a time; then one copy each of the C x C arrays
 //     U_ij = rq_i Gamma_ij Z_ij,   V_ij = -rk_i Gamma_ij X_ij
-// (rq, rk: what q, k as passed are multiplied by), which serves by rows for F
-// and, through transposing reads, by columns for dq and A, whose other operand
-// is k_j beta_j rk_j and whose rows are divided by rq_i, rk_i again.
+// (rq, rk: what q, k as passed are multiplied by), which serves by rows for dq
+// and A and by columns for F.  By rows it meets k_j beta_j rk_j, and the sums
+// are divided by rq_i, rk_i again (__builtin_amdgcn_rcpf, within one step of
+// float); by columns it meets q and k as passed, exact in bf16.
+//
+// Measured, bf16: 8 x 4096 x 32, K = V = 64: 0.53 ms for 1.7 GB (3.2 TB/s);
+// 4 x 4096 x 8 / 16 heads, K = V = 128: 0.42 ms for 0.9 GB.  The time goes to
+// turns of loading, LDS and products that at three and one workgroups to a
+// compute unit overlap only in part.  Loading the next block, or the next
+// head's first, before the products did not help (443, 470 against 433 us at
+// K = 128), values 64 at a time did (421 us: whole 256-byte rows of S and D),
+// two workgroups instead of three at K = 64 took 640 against 619 us.
 
 #include "gdr_factor.h"
 
@@ -120,12 +129,12 @@ __device__ __forceinline__ Frag<T, P> tri_cols(const T *base, int jt, int ks, in
 
 template <typename T, int K>
 struct GradLds {
-    static constexpr int P = Num<T>::kPlanes, W = K / 16;
+    static constexpr int P = Num<T>::kPlanes, W = K / 16, kBlocks = K / 64;   // blocks of values at a time
     char k[Swizzled<T, K>::kBytes], q[Swizzled<T, K>::kBytes];
     union {
         struct {
             T dy[64 * kVB], dr[P * 64 * kVB], e[P * 64 * kVB];
-        } in;
+        } in[kBlocks];
         T w[2][P * kTri16];   // U, V
     } u;
     float tab[kTableFloats], gam[64], eh[64];
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
     using L = GradLds<T, K>;
     using Quad = typename Num<T>::Quad;
     using Sw = Swizzled<T, K>;
-    constexpr int P = L::P, W = L::W;
+    constexpr int P = L::P, W = L::W, NB = L::kBlocks;
     __shared__ __align__(16) char buf[sizeof(L)];
     L &s = *reinterpret_cast<L *>(buf);
     // the heads of a chunk together on one of the 8 dies, as in gdr_prep.hip: dg
@@ -165,7 +174,6 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
     // column tile w % 4 of Z and 3 - w % 4 of X is this wave's, five tiles; of
     // eight waves, two have every other row tile
     constexpr int kHalf = W / 4;
-    constexpr bool kAhead = W == 8;   // loads of the next block before this one's products
     const int zcol = w & 3, xcol = 3 - zcol;
     auto mine = [&](int it, int jt) { return it >= jt && (kHalf == 1 || ((it ^ w ^ (w >> 2)) & 1) == 0); };
 
@@ -190,89 +198,91 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
         const float *Sb = a.S + ch * K * a.V, *Db = a.D + ch * K * a.V, *Rb = a.dR + ch * 64 * a.V, *Eb = a.E + ch * 64 * a.V;
         const T *yb = a.dy + (c.tok * a.Hv + hv) * a.V;
         const uint32_t ys = (uint32_t)(a.Hv * a.V);
-        f32x4 x[2], d[2], rq[8 / W], eq[8 / W];
-        Quad yq[8 / W];
-        auto fetch = [&](uint32_t v0) {
-            const uint32_t tid = fresh(threadIdx.x), lg = tid >> 4 & 3, l16 = tid & 15;   // addresses formed anew, not kept
-            // V is a multiple of 16: the second half of the block may be beyond it
-            const uint32_t so = (uint32_t)(16 * w + l16) * V + v0 + 4 * lg;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                x[h] = d[h] = zero4();
-                if (v0 + 16 * h < V) {
-                    x[h] = *reinterpret_cast<const f32x4 *>(Sb + so + 16 * h);
-                    d[h] = *reinterpret_cast<const f32x4 *>(Db + so + 16 * h);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < 8 / W; ++n) {
-                const uint32_t t = (tid + n * 64 * W) >> 3, v = v0 + 4 * (tid & 7);
-                yq[n] = Quad{};
-                rq[n] = eq[n] = zero4();
-                if (v < V) {
-                    if ((int)t < c.len) yq[n] = *reinterpret_cast<const Quad *>(yb + t * ys + v);
-                    rq[n] = *reinterpret_cast<const f32x4 *>(Rb + t * V + v);
-                    eq[n] = *reinterpret_cast<const f32x4 *>(Eb + t * V + v);
-                }
-            }
-        };
-        if constexpr (kAhead) fetch(0);
         const f32x4 tv = reinterpret_cast<const f32x4 *>(a.table + ch * kTableFloats)[tid < kTableFloats / 4 ? tid : 0];
         if (gi > 0) __syncthreads();   // the table of the head before is done with
-        for (uint32_t v0 = 0; v0 < V; v0 += kVB) {
-            if constexpr (!kAhead) fetch(v0);
-            const int ft = (int)fresh(tid), lane = ft & 63, lg = lane >> 4, l16 = lane & 15;
+        for (uint32_t v0 = 0; v0 < V; v0 += NB * kVB) {
+            // addresses formed anew, not kept
+            const uint32_t ft = fresh((uint32_t)tid), lg = ft >> 4 & 3, l16 = ft & 15;
+            // V is a multiple of 16: halves of the last block may be beyond it
+            f32x4 x[NB][2], d[NB][2], rq[NB][8 / W], eq[NB][8 / W];
+            Quad yq[NB][8 / W];
+#pragma unroll
+            for (int h = 0; h < 2 * NB; ++h) {
+                const uint32_t so = (uint32_t)(16 * w + l16) * V + v0 + 4 * lg + 16 * h;
+                f32x4 &xh = x[h >> 1][h & 1], &dh = d[h >> 1][h & 1];
+                xh = dh = zero4();
+                if (v0 + 16 * h < V) {
+                    xh = *reinterpret_cast<const f32x4 *>(Sb + so);
+                    dh = *reinterpret_cast<const f32x4 *>(Db + so);
+                }
+            }
+            // NB = 2: 16 lanes to a row of both blocks
+#pragma unroll
+            for (int n = 0; n < NB * 8 / W; ++n) {
+                const uint32_t t = (ft + n * 64 * W) / (8 * NB), v = v0 + 4 * (ft % (8 * NB));
+                Quad &yn = yq[n / (8 / W)][n % (8 / W)];
+                f32x4 &rn = rq[n / (8 / W)][n % (8 / W)], &en = eq[n / (8 / W)][n % (8 / W)];
+                yn = Quad{};
+                rn = en = zero4();
+                if (v < V) {
+                    if ((int)t < c.len) yn = *reinterpret_cast<const Quad *>(yb + t * ys + v);
+                    rn = *reinterpret_cast<const f32x4 *>(Rb + t * V + v);
+                    en = *reinterpret_cast<const f32x4 *>(Eb + t * V + v);
+                }
+            }
             if (v0 > 0)
-                __syncthreads();   // the block before is done with
+                __syncthreads();   // the blocks before are done with
             else if (tid < kTableFloats / 4)
                 reinterpret_cast<f32x4 *>(s.tab)[tid] = tv;
 #pragma unroll
-            for (int n = 0; n < 8 / W; ++n) {
-                const int to = in_row<T>((ft + n * 64 * W) >> 3, 4 * (ft & 7));
+            for (int n = 0; n < NB * 8 / W; ++n) {
+                const int to = in_row<T>((ft + n * 64 * W) / (8 * NB), 4 * (ft & 7));
+                auto &in = s.u.in[NB == 1 ? 0 : ft >> 3 & 1];
                 Quad rz[P], ez[P];
-                split_quad<T, P>(rq[n], rz);
-                split_quad<T, P>(eq[n], ez);
-                *reinterpret_cast<Quad *>(s.u.in.dy + to) = yq[n];
+                split_quad<T, P>(rq[n / (8 / W)][n % (8 / W)], rz);
+                split_quad<T, P>(eq[n / (8 / W)][n % (8 / W)], ez);
+                *reinterpret_cast<Quad *>(in.dy + to) = yq[n / (8 / W)][n % (8 / W)];
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    *reinterpret_cast<Quad *>(s.u.in.dr + p * 64 * kVB + to) = rz[p];
-                    *reinterpret_cast<Quad *>(s.u.in.e + p * 64 * kVB + to) = ez[p];
+                    *reinterpret_cast<Quad *>(in.dr + p * 64 * kVB + to) = rz[p];
+                    *reinterpret_cast<Quad *>(in.e + p * 64 * kVB + to) = ez[p];
                 }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 xd = x[h] * d[h];
-                ip += (xd[0] + xd[1]) + (xd[2] + xd[3]);
-            }
-            const Frag<T, P> Sf = make_frag<T, P>(x[0], x[1]), Df = make_frag<T, P>(d[0], d[1]);
-            if constexpr (kAhead) {
-                if (v0 + kVB < V) fetch(v0 + kVB);
             }
             if (v0 == 0 && gi == 0) wait_dma();   // of k, q, older than the block's loads
             __syncthreads();
-            // one array of rows after the other: registers for few operands at a time
-            {
-                const Frag<T, P> E = load_in<T, P>(s.u.in.e, zcol, lg, l16);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag<T, 1> y = load_in<T, 1>(s.u.in.dy, it, lg, l16);
-                    M1[it] = mma(M1[it], y, Sf);
-                    if (mine(it, zcol)) Z[0][it / kHalf] = mma(Z[0][it / kHalf], y, E);
+            for (int b = 0; b < NB; ++b) {
+                const auto &in = s.u.in[b];
+                f32x4 xd = x[b][0] * d[b][0];
+                xd += x[b][1] * d[b][1];
+                ip += (xd[0] + xd[1]) + (xd[2] + xd[3]);
+                // one array of rows after the other: registers for few operands at a time
+                const Frag<T, P> Sf = make_frag<T, P>(x[b][0], x[b][1]);
+                {
+                    const Frag<T, P> E = load_in<T, P>(in.e, zcol, lg, l16);
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const Frag<T, 1> y = load_in<T, 1>(in.dy, it, lg, l16);
+                        M1[it] = mma(M1[it], y, Sf);
+                        if (mine(it, zcol)) Z[0][it / kHalf] = mma(Z[0][it / kHalf], y, E);
+                    }
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            {
-                const Frag<T, P> E = load_in<T, P>(s.u.in.e, xcol, lg, l16);
+                __builtin_amdgcn_sched_barrier(0);
+                {
+                    const Frag<T, P> E = load_in<T, P>(in.e, xcol, lg, l16);
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag<T, P> r = load_in<T, P>(s.u.in.dr, it, lg, l16);
-                    M2[it] = mma(M2[it], r, Sf);
-                    if (mine(it, xcol)) Z[1][it / kHalf] = mma(Z[1][it / kHalf], r, E);
+                    for (int it = 0; it < 4; ++it) {
+                        const Frag<T, P> r = load_in<T, P>(in.dr, it, lg, l16);
+                        M2[it] = mma(M2[it], r, Sf);
+                        if (mine(it, xcol)) Z[1][it / kHalf] = mma(Z[1][it / kHalf], r, E);
+                    }
                 }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
+                const Frag<T, P> Df = make_frag<T, P>(d[b][0], d[b][1]);
 #pragma unroll
-            for (int it = 0; it < 4; ++it) M3[it] = mma(M3[it], load_in<T, P>(s.u.in.e, it, lg, l16), Df);
+                for (int it = 0; it < 4; ++it) M3[it] = mma(M3[it], load_in<T, P>(in.e, it, lg, l16), Df);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         const int ln = (int)fresh(lane), lg = ln >> 4, l16 = ln & 15;
         if (tid < 64) {
