@@ -35,8 +35,9 @@
  *
  * Numbers.  State, sums and the products inside a chunk are fp32 (fp32
  * inputs), or, with bf16 inputs, products of bf16 parts that carry a value's
- * leading 24 bits, with fp32 sums.  y and the gradients of q, k, v are rounded once, to the
- * inputs' type.  Results are the same bit for bit from run to run.
+ * leading 24 bits (16 bits for what only y, itself bf16, is made of), with
+ * fp32 sums.  y and the gradients of q, k, v are rounded once, to the inputs'
+ * type.  Results are the same bit for bit from run to run.
  *
  * Sizes.  At most 65535 sequences and value heads, and 2^22 chunks of 64
  * tokens times value heads (WKV7_ERR_UNSUPPORTED beyond).
@@ -82,9 +83,10 @@ typedef struct {
 size_t gdr_checkpoint_bytes(const gdr_shape *shape);
 
 /* Bytes of device workspace gdr_forward and gdr_backward need (the chunks'
- * triangular factors and decay tables; for the backward also the chunks'
- * state gradients and, with ckpt_provided 0, the record).  0 when the shape
- * is invalid or empty. */
+ * triangular factors where a kernel of their own makes them, decay tables,
+ * and for few, long rows the transitions of their segments; for the backward
+ * also the chunks' state gradients and, with ckpt_provided 0, the record).
+ * 0 when the shape is invalid or empty, or needs none. */
 size_t gdr_forward_workspace_bytes(const gdr_shape *shape);
 size_t gdr_backward_workspace_bytes(const gdr_shape *shape, int ckpt_provided);
 

@@ -60,10 +60,6 @@ struct Num<bf16> {
 template <typename T>
 constexpr int kYParts = sizeof(T) == 4 ? 1 : 2;
 
-// LDS row padding: 16 bytes, so that 16 rows' 16-byte reads meet all banks.
-template <typename T>
-constexpr int kPad = 16 / (int)sizeof(T);
-
 // The stored position of k inside its 32-deep step.
 __device__ __forceinline__ int kpos(int k)
 {
@@ -153,19 +149,6 @@ __device__ __forceinline__ Frag<T, P> make_frag(f32x4 lo, f32x4 hi)
 #pragma unroll
         for (int p = 0; p < P; ++p) __builtin_memcpy(&f.p[p], u[p], 16);
     }
-    return f;
-}
-
-// A lane's 8 values of step ks of LDS row `row` (row stride ld, planes
-// `plane` elements apart).
-template <typename T, int P>
-__device__ __forceinline__ Frag<T, P> load_frag(const T *base, int row, int ld, int ks, int lg, int plane)
-{
-    Frag<T, P> f;
-    const T *a = base + row * ld + ks * 32 + lg * 8;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-        f.p[i] = *reinterpret_cast<const typename Num<T>::Oct *>(a + i * plane);
     return f;
 }
 

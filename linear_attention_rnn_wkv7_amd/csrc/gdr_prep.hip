@@ -1,7 +1,9 @@
 // The triangular factors (gdr_factor.h) of every chunk and value head in
 // memory, for the scans that do not make them themselves.  One wave per chunk
 // and head, four to a workgroup: nothing waits at a barrier.  Bound by what it
-// writes: 26 KB (bf16) per chunk and head against 16 or 32 KB read.
+// writes: 26 KB (bf16) per chunk and head against 16 or 32 KB read.  Measured:
+// 6144 chunks and heads, K = 128, bf16: 78 us, 4.6 TB/s; 16384, K = 64, fp32:
+// 214 us, 4 TB/s.
 
 #include "gdr_factor.h"
 

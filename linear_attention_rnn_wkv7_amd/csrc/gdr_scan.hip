@@ -19,7 +19,15 @@
 // M S0 + L; a first pass runs every segment from a zero state, and beside it
 // K columns that start as the identity and see no values, which gives the
 // segment's L and M; a small kernel runs through the segments of a row; the
-// second pass starts each from its own state.  (Reverse the same way.)
+// second pass starts each from its own state.  (Reverse the same way.)  At 1 x
+// 65536 x 32, K = V = 64, bf16, in 8 segments: 0.40 and 0.43 ms for the passes
+// and 0.03 between (the whole call 2.84 ms in one piece, 1.19 in segments).
+//
+// What bounds them.  fp32: the fp32 matrix instruction (8 x 4096 x 32, K = V =
+// 64: 37 GFLOP in 0.39 ms, 95 TFLOP/s of 157).  bf16: the chain of one chunk,
+// about 1100 instructions of one wave at K = 64 and one such wave per SIMD (the
+// same shape: 0.31 ms a direction, 64 steps of 4.9 us); at K = 128 twice as
+// many, on half of the SIMDs where there are 64 heads (4 x 4096 x 16: 0.31 ms).
 
 #include "gdr_factor.h"
 
