@@ -72,7 +72,7 @@ typedef struct {
     int64_t nseq;   /* packed sequences, or 0 */
     int32_t dtype;  /* wkv7_dtype of q, k, v, y, dy, dq, dk, dv */
     int32_t flags;  /* 0 or GDR_NORM_QK */
-    float scale;    /* finite, not zero */
+    float scale;    /* a normal number: finite, not zero, not denormal */
 } gdr_shape;
 
 /* Bytes of the record that gdr_forward leaves for gdr_backward: for each
@@ -100,7 +100,8 @@ int gdr_forward(const gdr_shape *shape, const void *q, const void *k, const void
 
 /* Backward.  dy required; dsT NULL = zeros; ckpt: the record a gdr_forward
  * with the same inputs wrote, or NULL to recompute it into the workspace (s0
- * is read only then).  dq, dk, dv, dg, dbeta required; ds0 may be NULL. */
+ * is read only then).  dq, dk, dv, dg, dbeta required; ds0 may be NULL.  No
+ * output may overlap an input or another output. */
 int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const void *v, const float *g,
                  const float *beta, const float *s0, const int32_t *seq_starts, const void *dy,
                  const float *dsT, const float *ckpt, void *dq, void *dk, void *dv, float *dg,
@@ -112,7 +113,8 @@ int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const voi
  * slots [B] int32 device array: the state of each row, or NULL for row b =
  * state b (pool >= B).  A row whose slot is outside [0, pool), or which an
  * earlier row names too, is skipped: its y is not written, and the state it
- * names is written by the earlier row alone.  shape->nseq must be 0. */
+ * names is written by the earlier row alone.  shape->nseq must be 0.  y may
+ * not overlap an input. */
 int gdr_decode(const gdr_shape *shape, const void *q, const void *k, const void *v, const float *g,
                const float *beta, float *state, int64_t pool, const int32_t *slots, void *y,
                hipStream_t stream);
@@ -122,7 +124,8 @@ int gdr_decode(const gdr_shape *shape, const void *q, const void *k, const void 
  * y, gate, z, dz, dy, dgate [rows][H][N] of `dtype`, w and dw [Hw][N] fp32
  * with Hw = 1 (one weight for all heads) or H.  N is a power of two from 16
  * to 256.  The backward sums dw in a fixed order through a workspace of
- * gdr_epilogue_workspace_bytes bytes, 256-byte aligned. */
+ * gdr_epilogue_workspace_bytes bytes, 256-byte aligned.  No output may overlap
+ * an input. */
 typedef struct {
     int64_t rows;   /* tokens, >= 0 */
     int64_t H;      /* heads, >= 0 */

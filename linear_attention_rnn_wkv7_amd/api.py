@@ -409,7 +409,7 @@ def _gdr_dims(q, k, v, g, beta, seq_starts, scale, norm_qk):
         if B != 1 or nseq < 1:
             raise ValueError("seq_starts needs B = 1 and at least two entries")
         _check_like("seq_starts", seq_starts, (nseq + 1,), torch.int32, at)
-    return (B, T, Hk, Hv, K, V, dt, nseq, bool(norm_qk), scale), ys, (nseq or B, Hv, V, K), at
+    return (B, T, Hk, Hv, K, V, dt, nseq, bool(norm_qk), None if scale is None else float(scale)), ys, (nseq or B, Hv, V, K), at
 
 
 def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_qk=False, want_y=True,
@@ -424,7 +424,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_
 
     seq_starts (int32, on the device) packs sequences end to end into B = 1:
     sequence s is tokens seq_starts[s] .. seq_starts[s + 1] - 1.  Rows of y
-    outside every sequence are not written.
+    outside every sequence are not written.  No output may overlap an input.
 
     ckpt is the record gdr_backward consumes.  ``out`` may supply (y, sT,
     ckpt) tensors (None entries are allocated when wanted)."""
@@ -524,7 +524,7 @@ def _gdr_epilogue_dims(y, gate, w, eps):
     _check_like("y", y, ys, dt, at)
     _check_like("gate", gate, ys, dt, at)
     _check_like("w", w, (Hw, N), torch.float32, at)
-    return _epilogue_sizes(B * T, H, N, Hw, _VEC_DTYPES[dt], 0, eps), ys, at
+    return _epilogue_sizes(B * T, H, N, Hw, _VEC_DTYPES[dt], 0, float(eps)), ys, at
 
 
 def gdr_epilogue_forward(y, gate, w, *, eps=1e-6, stream=None, out=None):
@@ -575,7 +575,7 @@ def _norm_dims(x, eps):
     D = x.shape[-1]
     if D == 0:
         raise ValueError("the residual stream has rows of no entries")
-    return _norm_sizes(x.numel() // D, D, _VEC_DTYPES[x.dtype], 0, eps), D, x.get_device()
+    return _norm_sizes(x.numel() // D, D, _VEC_DTYPES[x.dtype], 0, float(eps)), D, x.get_device()
 
 
 def residual_norm_forward(x, y, w, scale=None, *, eps=1e-6, want_x_out=True, stream=None, out=None):

@@ -62,7 +62,7 @@ int check(const gdr_shape *s, Dims *d)
         return WKV7_ERR_INVALID;
     if (s->dtype != WKV7_F32 && s->dtype != WKV7_BF16) return WKV7_ERR_INVALID;
     if ((s->flags & ~GDR_NORM_QK) != 0) return WKV7_ERR_INVALID;
-    if (!isfinite(s->scale) || s->scale == 0.f) return WKV7_ERR_INVALID;
+    if (!std::isnormal(s->scale)) return WKV7_ERR_INVALID;
     if (s->Hk == 0 ? s->Hv != 0 : s->Hv % s->Hk != 0) return WKV7_ERR_INVALID;
     if (s->nseq > 0 && (s->B != 1 || s->T > INT32_MAX)) return WKV7_ERR_INVALID;
     if ((s->K != 64 && s->K != 128) || s->V % 16 != 0 || s->V > 256) return WKV7_ERR_UNSUPPORTED;

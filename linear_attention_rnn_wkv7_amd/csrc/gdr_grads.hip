@@ -20,9 +20,9 @@
 // values at a time; then one copy each of the C x C arrays
 //     U_ij = rq_i Gamma_ij Z_ij,   V_ij = -rk_i Gamma_ij X_ij
 // (rq, rk: what q, k as passed are multiplied by), which serves by rows for dq
-// and A and by columns for F.  By rows it meets k_j beta_j rk_j, and the sums
-// are divided by rq_i, rk_i again (__builtin_amdgcn_rcpf, within one step of
-// float); by columns it meets q and k as passed, exact in bf16.
+// and A, times rq_i and rk_i as the gradients of what was passed want them, and
+// by columns for F.  By rows it meets k_j beta_j rk_j, by columns q and k as
+// passed, exact in bf16.
 //
 // Measured, bf16: 8 x 4096 x 32, K = V = 64: 0.53 ms for 1.7 GB (3.2 TB/s);
 // 4 x 4096 x 8 / 16 heads, K = V = 128: 0.42 ms for 0.9 GB.  The time goes to
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        // M1, M2, M3 become dq rq, A rk, F
+        // M1, M2, M3 become rq dq, rk A, F
         f32x4 ck[4];
         float end = 0.f;
 #pragma unroll
@@ -363,19 +363,14 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const int i0 = 16 * it + 4 * lg;
-            const f32x4 be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0), rq = row4(s.tab, 4, i0);
-            const f32x4 kv = value(kf, it), qd = value(qf, it) * M1[it];   // q rq . M1 / rq
+            const f32x4 be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0);
+            const f32x4 kv = value(kf, it), qd = value(qf, it) * M1[it];   // q rq . dq
             f32x4 kF = kv * rk * M3[it];
             const f32x4 kA = kv * M2[it];
             row_sums(s.red[0][w], it, lg, l16, a.norm ? kA : qd + kA - be * kF);
             row_sums(s.red[1][w], it, lg, l16, kF);
             if (a.norm) row_sums(s.red[2][w], it, lg, l16, qd);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                M1[it][r] *= __builtin_amdgcn_rcpf(rq[r]);
-                M2[it][r] *= __builtin_amdgcn_rcpf(rk[r]);
-            }
-            M2[it] += be * M3[it];
+            M2[it] += be * rk * M3[it];
             if constexpr (kShared) {
                 dq[it] += M1[it];
                 dk[it] += M2[it];
@@ -414,14 +409,14 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
     }
     __syncthreads();
     const int ln = (int)fresh(lane), lg = ln >> 4, l16 = ln & 15;
-    // with q = n scale and n = x rq / scale: dx = rq (dq - q (q . dq) / scale^2),
+    // with q = n scale and n = x rq / scale: dx = rq dq - x (rq / scale)^2 (q . dq),
     // each value in the place of the q or k that it needs, then out by whole rows
     const float is = 1.f / a.scale;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int t0 = 16 * it + 4 * lg;
         const f32x4 rq = row4(s.tab, 4, t0), rk = row4(s.tab, 3, t0);
-        f32x4 x = dq[it] * rq, z = dk[it] * rk;
+        f32x4 x = dq[it], z = dk[it];
         f32x4 nq = rq * is, nk = rk;   // 1 / |q|, 1 / |k|
         nq *= nq * row4(s.tq, 0, t0);
         nk *= nk * row4(s.tk, 0, t0);

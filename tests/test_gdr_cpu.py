@@ -319,3 +319,19 @@ def test_binding_refuses_host_tensors():
         api.residual_norm_forward(x, x, torch.ones(64))
     with pytest.raises(ValueError):
         api.gdr_decode(x, x, x, g, g, torch.zeros(1, 2, 64, 64))
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(scale=1e-40), INVALID), (dict(scale=-1e-45), INVALID),     # denormal
+    (dict(B=128, T=64 * 1024, Hk=33, Hv=33), UNSUPPORTED),           # 2^17 chunks x 33 heads
+    (dict(B=1, T=64 * 65536, Hk=1, Hv=65, nseq=1), UNSUPPORTED)])    # 65537 slots x 65 heads
+def test_rule_refuses_more_shapes(change, want):
+    test_rule_refuses_shapes(change, want)
+
+
+def test_rule_sizes_of_the_largest():
+    """2^22 chunks times heads, and one fewer chunk's worth of heads than refused above."""
+    sh = _rule_shape(B=128, T=64 * 1024, Hk=32, Hv=32, K=128, V=256)
+    per = 128 * 1024 * 32
+    assert _lib.lib().gdr_checkpoint_bytes(ctypes.byref(sh)) == per * 4 * (128 * 256 + 64 * 256)
+    assert _lib.lib().gdr_backward_workspace_bytes(ctypes.byref(sh), 0) > 2 * per * 4 * (128 * 256 + 64 * 256)

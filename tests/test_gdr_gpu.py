@@ -293,6 +293,110 @@ def test_rule_offsets_beyond_32_bits():
     assert torch.equal(a["sT"][-1], b["sT"][0])
 
 
+# B, T, Hk, Hv, K, V, dtype, norm, s0, dsT, record
+MANY = [
+    (4, 130, 16, 32, 64, 64, BF16, True, True, True, True),     # 128 heads of 64 and more: the scans
+    (8, 64, 16, 16, 64, 16, BF16, False, True, True, False),    # make their triangular factors themselves
+    (3, 199, 15, 45, 64, 48, BF16, True, False, True, True),
+    (2, 1, 64, 64, 64, 32, BF16, False, True, True, True),
+    (4, 130, 16, 32, 64, 80, BF16, True, True, True, True),     # and not: wider values
+    (11, 70, 3, 27, 128, 96, BF16, True, True, False, True),    # more workgroups than compute units
+    (2, 90, 5, 10, 128, 256, F32, False, True, True, True),     # 16 slabs of 20 heads
+    (17, 66, 1, 1, 64, 256, BF16, True, True, True, True),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=["-".join(map(str, c)).replace("torch.", "") for c in MANY])
+def test_rule_many_heads(case):
+    test_rule(case)
+
+
+@pytest.mark.parametrize("starts", PACKED[:4], ids=[str(i) for i in range(4)])
+def test_rule_packed_many_heads(starts):
+    """As test_rule_packed, with the factors made by the scans' workgroups."""
+    T, H = starts[-1] + 9, 128
+    d = inputs(1, T, 32, H, 64, 32, BF16, starts=starts, norm=True)
+    for n in IN + ("dy",):
+        d[n][:, :starts[0]] = float("nan")
+        d[n][:, starts[-1]:] = float("nan")
+    got = run(d, starts=starts, norm=True)
+    inside = slice(starts[0], starts[-1])
+    for n in ("y",) + tuple("d" + m for m in IN):   # what is outside is not written
+        got[n] = got[n][:, inside]
+    want = reference(d, starts=starts, norm=True)
+    want = {n: w if n in ("sT", "ds0") else w[:, inside] for n, w in want.items()}
+    check(got, want, f"many {starts}")
+
+
+def test_rule_extreme_gates_many_heads():
+    """test_rule_extreme_gates' gates and keys, in 128 heads."""
+    d = inputs(1, 150, 128, 128, 64, 16, BF16, norm=True)
+    g, be = d["g"], d["beta"]
+    g[:, 10:30:4] = -float("inf")
+    g[:, 70, 0] = -1e30
+    g[:, 71, 0] = -200.0
+    g[:, 90:128, 1] = 0.0
+    be[:, 20:40] = 0.0
+    be[:, 90:110] = 1.0
+    d["k"][:, 80:128] = d["k"][:, 80:81]
+    d["k"][:, 5] = 0
+    d["q"][:, 6] = 0
+    check(run(d, norm=True), reference(d, norm=True), "gates, many")
+
+
+def test_rule_heads_do_not_leak():
+    """inf and NaN in one head stay in it."""
+    d = inputs(1, 100, 128, 128, 64, 64, BF16)
+    clean = run(d)
+    for n, x in (("v", float("inf")), ("q", float("nan")), ("dy", float("inf")), ("g", float("nan"))):
+        d[n][:, 40, 77] = x
+    got = run(d)
+    for n in ("y",) + tuple("d" + m for m in IN):
+        for part in (slice(0, 77), slice(78, 128)):
+            assert torch.equal(got[n][:, :, part], clean[n][:, :, part]), n
+
+
+def test_rule_scale_tensor_changed_in_place():
+    """A scale given as a tensor is read at every call."""
+    d = inputs(1, 20, 1, 1, 64, 16, F32)
+    a, s = [d[n] for n in IN], torch.tensor(0.5)
+    y0 = api.gdr_forward(*a, scale=s)[0]
+    s.fill_(1.0)
+    assert torch.equal(api.gdr_forward(*a, scale=s)[0], 2 * y0)
+
+
+def test_rule_two_calls_at_once():
+    """Calls on two streams with nothing between them, again and again."""
+    d = [inputs(4, 150, 16, 32, 64, 64, BF16, seed=3), inputs(2, 200, 2, 4, 128, 64, F32, seed=4)]
+    want = [run(x) for x in d]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in d]
+    got = [[run(x, stream=s) for _ in range(3)] for x, s in zip(d, streams)]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for one in g:
+            for n in w:
+                assert torch.equal(one[n], w[n]), n
+
+
+def test_rule_many_heads_captured():
+    """A captured forward and backward whose workgroups make the factors."""
+    d = inputs(4, 100, 16, 32, 64, 64, BF16, seed=9)
+    want, g = run(d), torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        got = run(d)
+    for _ in range(3):
+        for x in got.values():
+            x.zero_()
+        g.replay()
+        eager = run(d)
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(got[n], want[n]) and torch.equal(eager[n], want[n]), n
+
+
 # ---------------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("B,T,Hk,Hv,K,V,dt,norm", [
