@@ -20,8 +20,9 @@
 // K columns that start as the identity and see no values, which gives the
 // segment's L and M; a small kernel runs through the segments of a row; the
 // second pass starts each from its own state.  (Reverse the same way.)  At 1 x
-// 65536 x 32, K = V = 64, bf16, in 8 segments: 0.40 and 0.43 ms for the passes
-// and 0.03 between (the whole call 2.84 ms in one piece, 1.19 in segments).
+// 65536 x 32, K = V = 64, bf16, in 8 segments: 0.39 ms for each of the passes
+// and 0.03 between (the whole call 2.84 ms in one piece, 1.19 in segments when
+// they came).
 //
 // What bounds them.  fp32: the fp32 matrix instruction (8 x 4096 x 32, K = V =
 // 64: 37 GFLOP in 0.39 ms, 95 TFLOP/s of 157).  bf16: the chain of one chunk,
@@ -150,6 +151,14 @@ __device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
     for (int i = 0; i < Q; ++i) g.p[i] = f.p[i];
     return g;
 }
+
+// When a slab loads its next chunk's values: with K = 64 after the products of
+// the state, when the step's operand copies are through (1 x 65536 x 32, bf16,
+// passes of 402 and 432 us -> 387 and 388; 8 x 4096 x 32 with the record 308 ->
+// 286); with K = 128 at the step's start, ahead of the stores of the state
+// (4 x 4096 x 16 with the record: 300 us, 312 after the products).
+template <int K>
+constexpr bool kFetchFirst = K == 128;
 
 // The waves of a workgroup run in steps, one chunk of the slabs to a step,
 // with a barrier between two steps: the slabs take chunk c in step c (the c-th
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
             f32x4 R[4], Y[4];
 #pragma unroll
             for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = Cols<T>::value(vn[i]);
-            if (c + 1 < nc) fetch(c + 1);
+            if (kFetchFirst<K> && c + 1 < nc) fetch(c + 1);
             if (!kMap && a.st) {
                 const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
@@ -358,6 +367,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
                 for (int ks = 0; ks <= it / 2; ++ks)
                     E[it] = mma(E[it], load_tri<T, P, false>(f.t, it, ks, lane), Rf[ks]);
             }
+            if (!kFetchFirst<K> && c + 1 < nc) fetch(c + 1);
             if (!kMap && a.rows) {
                 const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
 #pragma unroll
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
             f32x4 dY[4];
 #pragma unroll
             for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = Cols<T>::value(yn[j]);
-            if (c > 0) fetch(c - 1);
+            if (kFetchFirst<K> && c > 0) fetch(c - 1);
             if constexpr (!kMap) {
                 const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
 #pragma unroll
@@ -483,6 +493,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
                         dE[jt] = mma(dE[jt], load_tri<T, P, true>(f.p, jt, ks, lane), dYf[ks]);
                 }
             }
+            if (!kFetchFirst<K> && c > 0) fetch(c - 1);
             f32x4 dR[4];
             {
                 const Frag<T, P> dEf[2] = {make_frag<T, P>(dE[0], dE[1]), make_frag<T, P>(dE[2], dE[3])};
