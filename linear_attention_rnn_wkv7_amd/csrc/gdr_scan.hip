@@ -27,7 +27,7 @@
 // What bounds them.  fp32: the fp32 matrix instruction (8 x 4096 x 32, K = V =
 // 64: 37 GFLOP in 0.39 ms, 95 TFLOP/s of 157).  bf16: the chain of one chunk,
 // about 1100 instructions of one wave at K = 64 and one such wave per SIMD (the
-// same shape: 0.31 ms a direction, 64 steps of 4.9 us); at K = 128 twice as
+// same shape: 0.30 and 0.33 ms, 64 steps of about 5 us); at K = 128 twice as
 // many, on half of the SIMDs where there are 64 heads (4 x 4096 x 16: 0.31 ms).
 
 #include "gdr_factor.h"
