@@ -76,7 +76,7 @@ typedef struct {
 } gdr_shape;
 
 /* Bytes of the record that gdr_forward leaves for gdr_backward: for each
- * chunk of 64 tokens and value head, the state before it ([K][V] fp32) and
+ * chunk of 64 tokens and value head, the state before it ([V][K] fp32) and
  * the chunk's 64 correction rows ([64][V] fp32).  The chunks are those of
  * the rows, B ceil(T / 64), or, packed, at most floor(T / 64) + nseq.
  * 0 when the shape is invalid or empty. */

@@ -25,11 +25,11 @@
 // passed, exact in bf16.
 //
 // Measured, bf16: 8 x 4096 x 32, K = V = 64: 0.53 ms for 1.7 GB (3.2 TB/s);
-// 4 x 4096 x 8 / 16 heads, K = V = 128: 0.42 ms for 0.9 GB.  The time goes to
+// 4 x 4096 x 8 / 16 heads, K = V = 128: 0.41 ms for 0.9 GB.  The time goes to
 // turns of loading, LDS and products that at three and one workgroups to a
 // compute unit overlap only in part.  Loading the next block, or the next
 // head's first, before the products did not help (443, 470 against 433 us at
-// K = 128), values 64 at a time did (421 us: whole 256-byte rows of S and D),
+// K = 128), values 64 at a time did (421 us), and S and D by [V][K] (413 mean),
 // two workgroups instead of three at K = 64 took 640 against 619 us.
 
 #include "gdr_factor.h"
@@ -208,12 +208,15 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
             Quad yq[NB][8 / W];
 #pragma unroll
             for (int h = 0; h < 2 * NB; ++h) {
-                const uint32_t so = (uint32_t)(16 * w + l16) * V + v0 + 4 * lg + 16 * h;
+                const uint32_t so = (v0 + 16 * h + 4 * lg) * K + 16 * w + l16;
                 f32x4 &xh = x[h >> 1][h & 1], &dh = d[h >> 1][h & 1];
                 xh = dh = zero4();
                 if (v0 + 16 * h < V) {
-                    xh = *reinterpret_cast<const f32x4 *>(Sb + so);
-                    dh = *reinterpret_cast<const f32x4 *>(Db + so);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        xh[j] = Sb[so + j * K];
+                        dh[j] = Db[so + j * K];
+                    }
                 }
             }
             // NB = 2: 16 lanes to a row of both blocks

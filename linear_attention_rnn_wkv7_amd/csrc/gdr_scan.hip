@@ -28,7 +28,8 @@
 // 64: 37 GFLOP in 0.39 ms, 95 TFLOP/s of 157).  bf16: the chain of one chunk,
 // about 1100 instructions of one wave at K = 64 and one such wave per SIMD (the
 // same shape: 0.30 and 0.33 ms, 64 steps of about 5 us); at K = 128 twice as
-// many, on half of the SIMDs where there are 64 heads (4 x 4096 x 16: 0.31 ms).
+// many, on half of the SIMDs where there are 64 heads (4 x 4096 x 16: 0.29 and
+// 0.31 ms).
 
 #include "gdr_factor.h"
 
@@ -150,6 +151,17 @@ __device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
 #pragma unroll
     for (int i = 0; i < Q; ++i) g.p[i] = f.p[i];
     return g;
+}
+
+// The slab into a [V][K] matrix: four rows of a tile are 16 bytes of it.  (By
+// single values, [K][V], the 32 stores of K = 128 took 2700 of a step's 11000
+// cycles.)
+template <int KT>
+__device__ __forceinline__ void record_state(float *to, const f32x4 (&S)[KT], int64_t col, int lg)
+{
+    const uint32_t o = fresh((uint32_t)col * (16 * KT) + 4 * lg);
+#pragma unroll
+    for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(to + o + 16 * i) = S[i];
 }
 
 // When a slab loads its next chunk's values: with K = 64 after the products of
@@ -337,9 +349,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
             for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = Cols<T>::value(vn[i]);
             if (kFetchFirst<K> && c + 1 < nc) fetch(c + 1);
             if (!kMap && a.st) {
-                const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
-#pragma unroll
-                for (int i = 0; i < KT; ++i) st.store(i, S[i]);
+                record_state<KT>(a.st + at.ch * K * a.V, S, col, lg);
             }
             {   // K S and Q S
                 f32x4 acc[4];
@@ -470,9 +480,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
             for (int j = 0; j < 16; ++j) dY[j >> 2][j & 3] = Cols<T>::value(yn[j]);
             if (kFetchFirst<K> && c > 0) fetch(c - 1);
             if constexpr (!kMap) {
-                const Tiles st(a.st + at.ch * K * a.V, K, a.V, col, lg);
-#pragma unroll
-                for (int j = 0; j < KT; ++j) st.store(j, D[j]);
+                record_state<KT>(a.st + at.ch * K * a.V, D, col, lg);
             }
             f32x4 dE[4];
 #pragma unroll
