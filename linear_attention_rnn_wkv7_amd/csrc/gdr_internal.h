@@ -61,7 +61,7 @@ struct Launch {
     const float *dsT = nullptr;
     void *dq = nullptr, *dk = nullptr, *dv = nullptr;
     float *dg = nullptr, *dbeta = nullptr, *ds0 = nullptr;
-    float *ws_ds = nullptr, *ws_dr = nullptr;   // [slots][Hv][K][V], [slots][Hv][64][V]
+    float *ws_ds = nullptr, *ws_dr = nullptr;   // [slots][Hv][V][K], [slots][Hv][64][V]
     float *table = nullptr;                     // [slots][Hv][5][64]
     void *factors = nullptr;                    // [slots][Hv][factor_bytes], or null
     // segments: how each takes its state on, and the states they start from
