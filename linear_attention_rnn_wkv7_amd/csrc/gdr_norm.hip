@@ -14,7 +14,8 @@
 // Measured, bf16: epilogue at 8 x 4096 x 32 heads of 64: forward 82 us for 403
 // MB (4.9 TB/s), backward 130 us for 671 MB (5.2) and 16 us for the sums;
 // residual norm at 32768 rows of 2048: forward 96 us for 537 MB (5.6 TB/s),
-// backward with scale 172 us for 805 MB (4.7) and 2 x 7 us.
+// backward with scale 172 us for 805 MB (4.7) and 2 x 7 us.  bf16 rows whose
+// length is no multiple of 8 go by 2 bytes a lane: 1.3 to 2.4 TB/s.
 
 #include "gdr_device.h"
 
@@ -235,6 +236,46 @@ __device__ __forceinline__ void put8(T *row, int i, int t, int D, f32x8 x)
     }
 }
 
+// Such a piece as it lies in memory: half the registers for bf16 (backward with
+// scale, 2^26 values in rows of 1024: 271 -> 225 us, 4096: 236 -> 195, 16384: 403
+// -> 245; of 2048, where there were enough: 176 -> 182).  again() hides that the
+// values have been widened before, or the compiler would keep them wide.
+template <typename T, bool kVec>
+struct Piece {
+    f32x8 x;
+    template <int NT>
+    __device__ __forceinline__ void get(const T *row, int i, int t, int D) { x = get8<T, NT, kVec>(row, i, t, D); }
+    __device__ __forceinline__ void clear() { x = zero8(); }
+    __device__ __forceinline__ f32x8 wide() const { return x; }
+    __device__ __forceinline__ void again() {}
+};
+template <>
+struct Piece<bf16, true> {
+    uint32_t u[4];
+    template <int NT>
+    __device__ __forceinline__ void get(const bf16 *row, int i, int t, int D)
+    {
+        clear();
+        if (elem<NT, true>(i, 0, t) < D) __builtin_memcpy(u, row + elem<NT, true>(i, 0, t), 16);
+    }
+    __device__ __forceinline__ void clear() { u[0] = u[1] = u[2] = u[3] = 0; }
+    __device__ __forceinline__ f32x8 wide() const
+    {
+        f32x8 x;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            x[2 * n] = bf16_lo(u[n]);
+            x[2 * n + 1] = bf16_hi(u[n]);
+        }
+        return x;
+    }
+    __device__ __forceinline__ void again()
+    {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) asm("" : "+v"(u[n]));
+    }
+};
+
 // Sums of a and b over the row's NT threads.  `turn` alternates from call to
 // call, so that one barrier per call is enough.
 template <int NT>
@@ -296,41 +337,55 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT) norm_bwd_kernel(NormArgs<
 {
     constexpr int RB = NT < 256 ? 256 / NT : 1;
     __shared__ float red[2][2][16];
+    // the longest rows read w and scale again for every row, from the cache:
+    // 1024 threads have 128 registers each (4096 rows of 16384: bf16 245 -> 229
+    // us, fp32 506 -> 449)
+    constexpr bool kHold = !(NT == 1024 && kN == 2 && kScale);
     const int t = threadIdx.x % NT, grp = threadIdx.x / NT;
     f32x8 w[kN], sc[kN], dw[kN], ds[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-        w[i] = get8<float, NT, kVec>(a.w, i, t, a.D);
-        if (kScale) sc[i] = get8<float, NT, kVec>(a.scale, i, t, a.D);
+        if (kHold) w[i] = get8<float, NT, kVec>(a.w, i, t, a.D);
+        if (kHold && kScale) sc[i] = get8<float, NT, kVec>(a.scale, i, t, a.D);
         dw[i] = ds[i] = zero8();
     }
+    auto weight = [&](int i) { return kHold ? w[i] : get8<float, NT, kVec>(a.w, i, t, a.D); };
     const int64_t first = (int64_t)blockIdx.x * a.per;
     const int64_t end = first + a.per < a.rows ? first + a.per : a.rows;
     int turn = 0;
     for (int64_t row = first + grp; row < end; row += RB, turn ^= 1) {
         const int64_t o = row * a.D;
-        f32x8 x[kN], dh[kN], d[kN], y[kN];
+        Piece<T, kVec> xp[kN], hp[kN], dp[kN], yp[kN];
         float ss = 0.f, sm = 0.f;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            x[i] = get8<T, NT, kVec>(a.x + o, i, t, a.D);
-            dh[i] = get8<T, NT, kVec>(a.dh + o, i, t, a.D);
-            d[i] = a.dxo ? get8<T, NT, kVec>(a.dxo + o, i, t, a.D) : zero8();
-            if (kScale) y[i] = get8<T, NT, kVec>(a.y + o, i, t, a.D);
-            ss += sum8(x[i] * x[i]);
-            sm += sum8(dh[i] * w[i] * x[i]);
+            xp[i].template get<NT>(a.x + o, i, t, a.D);
+            hp[i].template get<NT>(a.dh + o, i, t, a.D);
+            if (a.dxo)
+                dp[i].template get<NT>(a.dxo + o, i, t, a.D);
+            else
+                dp[i].clear();
+            if (kScale) yp[i].template get<NT>(a.y + o, i, t, a.D);
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const f32x8 x = xp[i].wide();
+            ss += sum8(x * x);
+            sm += sum8(hp[i].wide() * weight(i) * x);
+            xp[i].again();
+            hp[i].again();
         }
         row_sums<NT>(ss, sm, red, turn);
         const float r = 1.f / sqrtf(ss / a.D + a.eps), m = sm / a.D * r;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-            const f32x8 xn = x[i] * r;
-            dw[i] += dh[i] * xn;
-            const f32x8 dx = d[i] + r * (dh[i] * w[i] - xn * m);
+            const f32x8 xn = xp[i].wide() * r, dh = hp[i].wide();
+            dw[i] += dh * xn;
+            const f32x8 dx = dp[i].wide() + r * (dh * weight(i) - xn * m);
             put8<T, NT, kVec>(a.dx + o, i, t, a.D, dx);
             if (kScale) {
-                put8<T, NT, kVec>(a.dy + o, i, t, a.D, dx * sc[i]);
-                ds[i] += dx * y[i];
+                put8<T, NT, kVec>(a.dy + o, i, t, a.D, dx * (kHold ? sc[i] : get8<float, NT, kVec>(a.scale, i, t, a.D)));
+                ds[i] += dx * yp[i].wide();
             }
         }
     }

@@ -542,6 +542,12 @@ def test_residual_norm(rows, D, scaled, dt):
                dscale=float((term * y.cpu().double()).abs().sum(0).norm())))
 
 
+@pytest.mark.parametrize("rows,D,scaled,dt", [
+    (2100, 8200, True, BF16), (1030, 16384, True, F32), (2050, 4096, True, BF16), (1100, 8192, False, BF16)])
+def test_residual_norm_more_rows_than_workgroups(rows, D, scaled, dt):
+    test_residual_norm(rows, D, scaled, dt)
+
+
 def test_residual_norm_captured_and_empty():
     x, y = (torch.randn(70, 300, device="cuda") for _ in range(2))
     w, s = (torch.randn(300, device="cuda") for _ in range(2))
