@@ -35,8 +35,7 @@
  *
  * Numbers.  State, sums and the products inside a chunk are fp32 (fp32
  * inputs), or, with bf16 inputs, products of bf16 parts that carry a value's
- * leading 24 bits (16 bits for what only y, itself bf16, is made of), with
- * fp32 sums.  y and the gradients of q, k, v are rounded once, to the inputs'
+ * leading 24 bits, with fp32 sums.  y and the gradients of q, k, v are rounded once, to the inputs'
  * type.  Results are the same bit for bit from run to run.
  *
  * Sizes.  At most 65535 sequences and value heads, and 2^22 chunks of 64

@@ -23,7 +23,11 @@
 // fp32 inputs use the fp32 matrix instruction (8 per 32-deep step).  With
 // bf16 inputs, q, k, v, dy are exact operands, and every fp32 operand is
 // carried as kParts bf16 parts x = x0 + x1 + .. (each the rounding of what
-// is left), of whose products those above 2^-8 kParts are formed.
+// is left), of whose products those above 2^-8 kParts are formed.  That holds
+// for what y alone is made of too: y is the difference of large terms where a
+// token reads a key that has been written again, and two parts, 2^-16 of each
+// term, would then be worse than y's own rounding (a state 4096 times as large
+// as the value in its place: 15 half steps of bf16 and more).
 #pragma once
 
 #include "gdr_internal.h"
@@ -55,11 +59,6 @@ struct Num<bf16> {
     using Oct = bf16x8;
 };
 
-// Parts of P and of the operands of y: y is rounded to T, so that with bf16
-// two parts (2^-16 of each term) are 2^-8 of that rounding.
-template <typename T>
-constexpr int kYParts = sizeof(T) == 4 ? 1 : 2;
-
 // The stored position of k inside its 32-deep step.
 __device__ __forceinline__ int kpos(int k)
 {
@@ -74,18 +73,18 @@ struct Frag {
 
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
 
-// kLim: products of parts i + j >= kLim are left out.
-template <int kLim = kParts, int PA, int PB>
+// Products of parts i + j >= kParts are left out.
+template <int PA, int PB>
 __device__ __forceinline__ f32x4 mma(f32x4 c, const Frag<bf16, PA> &a, const Frag<bf16, PB> &b)
 {
 #pragma unroll
     for (int i = PA - 1; i >= 0; --i)
 #pragma unroll
         for (int j = PB - 1; j >= 0; --j)
-            if (i + j < kLim) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
+            if (i + j < kParts) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.p[i], b.p[j], c, 0, 0, 0);
     return c;
 }
-template <int kLim = kParts, int PA, int PB>
+template <int PA, int PB>
 __device__ __forceinline__ f32x4 mma(f32x4 c, const Frag<float, PA> &a, const Frag<float, PB> &b)
 {
 #pragma unroll

@@ -75,11 +75,11 @@ __device__ __forceinline__ Frag<T, P> load_tri(const T *base, int it, int ks, in
 // beta_i, and gamma_C.
 constexpr int kWeights = 256;
 
-// A chunk's factors as the scan reads them, T in the parts of an fp32 operand,
-// P in PP parts (1 KB copies move it whole).
-template <typename T, int PP>
+// A chunk's factors as the scan reads them, T and P in the parts of an fp32
+// operand (1 KB copies move it whole).
+template <typename T>
 struct Factor {
-    T t[Num<T>::kPlanes * kTri], p[PP * kTri];
+    T t[Num<T>::kPlanes * kTri], p[Num<T>::kPlanes * kTri];
     float w[kWeights];
 };
 
@@ -329,11 +329,10 @@ struct Factors {
 
     // T and P (kTrans: their transposes) and the weights to where the scan
     // reads them
-    template <int PP>
     __device__ __forceinline__ void finish(T *t, T *p, float *weights, int lane)
     {
         write_tri<T, Num<T>::kPlanes, kTrans>(t, kk, lane);
-        write_tri<T, PP, kTrans>(p, qk, lane);
+        write_tri<T, Num<T>::kPlanes, kTrans>(p, qk, lane);
         weights[lane] = wa;
         weights[64 + lane] = wb;
         weights[128 + lane] = we;

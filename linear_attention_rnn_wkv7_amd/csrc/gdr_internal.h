@@ -43,7 +43,7 @@ inline bool scan_makes_factors(int dtype, int64_t K, int64_t V, int64_t units)
 {
     return dtype == WKV7_BF16 && K == 64 && V <= 64 && units >= 128;
 }
-// Bytes of a chunk's factors in memory.
+// Bytes of a chunk's factors in memory, for the forward or (transposed) the reverse scan.
 size_t factor_bytes(int dtype, bool transposed);
 
 struct Launch {

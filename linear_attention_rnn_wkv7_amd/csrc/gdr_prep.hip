@@ -26,7 +26,6 @@ struct PrepArgs {
 template <typename T, int K, bool kTrans>
 __global__ void __launch_bounds__(256, 2) gdr_prep_kernel(PrepArgs<T> a)
 {
-    constexpr int PP = kTrans ? Num<T>::kPlanes : kYParts<T>;
     __shared__ __align__(16) FactorLds lds[4];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     // Workgroups go round the 8 dies; those of one die take the heads of one
@@ -38,12 +37,12 @@ __global__ void __launch_bounds__(256, 2) gdr_prep_kernel(PrepArgs<T> a)
     const Chunk c = locate(a.map, slot);
     if (c.len == 0) return;
     const int64_t o = (c.tok * a.Hk + hk) * K, og = c.tok * a.Hv + hv;
-    Factor<T, PP> &to = reinterpret_cast<Factor<T, PP> *>(a.factors)[ch];
+    Factor<T> &to = reinterpret_cast<Factor<T> *>(a.factors)[ch];
     Factors<T, K, kTrans> f;
     f.products(lds[w], a.k + o, a.q + o, a.g + og, a.beta + og, a.Hk, a.Hv, c.len, a.norm, a.scale, lane);
     f.decays(lds[w], kTrans ? a.table + ch * kTableFloats : nullptr, c.len, lane);
     f.solve(lds[w], lane);
-    f.template finish<PP>(to.t, to.p, to.w, lane);
+    f.finish(to.t, to.p, to.w, lane);
 }
 
 template <typename T, int K>
@@ -72,10 +71,9 @@ hipError_t launch_t(const Launch &a, bool transposed, hipStream_t stream)
 
 }  // namespace
 
-size_t factor_bytes(int dtype, bool transposed)
+size_t factor_bytes(int dtype, bool)
 {
-    if (dtype == WKV7_F32) return sizeof(Factor<float, 1>);
-    return transposed ? sizeof(Factor<bf16, kParts>) : sizeof(Factor<bf16, kYParts<bf16>>);
+    return dtype == WKV7_F32 ? sizeof(Factor<float>) : sizeof(Factor<bf16>);
 }
 
 hipError_t launch_prep(const Launch &a, bool transposed, hipStream_t stream)

@@ -132,26 +132,17 @@ __device__ __forceinline__ Pos chunk_at(int64_t lo, int64_t hi, int64_t slot0, i
 // written, and the scratch of the waves that write them.  Else: two sets of
 // all, or one where two do not fit (fp32 with K = 128).
 constexpr int kMakers = 4;
-template <typename T, int K, int PP>
+template <typename T, int K>
 struct ScanLds {
     static constexpr int kMat = Swizzled<T, K>::kBytes;
-    static constexpr int kSets = 2 * (2 * kMat + (int)sizeof(Factor<T, PP>)) <= 160 * 1024 ? 2 : 1;
+    static constexpr int kSets = 2 * (2 * kMat + (int)sizeof(Factor<T>)) <= 160 * 1024 ? 2 : 1;
     char k[kSets][kMat], q[kSets][kMat];
-    Factor<T, PP> f[kSets];
+    Factor<T> f[kSets];
 };
-template <typename T, int K, int PP>
-struct MakeLds : ScanLds<T, K, PP> {
+template <typename T, int K>
+struct MakeLds : ScanLds<T, K> {
     FactorLds scratch[kMakers];
 };
-
-template <typename T, int P, int Q>
-__device__ __forceinline__ Frag<T, Q> first_parts(const Frag<T, P> &f)
-{
-    Frag<T, Q> g;
-#pragma unroll
-    for (int i = 0; i < Q; ++i) g.p[i] = f.p[i];
-    return g;
-}
 
 // The slab into a [V][K] matrix: four rows of a tile are 16 bytes of it.  (By
 // single values, [K][V], the 32 stores of K = 128 took 2700 of a step's 11000
@@ -178,12 +169,12 @@ constexpr bool kFetchFirst = K == 128;
 
 // One wave copies them from memory (kAll: with Q and P): issuing copies stalls whenever the memory
 // system has no room for more, and would stall the products with it.
-template <typename T, int K, int PP, bool kTrans, bool kAll>
-__device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K, PP> &s, int64_t lo, int64_t hi, int64_t slot0,
+template <typename T, int K, bool kTrans, bool kAll>
+__device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K> &s, int64_t lo, int64_t hi, int64_t slot0,
                                           int64_t hv, int64_t hk, int64_t nc, int lane)
 {
-    using L = ScanLds<T, K, PP>;
-    using F = Factor<T, PP>;
+    using L = ScanLds<T, K>;
+    using F = Factor<T>;
     __builtin_amdgcn_s_setprio(2);
     for (int64_t i = 0; i < nc; ++i) {
         const Pos at = chunk_at(lo, hi, slot0, kTrans ? nc - 1 - i : i, a.Hv, hv);
@@ -208,11 +199,11 @@ __device__ __forceinline__ void copy_loop(const ScanArgs<T> &a, ScanLds<T, K, PP
 // chunk c in steps c - kMakers to c - 1, a stage to a step, and writes them in
 // the last.  The wave in its first stage, which waits for memory in any case,
 // also copies K and Q for the next step.
-template <typename T, int K, int PP, bool kTrans>
-__device__ __forceinline__ void make_loop(const ScanArgs<T> &a, MakeLds<T, K, PP> &s, int maker, bool tables, int64_t lo,
+template <typename T, int K, bool kTrans>
+__device__ __forceinline__ void make_loop(const ScanArgs<T> &a, MakeLds<T, K> &s, int maker, bool tables, int64_t lo,
                                           int64_t hi, int64_t slot0, int64_t hv, int64_t hk, int64_t nc, int lane)
 {
-    static_assert(MakeLds<T, K, PP>::kSets == 2, "two sets");
+    static_assert(MakeLds<T, K>::kSets == 2, "two sets");
     int64_t steps = nc + kMakers - 1;   // barriers still to come
     auto next = [&]() {
         if (steps > 0) __syncthreads();
@@ -243,27 +234,27 @@ __device__ __forceinline__ void make_loop(const ScanArgs<T> &a, MakeLds<T, K, PP
         next();
         if (made) f.solve(s.scratch[maker], (int)fresh(lane));
         next();
-        Factor<T, PP> &to = s.f[i & 1];
-        if (made) f.template finish<PP>(to.t, to.p, to.w, (int)fresh(lane));
+        Factor<T> &to = s.f[i & 1];
+        if (made) f.finish(to.t, to.p, to.w, (int)fresh(lane));
         next();
     }
 }
 
 // The waves besides the slabs': returns false in a slab's wave.
-template <typename T, int K, int PP, bool kTrans, bool kMake, bool kAll>
+template <typename T, int K, bool kTrans, bool kMake, bool kAll>
 __device__ __forceinline__ bool feed(const ScanArgs<T> &a, char *buf, int wave, int slabs, bool tables, int64_t lo,
                                      int64_t hi, int64_t slot0, int64_t hv, int64_t hk, int64_t nc, int lane)
 {
     if constexpr (kMake) {
         if (wave >= slabs) {
             if (nc > 0)
-                make_loop<T, K, PP, kTrans>(a, *reinterpret_cast<MakeLds<T, K, PP> *>(buf), wave - slabs, tables, lo, hi,
+                make_loop<T, K, kTrans>(a, *reinterpret_cast<MakeLds<T, K> *>(buf), wave - slabs, tables, lo, hi,
                                             slot0, hv, hk, nc, lane);
             return true;
         }
     } else {
         if (wave == slabs) {
-            copy_loop<T, K, PP, kTrans, kAll>(a, *reinterpret_cast<ScanLds<T, K, PP> *>(buf), lo, hi, slot0, hv, hk, nc, lane);
+            copy_loop<T, K, kTrans, kAll>(a, *reinterpret_cast<ScanLds<T, K> *>(buf), lo, hi, slot0, hv, hk, nc, lane);
             return true;
         }
     }
@@ -285,8 +276,8 @@ __device__ __forceinline__ void step_end()
     __syncthreads();
 }
 
-template <typename T, int K, int PP, bool kMake>
-constexpr int kScanLds = kMake ? (int)sizeof(MakeLds<T, K, PP>) : (int)sizeof(ScanLds<T, K, PP>);
+template <typename T, int K, bool kMake>
+constexpr int kScanLds = kMake ? (int)sizeof(MakeLds<T, K>) : (int)sizeof(ScanLds<T, K>);
 // The most waves: 8 slabs and the copies, or 4 slabs and the makers.
 template <bool kMake>
 constexpr int kMaxThreads = 64 * (kMake ? 4 + kMakers : 8 + 1);
@@ -295,11 +286,11 @@ constexpr int kMaxThreads = 64 * (kMake ? 4 + kMakers : 8 + 1);
 template <typename T, int K, bool kMake, bool kY, bool kMap>
 __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T> a)
 {
-    constexpr int P = Num<T>::kPlanes, PY = kYParts<T>;
+    constexpr int P = Num<T>::kPlanes;
     constexpr int KT = K / 16, KS = K / 32;
-    using L = ScanLds<T, K, PY>;
+    using L = ScanLds<T, K>;
     using Sw = Swizzled<T, K>;
-    __shared__ __align__(16) char buf[kScanLds<T, K, PY, kMake>];
+    __shared__ __align__(16) char buf[kScanLds<T, K, kMake>];
     L &s = *reinterpret_cast<L *>(buf);
     const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -313,7 +304,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (feed<T, K, PY, false, kMake, kY>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
+    if (feed<T, K, false, kMake, kY>(a, buf, wave, slabs, false, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)part * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)part * slabs + wave) < Vc;
     const bool extra = kMap && 16 * ((int64_t)part * slabs + wave) >= a.V;   // of the identity
@@ -342,7 +333,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
     for (int64_t c = 0; c < nc; ++c) {
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const int set = L::kSets == 2 ? (int)(c & 1) : 0;
-        const Factor<T, PY> &f = s.f[set];
+        const Factor<T> &f = s.f[set];
         if (own) {
             f32x4 R[4], Y[4];
 #pragma unroll
@@ -361,8 +352,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
                         acc[it] = mma(acc[it], Sw::rows(s.k[set], it, ks, lg, l16), Sf);
-                        if constexpr (kY)
-                            Y[it] = mma<PY>(Y[it], Sw::rows(s.q[set], it, ks, lg, l16), first_parts<T, P, PY>(Sf));
+                        if constexpr (kY) Y[it] = mma(Y[it], Sw::rows(s.q[set], it, ks, lg, l16), Sf);
                     }
                 }
 #pragma unroll
@@ -384,14 +374,14 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
                 for (int i = 0; i < 4; ++i) rows.store(i, E[i]);
             }
             if constexpr (kY) {
-                const Frag<T, PY> Ef[2] = {make_frag<T, PY>(E[0], E[1]), make_frag<T, PY>(E[2], E[3])};
+                const Frag<T, P> Ef[2] = {make_frag<T, P>(E[0], E[1]), make_frag<T, P>(E[2], E[3])};
                 const Cols<T> y(a.y + (at.tok * a.Hv + hv) * a.V, a.Hv * a.V, a.V, col, at.len, lg);
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     Y[it] *= row4(f.w, 1, 16 * it + 4 * lg);
 #pragma unroll
                     for (int ks = 0; ks <= it / 2; ++ks)
-                        Y[it] = mma<PY>(Y[it], load_tri<T, PY, false>(f.p, it, ks, lane), Ef[ks]);
+                        Y[it] = mma(Y[it], load_tri<T, P, false>(f.p, it, ks, lane), Ef[ks]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) y.store(4 * it + r, Y[it][r]);
                 }
@@ -427,9 +417,9 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
 {
     constexpr int P = Num<T>::kPlanes;
     constexpr int KT = K / 16, KS = K / 32;
-    using L = ScanLds<T, K, P>;
+    using L = ScanLds<T, K>;
     using Sw = Swizzled<T, K>;
-    __shared__ __align__(16) char buf[kScanLds<T, K, P, kMake>];
+    __shared__ __align__(16) char buf[kScanLds<T, K, kMake>];
     L &s = *reinterpret_cast<L *>(buf);
     const int lane = threadIdx.x & 63, lg = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -443,7 +433,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
     int64_t lo, hi;
     seq_range(a.map, seq, lo, hi);
     const int64_t slot0 = first_slot(a.map, seq, lo), nc = (hi - lo + kChunk - 1) / kChunk;
-    if (feed<T, K, P, true, kMake, true>(a, buf, wave, slabs, part == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
+    if (feed<T, K, true, kMake, true>(a, buf, wave, slabs, part == 0, lo, hi, slot0, hv, hk, nc, lane)) return;
     const int64_t col = 16 * ((int64_t)part * slabs + wave) + l16;
     const bool own = 16 * ((int64_t)part * slabs + wave) < Vc;
     const bool extra = kMap && 16 * ((int64_t)part * slabs + wave) >= a.V;   // of the identity
@@ -473,7 +463,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_reverse_kernel(ScanArg
         const int64_t c = nc - 1 - i;
         const Pos at = chunk_at(lo, hi, slot0, c, a.Hv, hv);
         const int set = L::kSets == 2 ? (int)(i & 1) : 0;
-        const Factor<T, P> &f = s.f[set];
+        const Factor<T> &f = s.f[set];
         if (own) {
             f32x4 dY[4];
 #pragma unroll
