@@ -20,8 +20,8 @@
  *   v, y, dy, dv        [B][T][Hv][V]    dtype per gdr_shape.dtype
  *   g, beta, dg, dbeta  [B][T][Hv]       fp32
  *   states s0, sT, dsT, ds0  [sequences][Hv][V][K]  fp32
- * g is the log decay.  Values of g at or below -200, -inf among them, forget
- * the whole state and have a zero gradient; k should not be longer than
+ * g is the log decay, at most 0.  Values of g at or below -200, -inf among them,
+ * forget the whole state, and their gradient is exactly zero; k should not be longer than
  * sqrt(2 / beta), or the recurrence itself grows.
  *
  * Sequences.  With nseq == 0 the B rows are B sequences of T tokens.  With

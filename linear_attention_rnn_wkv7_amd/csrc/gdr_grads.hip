@@ -8,11 +8,16 @@
 //     A_i  = -gamma_i M2_i - sum_j (beta_j Gamma_ij X_ij) k_j
 //     F_j  = e_j M3_j + sum_i Gamma_ij (Z_ij q_i - X_ij k_i),  e = gamma_C / gamma
 //     dbeta_j = k_j . F_j
-//     dG_i = q_i . dq_i + k_i . A_i - beta_i k_i . F_i   (+ at the chunk's end
-//            sum_j beta_j e_j k_j . M3_j + gamma_C <S, D>),
-// and dg is the reverse cumulative sum of dG.  (Every term that G_i, beta_i
-// enter is a row dot of what dq, dk are made of, so no C x C array besides Z
-// and X is needed.)
+//     dg_t = sum_{i >= t} gamma_i (q_i . M1_i - k_i . M2_i)
+//          + sum_{i >= t > j} beta_j Gamma_ij (Z_ij q_i . k_j - X_ij k_i . k_j)
+//          + sum_{j < t} beta_j e_j k_j . M3_j + gamma_C <S, D>
+// Every term of dg_t has exp(g_t) as a factor.  (The gradients of the sums G,
+// which are row dots of what dq and dk are made of, would give dg by a
+// cumulative sum that needs no C x C array; but the terms without g_t cancel
+// in it only but for their rounding, which at g = -16 is as large as dg.)
+// Sums over i >= t and j < t run over a tile's registers and lanes, then its
+// columns are added up; a wave has whole column tiles of Z and X, or, of eight
+// waves, every other tile of one, which its sums over rows pass through.
 //
 // One workgroup per chunk and key head; it adds up the group's value heads in
 // registers.  Each of its K / 16 waves owns 16 key columns: it reads its rows
@@ -138,8 +143,8 @@ struct GradLds {
         T w[2][P * kTri16];   // U, V
     } u;
     float tab[kTableFloats], gam[64], eh[64];
-    float red[3][W][64];       // of each wave's columns: all of dG's dots, k.F; with norm k.A, k.F, q.dq
-    float ip[W];               // gamma_C <S, D> + sum_j beta_j e_j k_j . M3_j
+    float red[4][W][64];       // of each wave's columns: dg but for ip, k.F; with norm q.dq, k.A
+    float ip[W];               // gamma_C <S, D>
     float tq[64], tk[64];      // over the group: q.dq, k.dk
 };
 
@@ -150,6 +155,28 @@ __device__ __forceinline__ void row_sums(float *red, int it, int lg, int l16, f3
 #pragma unroll
     for (int r = 0; r < 4; ++r) z[r] = group_allreduce<16>(x[r]);
     if (l16 == 0) *reinterpret_cast<f32x4 *>(red + 16 * it + 4 * lg) = z;
+}
+
+// x[r] becomes the sum of x over a tile's rows from 4 lg + r on and `below`,
+// which takes up the whole tile; column by column.
+__device__ __forceinline__ f32x4 sums_from(f32x4 x, float &below, int lg)
+{
+    x[2] += x[3];
+    x[1] += x[2];
+    x[0] += x[1];
+    const float a = __shfl_xor(x[0], 16), ab = x[0] + a, b = __shfl_xor(ab, 32);
+    const float rest = ((lg & 1 ? 0.f : a) + (lg & 2 ? 0.f : b)) + below;
+    below += ab + b;
+    return x + rest;
+}
+// The same over the rows before 4 lg + r, and `above`.
+__device__ __forceinline__ f32x4 sums_before(f32x4 x, float &above, int lg)
+{
+    const f32x4 z = {0.f, x[0], x[0] + x[1], (x[0] + x[1]) + x[2]};
+    const float all = z[3] + x[3], a = __shfl_xor(all, 16), ab = all + a, b = __shfl_xor(ab, 32);
+    const float rest = ((lg & 1 ? a : 0.f) + (lg & 2 ? b : 0.f)) + above;
+    above += ab + b;
+    return z + rest;
 }
 
 // Registers for three workgroups of four waves on a compute unit (LDS holds as
@@ -307,46 +334,64 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
             return x;
         };
         __syncthreads();   // E, dR, dY are done with; gam and eh are there
+        f32x4 dg[4];   // row by row, of this wave's columns
+#pragma unroll
+        for (int it = 0; it < 4; ++it) dg[it] = zero4();
 #pragma unroll
         for (int zx = 0; zx < 2; ++zx) {   // U and V
             const int jt = zx ? xcol : zcol, j = 16 * jt + l16;
-            const float Ghj = s.tab[j], Glj = s.tab[64 + j];
+            const float Ghj = s.tab[j], Glj = s.tab[64 + j], cj = s.tab[2 * 64 + j] * s.tab[3 * 64 + j];
+            float below = 0.f;
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                if (!mine(it, jt)) continue;
-                const int i0 = 16 * it + 4 * lg;
-                const f32x4 gh = row4(s.tab, 0, i0), gl = row4(s.tab, 1, i0), f = row4(s.tab, zx ? 3 : 4, i0);
-                f32x4 x;
+            for (int it = 3; it >= 0; --it) {
+                if (it < jt) continue;
+                f32x4 x = zero4();
+                if (mine(it, jt)) {
+                    const int i0 = 16 * it + 4 * lg;
+                    const f32x4 gh = row4(s.tab, 0, i0), gl = row4(s.tab, 1, i0), f = row4(s.tab, zx ? 3 : 4, i0);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj)) * f[r];
-                    x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -Z[1][it / kHalf][r] : Z[0][it / kHalf][r]) : 0.f;
+                    for (int r = 0; r < 4; ++r) {
+                        const float gd = __builtin_amdgcn_exp2f((gh[r] - Ghj) + (gl[r] - Glj)) * f[r];
+                        x[r] = (zx ? i0 + r > j : i0 + r >= j) ? gd * (zx ? -Z[1][it / kHalf][r] : Z[0][it / kHalf][r]) : 0.f;
+                    }
+                    Quad q[P];
+                    split_quad<T, P>(x, q);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        *reinterpret_cast<Quad *>(s.u.w[zx] + p * kTri16 + tile_id(it, jt) * 256 + l16 * 16 + 4 * lg) = q[p];
+                    f32x4 qk = zero4();   // q . k or k . k, as passed
+#pragma unroll
+                    for (int ks = 0; ks < K / 32; ++ks)
+                        qk = mma(qk, Sw::rows(zx ? s.k : s.q, it, ks, lg, l16), Sw::rows(s.k, jt, ks, lg, l16));
+                    x *= qk * cj;
                 }
-                Quad q[P];
-                split_quad<T, P>(x, q);
+                const f32x4 sum = sums_from(x, below, lg);
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<Quad *>(s.u.w[zx] + p * kTri16 + tile_id(it, jt) * 256 + l16 * 16 + 4 * lg) = q[p];
+                for (int r = 0; r < 4; ++r) dg[it][r] += it > jt || 4 * lg + r > l16 ? sum[r] : 0.f;
             }
         }
         __builtin_amdgcn_sched_barrier(0);
         // M1, M2, M3 become rq dq, rk A, F
         f32x4 ck[4];
-        float end = 0.f;
+        float below = 0.f, above = 0.f;
+#pragma unroll
+        for (int it = 3; it >= 0; --it) {
+            const int i0 = 16 * it + 4 * lg;
+            const f32x4 gam = row4(s.gam, 0, i0);
+            M1[it] *= gam * row4(s.tab, 4, i0);
+            M2[it] *= -gam * row4(s.tab, 3, i0);
+            dg[it] += sums_from(value(qf, it) * M1[it] + value(kf, it) * M2[it], below, lg);
+        }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const int i0 = 16 * it + 4 * lg;
-            const f32x4 gam = row4(s.gam, 0, i0), be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0);
-            M1[it] *= gam * row4(s.tab, 4, i0);
-            M2[it] *= -gam * rk;
             M3[it] *= row4(s.eh, 0, i0);
-            ck[it] = value(kf, it) * (be * rk);
-            const f32x4 e = ck[it] * M3[it];
-            end += (e[0] + e[1]) + (e[2] + e[3]);
+            ck[it] = value(kf, it) * (row4(s.tab, 2, i0) * row4(s.tab, 3, i0));
+            row_sums(s.red[0][w], it, lg, l16, dg[it] + sums_before(ck[it] * M3[it], above, lg));
         }
         const Frag<T, P> cf[2] = {make_frag<T, P>(ck[0], ck[1]), make_frag<T, P>(ck[2], ck[3])};
-        end = wave_sum(fmaf(ip, __builtin_amdgcn_exp2f(s.tab[63]), end));
-        if (lane == 0) s.ip[w] = end;
+        ip = wave_sum(ip * __builtin_amdgcn_exp2f(s.tab[63]));
+        if (lane == 0) s.ip[w] = ip;
         __syncthreads();
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -367,12 +412,12 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
         for (int it = 0; it < 4; ++it) {
             const int i0 = 16 * it + 4 * lg;
             const f32x4 be = row4(s.tab, 2, i0), rk = row4(s.tab, 3, i0);
-            const f32x4 kv = value(kf, it), qd = value(qf, it) * M1[it];   // q rq . dq
-            f32x4 kF = kv * rk * M3[it];
-            const f32x4 kA = kv * M2[it];
-            row_sums(s.red[0][w], it, lg, l16, a.norm ? kA : qd + kA - be * kF);
-            row_sums(s.red[1][w], it, lg, l16, kF);
-            if (a.norm) row_sums(s.red[2][w], it, lg, l16, qd);
+            const f32x4 kv = value(kf, it);
+            row_sums(s.red[1][w], it, lg, l16, kv * rk * M3[it]);
+            if (a.norm) {
+                row_sums(s.red[2][w], it, lg, l16, value(qf, it) * M1[it]);   // q rq . dq
+                row_sums(s.red[3][w], it, lg, l16, kv * M2[it]);
+            }
             M2[it] += be * rk * M3[it];
             if constexpr (kShared) {
                 dq[it] += M1[it];
@@ -384,30 +429,23 @@ __global__ void __launch_bounds__(4 * K, K == 64 && sizeof(T) == 2 && !kShared ?
         }
         __syncthreads();
         if (w == 0) {
-            float x[3];
+            float x[4];
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 x[i] = 0.f;
 #pragma unroll
-                for (int n = 0; n < W; ++n) x[i] += i == 2 && !a.norm ? 0.f : s.red[i][n][lane];
+                for (int n = 0; n < W; ++n) x[i] += i >= 2 && !a.norm ? 0.f : s.red[i][n][lane];
             }
-            const float be = s.tab[2 * 64 + lane];
-            double dG = a.norm ? (double)x[0] + x[2] - (double)be * x[1] : x[0], last = 0.;
+            float all = 0.f;
 #pragma unroll
-            for (int n = 0; n < W; ++n) last += s.ip[n];
-            if (lane == 63) dG += last;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double dn = __shfl_down(dG, d);
-                if (lane + d < 64) dG += dn;
-            }
+            for (int n = 0; n < W; ++n) all += s.ip[n];
             if (lane < c.len) {
                 const int64_t o = (c.tok + lane) * a.Hv + hv;
-                a.dg[o] = (float)dG;
+                a.dg[o] = x[0] + all;
                 a.dbeta[o] = x[1];
             }
             s.tq[lane] += x[2];
-            s.tk[lane] += x[0] + be * x[1];
+            s.tk[lane] += x[3] + s.tab[2 * 64 + lane] * x[1];
         }
     }
     __syncthreads();
