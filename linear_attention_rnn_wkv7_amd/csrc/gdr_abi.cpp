@@ -84,7 +84,7 @@ int check(const gdr_shape *s, Dims *d)
     // tokens and states of the caller's tensors
     if (!mul_ok(s->B, s->T, &x) || !mul_ok(x, s->Hv + 1, &x) || !mul_ok(x, 4 * D, &x)) return WKV7_ERR_INVALID;
     if (!mul_ok(d->seqs * (s->Hv + 1), s->K * s->V * 4, &x)) return WKV7_ERR_INVALID;
-    d->nck = (s->T + wkv7::gdr::kChunk - 1) / wkv7::gdr::kChunk;
+    d->nck = s->T / wkv7::gdr::kChunk + (s->T % wkv7::gdr::kChunk != 0);   // T may be the largest, with B or Hv 0
     if (d->packed)
         d->slots = s->T / wkv7::gdr::kChunk + s->nseq;
     else if (!mul_ok(s->B, d->nck, &d->slots))
