@@ -38,8 +38,11 @@
  * leading 24 bits, with fp32 sums.  y and the gradients of q, k, v are rounded once, to the inputs'
  * type.  Results are the same bit for bit from run to run.
  *
- * Sizes.  At most 65535 sequences and value heads, and 2^22 chunks of 64
- * tokens times value heads (WKV7_ERR_UNSUPPORTED beyond).
+ * Sizes.  At most 65535 sequences and value heads, 2^22 chunks of 64 tokens
+ * (as gdr_checkpoint_bytes counts them) times value heads, and, in the
+ * chunked calls with V above 128, about 3.7 million sequences times value heads,
+ * whose launch has 2^32 threads (WKV7_ERR_UNSUPPORTED beyond, before anything
+ * is enqueued).
  *
  * Ownership, execution and errors as for wkv7.h: device pointers owned by the
  * caller, work enqueued on `stream`, nothing allocated or synchronised, every

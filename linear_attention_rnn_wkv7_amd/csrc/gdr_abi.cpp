@@ -13,12 +13,15 @@
 namespace {
 
 constexpr size_t kAlign = 256;
+// Chunks times value heads.
+constexpr int64_t kMaxChunks = int64_t(1) << 22;
 // Threads of a launch in one dimension stay below 2^32.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
 constexpr int64_t kMaxGroups = (int64_t(1) << 32) / 1024 - 1;
 
 struct Dims {
     int64_t B, T, Hk, Hv, K, V, seqs, nck, slots;
-    bool packed;
+    bool packed, makes;
     int dtype, norm;
     float scale;
     size_t states, rows, table;       // bytes: chunk states, chunk rows, tables
@@ -89,21 +92,34 @@ int check(const gdr_shape *s, Dims *d)
         d->slots = s->T / wkv7::gdr::kChunk + s->nseq;
     else if (!mul_ok(s->B, d->nck, &d->slots))
         return WKV7_ERR_INVALID;
-    if (d->slots > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
+    if (d->slots > kMaxChunks) return WKV7_ERR_UNSUPPORTED;
     if (!mul_ok(d->slots, s->Hv, &per) || !mul_ok(per, 4 * 4 * (128 * 256 + 64 * 256 + 2 * 4096), &x))
         return WKV7_ERR_INVALID;   // any sum of the workspace's parts
-    if (per > (int64_t(1) << 22)) return WKV7_ERR_UNSUPPORTED;   // a workgroup of 512 for each
+    if (per > kMaxChunks) return WKV7_ERR_UNSUPPORTED;
     plan_segments(d);
     const size_t segs = d->nseg > 1 ? (size_t)(s->B * s->Hv * d->nseg) : 0;
     d->seg_map = segs * (size_t)(s->K * (s->V + s->K) * 4);
     d->carry = segs * (size_t)(s->V * s->K * 4);
     d->states = (size_t)(per * s->K * s->V * 4);
     d->rows = (size_t)(per * 64 * s->V * 4);
-    const bool makes = wkv7::gdr::scan_makes_factors(d->dtype, s->K, s->V, d->seqs * s->Hv);
-    d->factors = makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, false);
-    d->factors_t = makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, true);
+    d->makes = wkv7::gdr::scan_makes_factors(d->dtype, s->K, s->V, d->seqs * s->Hv);
+    d->factors = d->makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, false);
+    d->factors_t = d->makes ? 0 : (size_t)per * wkv7::gdr::factor_bytes(d->dtype, true);
     d->table = (size_t)(per * wkv7::gdr::kTableFloats * 4);
     return WKV7_OK;
+}
+
+// A shape of the chunked calls: every launch of one fits, whichever are made
+// (the passes over segments have 256 units at most).
+int check_chunked(const gdr_shape *s, Dims *d)
+{
+    const int rc = check(s, d);
+    if (rc != WKV7_OK || !d->tokens()) return rc;
+    const wkv7::gdr::ScanGrid g = wkv7::gdr::scan_grid(d->seqs * d->Hv, d->Hv / d->Hk, d->V, d->makes);
+    return g.blocks * g.threads < kMaxThreads && wkv7::gdr::prep_blocks(d->slots, d->Hv) * 256 < kMaxThreads &&
+                   wkv7::gdr::grads_blocks(d->slots, d->Hk) * 4 * d->K < kMaxThreads
+               ? WKV7_OK
+               : WKV7_ERR_UNSUPPORTED;
 }
 
 size_t segment_bytes(const Dims &d) { return round_up(d.seg_map) + round_up(d.carry); }
@@ -226,21 +242,21 @@ extern "C" {
 size_t gdr_checkpoint_bytes(const gdr_shape *shape)
 {
     Dims d;
-    if (check(shape, &d) != WKV7_OK || !d.tokens()) return 0;
+    if (check_chunked(shape, &d) != WKV7_OK || !d.tokens()) return 0;
     return record_bytes(d);
 }
 
 size_t gdr_forward_workspace_bytes(const gdr_shape *shape)
 {
     Dims d;
-    if (check(shape, &d) != WKV7_OK || !d.tokens()) return 0;
+    if (check_chunked(shape, &d) != WKV7_OK || !d.tokens()) return 0;
     return forward_bytes(d);
 }
 
 size_t gdr_backward_workspace_bytes(const gdr_shape *shape, int ckpt_provided)
 {
     Dims d;
-    if (check(shape, &d) != WKV7_OK || !d.tokens()) return 0;
+    if (check_chunked(shape, &d) != WKV7_OK || !d.tokens()) return 0;
     return backward_bytes(d, ckpt_provided != 0);
 }
 
@@ -249,7 +265,7 @@ int gdr_forward(const gdr_shape *shape, const void *q, const void *k, const void
                 float *ckpt, void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     Dims d;
-    int rc = check(shape, &d);
+    int rc = check_chunked(shape, &d);
     if (rc != WKV7_OK) return rc;
     rc = check_inputs(d, {q, k, v, g, beta}, {s0, y, sT, ckpt}, seq_starts);
     if (rc != WKV7_OK) return rc;
@@ -277,7 +293,7 @@ int gdr_backward(const gdr_shape *shape, const void *q, const void *k, const voi
                  hipStream_t stream)
 {
     Dims d;
-    int rc = check(shape, &d);
+    int rc = check_chunked(shape, &d);
     if (rc != WKV7_OK) return rc;
     rc = check_inputs(d, {q, k, v, g, beta, dy, dq, dk, dv, dg, dbeta}, {s0, dsT, ckpt, ds0}, seq_starts);
     if (rc != WKV7_OK) return rc;

@@ -509,7 +509,7 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.group = (int)(a.Hv / a.Hk);
     p.norm = a.norm;
     p.scale = a.scale;
-    const dim3 grid((unsigned)((a.map.slots + 7) / 8 * 8 * a.Hk));
+    const dim3 grid((unsigned)grads_blocks(a.map.slots, a.Hk));
     if (p.group > 1)
         hipLaunchKernelGGL((gdr_grads_kernel<T, K, true>), grid, dim3(4 * K), 0, stream, p);
     else

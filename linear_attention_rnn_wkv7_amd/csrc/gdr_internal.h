@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "gdr.h"
 #include "residual_norm.h"
 
@@ -43,6 +45,45 @@ inline bool scan_makes_factors(int dtype, int64_t K, int64_t V, int64_t units)
 {
     return dtype == WKV7_BF16 && K == 64 && V <= 64 && units >= 128;
 }
+// Waves that make them.
+constexpr int kMakers = 4;
+
+// The grid of a scan.  Slabs of 16 columns per workgroup, a wave each: as many
+// as there are (8 at most, 4 beside makers), fewer while that leaves compute
+// units without a workgroup.  A unit's slab groups read the same q, k and
+// factors, a key head's value heads the same q and k: they go to one die, whose
+// cache then holds them for all, unless that leaves a die with more than an
+// eighth above its share and its 32 compute units.  (4 x 4096 x 8 / 16 heads, K =
+// V = 128, bf16, four groups: reverse 332 -> 319 us, forward 315 -> 310; 24 packed
+// sequences of 12288 tokens, 16 / 32 heads, one group: 212 -> 209.)
+struct ScanGrid {
+    int64_t slabs;                  // of a workgroup
+    int64_t groups, share, total;   // slab groups of a unit, neighbours on a die, workgroups with work
+    int64_t blocks, threads;        // of the launch
+};
+inline ScanGrid scan_grid(int64_t units, int64_t heads_per_key, int64_t columns, bool makes)
+{
+    ScanGrid g;
+    const int64_t slabs = columns / 16, most = makes ? 4 : 8;
+    g.groups = (slabs + most - 1) / most;
+    while (units * g.groups < 256 && g.groups < slabs) ++g.groups;
+    g.slabs = (slabs + g.groups - 1) / g.groups;
+    g.groups = (slabs + g.slabs - 1) / g.slabs;
+    g.total = units * g.groups;
+    int64_t turns = 0;
+    for (int64_t s : {g.groups * heads_per_key, g.groups, (int64_t)1}) {
+        g.share = s;
+        turns = (g.total / s + 7) / 8 * s;   // a die's most
+        if (turns <= 32 || turns * 64 <= g.total * 9) break;
+    }
+    g.blocks = turns * 8;
+    g.threads = 64 * (g.slabs + (makes ? kMakers : 1));
+    return g;
+}
+// Workgroups of the factors' (256 threads) and the gradients' kernel (4 K).
+inline int64_t prep_blocks(int64_t slots, int64_t Hv) { return (slots + 31) / 32 * 8 * Hv; }
+inline int64_t grads_blocks(int64_t slots, int64_t Hk) { return (slots + 7) / 8 * 8 * Hk; }
+
 // Bytes of a chunk's factors in memory, for the forward or (transposed) the reverse scan.
 size_t factor_bytes(int dtype, bool transposed);
 

@@ -61,7 +61,7 @@ hipError_t launch_t(const Launch &a, bool transposed, hipStream_t stream)
     p.group = (int)(a.Hv / a.Hk);
     p.norm = a.norm;
     p.scale = a.scale;
-    const dim3 grid((unsigned)((a.map.slots + 31) / 32 * 8 * a.Hv));
+    const dim3 grid((unsigned)prep_blocks(a.map.slots, a.Hv));
     if (transposed)
         hipLaunchKernelGGL((gdr_prep_kernel<T, K, true>), grid, dim3(256), 0, stream, p);
     else

@@ -131,7 +131,6 @@ __device__ __forceinline__ Pos chunk_at(int64_t lo, int64_t hi, int64_t slot0, i
 // copies run while one is computed, two of factors, one read and one being
 // written, and the scratch of the waves that write them.  Else: two sets of
 // all, or one where two do not fit (fp32 with K = 128).
-constexpr int kMakers = 4;
 template <typename T, int K>
 struct ScanLds {
     static constexpr int kMat = Swizzled<T, K>::kBytes;
@@ -610,41 +609,18 @@ ScanArgs<T> scan_args(const Launch &a)
     return p;
 }
 
-// Slabs per workgroup, a wave each: as many as there are (`most` at most),
-// fewer while that leaves compute units without a workgroup.  A unit's slab
-// groups read the same q, k and factors, a key head's value heads the same q
-// and k: they go to one die, whose cache then holds them for all, unless that
-// leaves a die with more than an eighth above its share and its 32 compute
-// units.  (4 x 4096 x 8 / 16 heads, K = V = 128, bf16, four groups: reverse 332
-// -> 319 us, forward 315 -> 310; 24 packed sequences of 12288 tokens, 16 / 32
-// heads, one group: 212 -> 209.)
-int scan_grid(const Launch &a, int64_t columns, int most, Place *place, dim3 *grid)
-{
-    const int64_t slabs = columns / 16, units = a.map.nseq * a.map.nseg * a.Hv;
-    int64_t groups = (slabs + most - 1) / most;
-    while (units * groups < 256 && groups < slabs) ++groups;
-    const int64_t per = (slabs + groups - 1) / groups;
-    groups = (slabs + per - 1) / per;
-    const int64_t total = units * groups, sets[3] = {groups * (a.Hv / a.Hk), groups, 1};
-    int64_t share = 1, turns = 0;
-    for (int64_t s : sets) {
-        share = s;
-        turns = (total / s + 7) / 8 * s;   // a die's most
-        if (turns <= 32 || turns * 64 <= total * 9) break;
-    }
-    *place = Place{(uint32_t)groups, (uint32_t)share, (uint32_t)total};
-    *grid = dim3((unsigned)(turns * 8));
-    return (int)per;
-}
+Place place_of(const ScanGrid &g) { return Place{(uint32_t)g.groups, (uint32_t)g.share, (uint32_t)g.total}; }
 
 template <typename T, int K, bool kMake>
 hipError_t scan_t(const Launch &a, bool reverse, hipStream_t stream)
 {
     ScanArgs<T> p = scan_args<T>(a);
-    dim3 grid;
+    const int64_t units = a.map.nseq * a.map.nseg * a.Hv;
     if constexpr (!kMake) {
         if (a.map.nseg > 1) {
-            const dim3 block(64 * (scan_grid(a, a.V + K, 8, &p.place, &grid) + 1));
+            const ScanGrid g = scan_grid(units, p.group, a.V + K, false);
+            const dim3 grid((unsigned)g.blocks), block((unsigned)g.threads);
+            p.place = place_of(g);
             const dim3 rows((unsigned)(a.V / 16), (unsigned)a.Hv, (unsigned)a.map.nseq);
             if (reverse) {
                 hipLaunchKernelGGL((gdr_reverse_kernel<T, K, false, true>), grid, block, 0, stream, p);
@@ -661,8 +637,9 @@ hipError_t scan_t(const Launch &a, bool reverse, hipStream_t stream)
             if (e != hipSuccess) return e;
         }
     }
-    const int slabs = scan_grid(a, a.V, kMake ? 4 : 8, &p.place, &grid);
-    const dim3 block(64 * (slabs + (kMake ? kMakers : 1)));
+    const ScanGrid g = scan_grid(units, p.group, a.V, kMake);
+    const dim3 grid((unsigned)g.blocks), block((unsigned)g.threads);
+    p.place = place_of(g);
     if (reverse) {
         p.st = a.ws_ds;
         p.rows = a.ws_dr;

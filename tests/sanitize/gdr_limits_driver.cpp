@@ -75,10 +75,59 @@ void oversized()
         CHECK(launches() == before);
     }
 }
+
+// At the limit of chunks times heads: what is accepted makes launches of fewer
+// than 2^32 threads, and what is refused would not, or has more chunks.
+void edges()
+{
+    const int64_t most = int64_t(1) << 32, chunks = int64_t(1) << 22;
+    int accepted = 0, large = 0;
+    for (int dtype : {WKV7_F32, WKV7_BF16})
+        for (int64_t K : {64, 128})
+            for (int64_t V = 16; V <= 256; V += 16)
+                for (int64_t B : {int64_t(1), int64_t(64), int64_t(64527), int64_t(65535)})
+                    for (int64_t n : {int64_t(1), int64_t(65536), chunks - 1, chunks, chunks + 1})   // chunks of a row
+                        for (int64_t Hv : {int64_t(1), int64_t(56), int64_t(57), int64_t(64), int64_t(65), int64_t(65535)})
+                            for (int64_t Hk : {int64_t(1), Hv})
+                                for (int packed = 0; packed < 2; ++packed) {
+                                    const int64_t seqs = B, rows = packed ? 1 : B;
+                                    // packed: n - 1 whole chunks in all besides one for each sequence
+                                    const int64_t T = packed ? 64 * (n - 1) : 64 * n - 63;
+                                    if (T <= 0) continue;
+                                    const gdr_shape s{rows, T, Hk, Hv, K, V, packed ? B : 0, dtype, 0, 1.f};
+                                    const int64_t slots = packed ? n - 1 + B : B * n;
+                                    const bool makes = wkv7::gdr::scan_makes_factors(dtype, K, V, seqs * Hv);
+                                    const wkv7::gdr::ScanGrid g = wkv7::gdr::scan_grid(seqs * Hv, Hv / Hk, V, makes);
+                                    const bool fits = slots * Hv <= chunks && g.blocks * g.threads < most;
+                                    CHECK((gdr_checkpoint_bytes(&s) > 0) == fits);
+                                    if (!fits) {
+                                        const int32_t *st = packed ? reinterpret_cast<const int32_t *>(kIn) : nullptr;
+                                        const size_t before = g_scan.size();
+                                        const int rc = gdr_forward(&s, kIn, kIn, kIn, kIn, kIn, nullptr, st, kIn, kIn,
+                                                                   kRec, kWs, SIZE_MAX, nullptr);
+                                        CHECK(rc == WKV7_ERR_UNSUPPORTED || rc == WKV7_ERR_INVALID);
+                                        CHECK(g_scan.size() == before);
+                                        continue;
+                                    }
+                                    ++accepted;
+                                    large += slots * Hv == chunks;
+                                    CHECK(wkv7::gdr::prep_blocks(slots, Hv) * 256 < most);
+                                    CHECK(wkv7::gdr::grads_blocks(slots, Hk) * 4 * K < most);
+                                    // each slab and unit has its place
+                                    CHECK(g.slabs * g.groups * 16 >= V && g.slabs * (g.groups - 1) * 16 < V);
+                                    CHECK(g.total == seqs * Hv * g.groups && g.blocks >= g.total && g.threads <= 576);
+                                }
+    CHECK(accepted > 1000 && large > 10);
+    // decode has no such launch
+    const gdr_shape s{65535, 1, 64, 64, 64, 256, 0, WKV7_BF16, 0, 1.f};
+    CHECK(gdr_checkpoint_bytes(&s) == 0);
+    CHECK(gdr_decode(&s, kIn, kIn, kIn, kIn, kIn, kIn, 65535, nullptr, kIn, nullptr) == WKV7_OK);
+}
 }  // namespace
 
 int main()
 {
     oversized();
+    edges();
     return g_fails ? 1 : 0;
 }
