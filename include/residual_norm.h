@@ -16,8 +16,8 @@
  * (without a scale, dy is dx).  The sums over rows run in a fixed order:
  * results are the same bit for bit from run to run.
  *
- * Any D from 1 to 16384 and any number of rows; pointers 16-byte aligned
- * (rows need not be).  Ownership, execution and errors as for wkv7.h.
+ * Any D from 1 to 16384 and any number of rows that memory holds (up to 2^38);
+ * pointers 16-byte aligned (rows need not be).  Ownership, execution and errors as for wkv7.h.
  */
 #ifndef RESIDUAL_NORM_H
 #define RESIDUAL_NORM_H

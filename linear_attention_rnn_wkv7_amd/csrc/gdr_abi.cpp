@@ -13,6 +13,8 @@
 namespace {
 
 constexpr size_t kAlign = 256;
+// Rows of the norms: more than memory holds.
+constexpr int64_t kMaxRows = int64_t(1) << 38;
 // Chunks times value heads.
 constexpr int64_t kMaxChunks = int64_t(1) << 22;
 // Threads of a launch in one dimension stay below 2^32.
@@ -216,7 +218,7 @@ int check(const residual_norm_shape *s, wkv7::gdr::NormLaunch *L)
     if (s->dtype != WKV7_F32 && s->dtype != WKV7_BF16) return WKV7_ERR_INVALID;
     if (!(s->eps > 0.f) || !isfinite(s->eps)) return WKV7_ERR_INVALID;
     if (s->D > 16384) return WKV7_ERR_UNSUPPORTED;
-    if (s->rows > kMaxGroups) return WKV7_ERR_UNSUPPORTED;
+    if (s->rows > kMaxRows) return WKV7_ERR_UNSUPPORTED;
     L->rows = s->rows;
     L->D = s->D;
     L->dtype = s->dtype;

@@ -48,6 +48,9 @@ __device__ __forceinline__ float lanes_sum(float x)
     return x;
 }
 
+// The most workgroups of a launch: its threads stay below 2^32.
+constexpr int64_t max_blocks(int threads) { return (int64_t(1) << 32) / threads - 1; }
+
 // ------------------------------------------------------------- the epilogue
 
 template <typename T>
@@ -199,8 +202,8 @@ struct NormArgs {
     const float *scale, *w;
     T *xo, *h, *dx, *dy;
     float *part;             // [parts][1 or 2][D]
-    int64_t rows;
-    int D, per;              // rows per backward workgroup
+    int64_t rows, per;       // rows per backward workgroup
+    int D;
     float eps;
 };
 
@@ -417,12 +420,22 @@ hipError_t norm_t(const NormLaunch &a, bool backward, hipStream_t stream)
     p.D = (int)a.D;
     p.eps = a.eps;
     if (!backward) {
-        hipLaunchKernelGGL((norm_fwd_kernel<T, NT, kN, kVec>), dim3((unsigned)((a.rows + RB - 1) / RB)), dim3(B), 0,
-                           stream, p);
-        return hipGetLastError();
+        const int64_t most = max_blocks(B) * RB;   // rows of a launch
+        for (int64_t left = a.rows; left > 0; left -= most) {
+            p.rows = left < most ? left : most;
+            hipLaunchKernelGGL((norm_fwd_kernel<T, NT, kN, kVec>), dim3((unsigned)((p.rows + RB - 1) / RB)), dim3(B), 0,
+                               stream, p);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            p.x += most * a.D;
+            p.h += most * a.D;
+            if (p.y) p.y += most * a.D;
+            if (p.xo) p.xo += most * a.D;
+        }
+        return hipSuccess;
     }
     const int64_t groups = norm_parts(a.rows, a.D) / RB;
-    p.per = (int)((a.rows + groups - 1) / groups);
+    p.per = (a.rows + groups - 1) / groups;
     if (a.scale)
         hipLaunchKernelGGL((norm_bwd_kernel<T, NT, kN, kVec, true>), dim3((unsigned)groups), dim3(B), 0, stream, p);
     else

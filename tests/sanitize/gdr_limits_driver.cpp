@@ -123,11 +123,28 @@ void edges()
     CHECK(gdr_checkpoint_bytes(&s) == 0);
     CHECK(gdr_decode(&s, kIn, kIn, kIn, kIn, kIn, kIn, 65535, nullptr, kIn, nullptr) == WKV7_OK);
 }
+
+// Rows beyond what one launch has threads for.
+void many_rows()
+{
+    const int64_t most = int64_t(1) << 38;
+    for (int64_t rows : {int64_t(4194303), int64_t(4194304), int64_t(1) << 32, most, most + 1}) {
+        const int ok = rows <= most ? WKV7_OK : WKV7_ERR_UNSUPPORTED;
+        for (int64_t D : {1, 1024, 16384}) {
+            const residual_norm_shape n{rows, D, WKV7_BF16, 0, 1e-6f};
+            const size_t ws = residual_norm_workspace_bytes(&n);
+            CHECK((ws > 0) == (ok == WKV7_OK));
+            CHECK(residual_norm_forward(&n, kIn, kIn, kIn, kIn, kIn, kIn, nullptr) == ok);
+            CHECK(residual_norm_backward(&n, kIn, nullptr, kIn, kIn, kIn, kIn, kIn, kIn, kIn, kIn, kWs, ws, nullptr) == ok);
+        }
+    }
+}
 }  // namespace
 
 int main()
 {
     oversized();
     edges();
+    many_rows();
     return g_fails ? 1 : 0;
 }
