@@ -129,8 +129,8 @@ int gdr_decode(const gdr_shape *shape, const void *q, const void *k, const void 
  * gdr_epilogue_workspace_bytes bytes, 256-byte aligned.  No output may overlap
  * an input. */
 typedef struct {
-    int64_t rows;   /* tokens, >= 0 */
-    int64_t H;      /* heads, >= 0 */
+    int64_t rows;   /* tokens, >= 0; rows times H at most 2^38 */
+    int64_t H;      /* heads, >= 0; at most 65535 with a weight for each */
     int64_t N;      /* entries of a head */
     int64_t Hw;     /* heads of the weight: 1 or H */
     int32_t dtype;  /* wkv7_dtype */

@@ -19,7 +19,6 @@ constexpr int64_t kMaxRows = int64_t(1) << 38;
 constexpr int64_t kMaxChunks = int64_t(1) << 22;
 // Threads of a launch in one dimension stay below 2^32.
 constexpr int64_t kMaxThreads = int64_t(1) << 32;
-constexpr int64_t kMaxGroups = (int64_t(1) << 32) / 1024 - 1;
 
 struct Dims {
     int64_t B, T, Hk, Hv, K, V, seqs, nck, slots;
@@ -201,7 +200,7 @@ int check(const gdr_epilogue_shape *s, wkv7::gdr::EpilogueLaunch *L)
     if (s->N < 16 || s->N > 256 || (s->N & (s->N - 1)) != 0 || s->Hw > 65535) return WKV7_ERR_UNSUPPORTED;
     int64_t n, x;
     if (!mul_ok(s->rows, s->H, &n) || !mul_ok(n, s->N * 4, &x)) return WKV7_ERR_INVALID;
-    if (n / (2048 / s->N) >= kMaxGroups) return WKV7_ERR_UNSUPPORTED;
+    if (n > kMaxRows) return WKV7_ERR_UNSUPPORTED;
     L->rows = s->rows;
     L->H = s->H;
     L->N = s->N;

@@ -59,7 +59,7 @@ struct EpiArgs {
     const float *w;
     T *z, *dy, *dgate;
     float *part;              // [Hw][parts][N]
-    int64_t rows, H, Hw;      // tokens
+    int64_t rows, H, Hw;      // heads of the forward's launch, tokens of the backward
     int64_t per, parts;       // rows of a weight head per backward workgroup
     float eps;
 };
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) epilogue_fwd_kernel(EpiArgs<T> a)
 {
     constexpr int L = N / 8, R = 256 / L;   // lanes per row, rows per workgroup
     const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / L;
-    if (row >= a.rows * a.H) return;        // whole rows
+    if (row >= a.rows) return;              // whole rows
     const int col = 8 * (threadIdx.x % L);
     const int64_t o = row * N + col;
     const f32x8 y = load8(a.y + o), g = load8(a.gate + o);
@@ -167,9 +167,19 @@ hipError_t epilogue_t(const EpilogueLaunch &a, bool backward, hipStream_t stream
     p.eps = a.eps;
     constexpr int R = 256 / (N / 8);
     if (!backward) {
-        hipLaunchKernelGGL((epilogue_fwd_kernel<T, N>), dim3((unsigned)((a.rows * a.H + R - 1) / R)), dim3(256), 0,
-                           stream, p);
-        return hipGetLastError();
+        // heads of a launch; with a weight for each of H (65535 at most), whole tokens
+        const int64_t most = max_blocks(256) * R / a.Hw * a.Hw;
+        for (int64_t left = a.rows * a.H; left > 0; left -= most) {
+            p.rows = left < most ? left : most;
+            hipLaunchKernelGGL((epilogue_fwd_kernel<T, N>), dim3((unsigned)((p.rows + R - 1) / R)), dim3(256), 0, stream,
+                               p);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            p.y += most * N;
+            p.gate += most * N;
+            p.z += most * N;
+        }
+        return hipSuccess;
     }
     const int64_t all = a.rows * a.H / a.Hw;
     p.parts = epilogue_parts(a.rows, a.H, N, a.Hw);

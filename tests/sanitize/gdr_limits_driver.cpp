@@ -137,6 +137,13 @@ void many_rows()
             CHECK(residual_norm_forward(&n, kIn, kIn, kIn, kIn, kIn, kIn, nullptr) == ok);
             CHECK(residual_norm_backward(&n, kIn, nullptr, kIn, kIn, kIn, kIn, kIn, kIn, kIn, kIn, kWs, ws, nullptr) == ok);
         }
+        for (int64_t N : {16, 256}) {
+            const gdr_epilogue_shape e{rows, 1, N, 1, WKV7_BF16, 0, 1e-6f};
+            const size_t ws = gdr_epilogue_workspace_bytes(&e);
+            CHECK((ws > 0) == (ok == WKV7_OK));
+            CHECK(gdr_epilogue_forward(&e, kIn, kIn, kIn, kIn, nullptr) == ok);
+            CHECK(gdr_epilogue_backward(&e, kIn, kIn, kIn, kIn, kIn, kIn, kIn, kWs, ws, nullptr) == ok);
+        }
     }
 }
 }  // namespace

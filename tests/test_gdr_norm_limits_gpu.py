@@ -37,3 +37,18 @@ def test_residual_norm_more_rows_than_a_launch(rows, D, dt):
         # 2^-24 of their 2-norm's size, 16 times that for a single sum
         terms = (len(at) ** 0.5) * float(want[name].abs().max()) + float(want[name].abs().sum() / D)
         assert float((got[name] - want[name]).abs().max()) <= 16 * 20 * 2.0 ** -24 * terms, name
+
+
+@pytest.mark.parametrize("heads", [False, True])
+def test_epilogue_more_rows_than_a_launch(heads):
+    """2^29 heads of 16 and more, as those at the end alone."""
+    H, N = 3, 16
+    rows = (1 << 29) // H + 50
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    small = [torch.randn(1, 40, H, N, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    y, gate = (torch.zeros(1, rows, H, N, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    y[:, -40:], gate[:, -40:] = small
+    w = torch.randn(H if heads else 1, N, generator=gen, device="cuda")
+    z = api.gdr_epilogue_forward(y, gate, w)
+    assert torch.equal(z[:, -40:], api.gdr_epilogue_forward(*small, w))
+    assert not z[:, -80:-40].any()
