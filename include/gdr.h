@@ -20,6 +20,7 @@
  *   v, y, dy, dv        [B][T][Hv][V]    dtype per gdr_shape.dtype
  *   g, beta, dg, dbeta  [B][T][Hv]       fp32
  *   states s0, sT, dsT, ds0  [sequences][Hv][V][K]  fp32
+ *   seq_starts, slots   int32 (16-byte aligned too)
  * g is the log decay, at most 0.  Values of g at or below -200, -inf among them,
  * forget the whole state, and their gradient is exactly zero; k should not be longer than
  * sqrt(2 / beta), or the recurrence itself grows.

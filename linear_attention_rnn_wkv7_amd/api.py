@@ -348,6 +348,12 @@ def _workspace(name, workspace, need, index):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _aligned(*tensors):
+    """The tensors, those off the library's 16-byte alignment copied (on the
+    current stream): slices of slots, starts, g or beta begin anywhere."""
+    return [t if t is None or t.data_ptr() % 16 == 0 else t.clone() for t in tensors]
+
+
 def _output(name, t, shape, dtype, index):
     """A caller's output, checked, or a new one."""
     if t is None:
@@ -439,7 +445,8 @@ def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_
         sT_ = _output("sT", sT, ss, f32, at) if want_sT else None
         ckpt_ = _output("ckpt", ckpt, (ck_bytes // 4,), f32, at) if want_ckpt else None
         ws, wp, wb = _workspace("gdr_forward", workspace, need, at)
-        rc = _lib.lib().gdr_forward(sh, *map(_at, (q, k, v, g, beta, s0, seq_starts, y_, sT_, ckpt_)), wp, wb, st)
+        g_, beta_, starts = _aligned(g, beta, seq_starts)
+        rc = _lib.lib().gdr_forward(sh, *map(_at, (q, k, v, g_, beta_, s0, starts, y_, sT_, ckpt_)), wp, wb, st)
         _lib.check("gdr_forward", rc)
         return y_, sT_, ckpt_
 
@@ -465,8 +472,9 @@ def gdr_backward(q, k, v, g, beta, dy, s0=None, dsT=None, ckpt=None, *, seq_star
             grads[n] = _output(n, grads.get(n), like.shape, like.dtype, at)
         grads["ds0"] = _output("ds0", grads.get("ds0"), ss, f32, at) if want_ds0 else None
         ws, wp, wb = _workspace("gdr_backward", workspace, need[ckpt is not None], at)
+        g_, beta_, starts = _aligned(g, beta, seq_starts)
         rc = _lib.lib().gdr_backward(
-            sh, *map(_at, (q, k, v, g, beta, s0, seq_starts, dy, dsT, ckpt)),
+            sh, *map(_at, (q, k, v, g_, beta_, s0, starts, dy, dsT, ckpt)),
             *(_at(grads[n]) for n in ("dq", "dk", "dv", "dg", "dbeta", "ds0")), wp, wb, st)
         _lib.check("gdr_backward", rc)
         return grads
@@ -493,8 +501,9 @@ def gdr_decode(q, k, v, g, beta, state, slots=None, *, scale=None, norm_qk=False
 
     def call(st):
         y = _output("y", out, ys, q.dtype, at)
-        rc = _lib.lib().gdr_decode(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                   state.data_ptr(), pool, _at(slots), y.data_ptr(), st)
+        g_, beta_, slots_ = _aligned(g, beta, slots)
+        rc = _lib.lib().gdr_decode(sh, q.data_ptr(), k.data_ptr(), v.data_ptr(), g_.data_ptr(), beta_.data_ptr(),
+                                   state.data_ptr(), pool, _at(slots_), y.data_ptr(), st)
         _lib.check("gdr_decode", rc)
         return y
 
