@@ -10,8 +10,8 @@ __all__ = ["wkv7_forward", "wkv7_backward", "wkv7_checkpoint_bytes",
            "wkv7_backward_workspace_bytes",
            "gdr_forward", "gdr_backward", "gdr_decode", "gdr_checkpoint_bytes",
            "gdr_forward_workspace_bytes", "gdr_backward_workspace_bytes",
-           "gdr_epilogue_forward", "gdr_epilogue_backward",
-           "residual_norm_forward", "residual_norm_backward"]
+           "gdr_epilogue_forward", "gdr_epilogue_backward", "gdr_epilogue_workspace_bytes",
+           "residual_norm_forward", "residual_norm_backward", "residual_norm_workspace_bytes"]
 
 
 def __getattr__(name):

@@ -517,6 +517,12 @@ def _epilogue_sizes(*key):
     return sh, r, _lib.lib().gdr_epilogue_workspace_bytes(r)
 
 
+def gdr_epilogue_workspace_bytes(rows, H, N, Hw=1, dtype=torch.float32):
+    """Of gdr_epilogue_backward: ``rows`` tokens of H heads of N, weights for
+    Hw heads (1 or H)."""
+    return _epilogue_sizes(rows, H, N, Hw, _VEC_DTYPES[dtype], 0, 1e-6)[2]
+
+
 def _gdr_epilogue_dims(y, gate, w, eps):
     if y.dim() != 4 or w.dim() != 2:
         raise ValueError("y must be [B, T, H, N] and w [1 or H, N]")
@@ -576,6 +582,11 @@ def _norm_sizes(*key):
     sh = _lib.ResidualNormShape(*key)
     r = ctypes.byref(sh)
     return sh, r, _lib.lib().residual_norm_workspace_bytes(r)
+
+
+def residual_norm_workspace_bytes(rows, D, dtype=torch.float32):
+    """Of residual_norm_backward: ``rows`` rows of D."""
+    return _norm_sizes(rows, D, _VEC_DTYPES[dtype], 0, 1e-6)[2]
 
 
 def _norm_dims(x, eps):
