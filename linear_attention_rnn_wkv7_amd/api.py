@@ -363,8 +363,10 @@ def _output(name, t, shape, dtype, index):
 
 
 def gdr_shape(B, T, Hk, Hv, K, V, dtype=torch.float32, nseq=0, norm_qk=False, scale=None):
+    if scale is None:
+        scale = K ** -0.5 if K > 0 else 1.0   # the library refuses other K
     return _lib.GdrShape(B, T, Hk, Hv, K, V, nseq, _VEC_DTYPES[dtype],
-                         _lib.GDR_NORM_QK if norm_qk else 0, K ** -0.5 if scale is None else scale)
+                         _lib.GDR_NORM_QK if norm_qk else 0, scale)
 
 
 @functools.lru_cache(maxsize=256)

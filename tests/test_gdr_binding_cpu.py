@@ -22,3 +22,10 @@ def test_norm_workspace_sizes():
         assert pkg.residual_norm_workspace_bytes(rows, D, dt) == want
         assert (want > 0) == (rows > 0)
     assert "gdr_epilogue_workspace_bytes" in pkg.__all__ and "residual_norm_workspace_bytes" in pkg.__all__
+
+
+def test_sizes_of_a_rule_without_a_key():
+    """K = 0 is refused like other sizes, though the default scale is K ** -0.5."""
+    assert pkg.gdr_checkpoint_bytes(1, 5, 1, 1, 0, 16) == 0
+    assert pkg.gdr_forward_workspace_bytes(1, 5, 1, 1, 0, 16) == 0
+    assert pkg.gdr_backward_workspace_bytes(1, 5, 1, 1, 0, 16) == 0
