@@ -29,3 +29,10 @@ def test_sizes_of_a_rule_without_a_key():
     assert pkg.gdr_checkpoint_bytes(1, 5, 1, 1, 0, 16) == 0
     assert pkg.gdr_forward_workspace_bytes(1, 5, 1, 1, 0, 16) == 0
     assert pkg.gdr_backward_workspace_bytes(1, 5, 1, 1, 0, 16) == 0
+
+
+def test_unsupported_says_what_of():
+    """The text for a size that a call does not take is not only about wkv7's
+    head sizes."""
+    text = _lib.status_text(_lib.WKV7_ERR_UNSUPPORTED)
+    assert "a size that the call does not take" in text and "gdr.h" in text and "residual_norm.h" in text
