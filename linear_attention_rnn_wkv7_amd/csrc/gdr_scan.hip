@@ -154,11 +154,12 @@ __device__ __forceinline__ void record_state(float *to, const f32x4 (&S)[KT], in
     for (int i = 0; i < KT; ++i) *reinterpret_cast<f32x4 *>(to + o + 16 * i) = S[i];
 }
 
-// When a slab loads its next chunk's values: with K = 64 after the products of
-// the state, when the step's operand copies are through (1 x 65536 x 32, bf16,
-// passes of 402 and 432 us -> 387 and 388; 8 x 4096 x 32 with the record 308 ->
-// 286); with K = 128 at the step's start, ahead of the stores of the state
-// (4 x 4096 x 16 with the record: 300 us, 312 after the products).
+// When a slab loads its next chunk's values: after the products of the state,
+// when the step's operand copies are through, but in the reverse scan with K =
+// 128 at the step's start, ahead of the stores of the state.  (At the start
+// against after: forward, 1 x 65536 x 32, bf16, second pass 468 and 455 us; 8 x
+// 4096 x 32 323 and 306; K = 128, 4 x 4096 x 16, 314 and 300.  Reverse: 8 x 4096 x
+// 32 321 and 319; K = 128, 4 x 4096 x 16, 291 and 306.)
 template <int K>
 constexpr bool kFetchFirst = K == 128;
 
@@ -337,7 +338,6 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
             f32x4 R[4], Y[4];
 #pragma unroll
             for (int i = 0; i < 16; ++i) R[i >> 2][i & 3] = Cols<T>::value(vn[i]);
-            if (kFetchFirst<K> && c + 1 < nc) fetch(c + 1);
             if (!kMap && a.st) {
                 record_state<KT>(a.st + at.ch * K * a.V, S, col, lg);
             }
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kMaxThreads<kMake>) gdr_scan_kernel(ScanArgs<T
                 for (int ks = 0; ks <= it / 2; ++ks)
                     E[it] = mma(E[it], load_tri<T, P, false>(f.t, it, ks, lane), Rf[ks]);
             }
-            if (!kFetchFirst<K> && c + 1 < nc) fetch(c + 1);
+            if (c + 1 < nc) fetch(c + 1);
             if (!kMap && a.rows) {
                 const Tiles rows(a.rows + at.ch * 64 * a.V, 64, a.V, col, lg);
 #pragma unroll
