@@ -33,11 +33,17 @@
  * sequence are neither read nor written, in any output.  The starts are read
  * on the device: values outside the documented range are clamped to it (no
  * access leaves the buffers), and starts that decrease give undefined outputs.
+ * A packed sequence runs in one piece, while few, long rows are cut into segments
+ * that run at once: a single long document is faster as a row without starts
+ * (65536 tokens x 32 heads of 64, bf16: 1.12 ms, packed 2.84).
  *
  * Numbers.  State, sums and the products inside a chunk are fp32 (fp32
  * inputs), or, with bf16 inputs, products of bf16 parts that carry a value's
  * leading 24 bits, with fp32 sums.  y and the gradients of q, k, v are rounded once, to the inputs'
- * type.  Results are the same bit for bit from run to run.
+ * type.  Results are the same bit for bit from run to run.  Tokens of a chunk are
+ * computed together: an infinity or NaN in one token's inputs may reach every
+ * output of its chunk of 64 and of later (in the gradients also earlier) chunks,
+ * of its own sequence and head (key head, in the gradients) alone.
  *
  * Sizes.  At most 65535 sequences and value heads, 2^22 chunks of 64 tokens
  * (as gdr_checkpoint_bytes counts them) times value heads, and, in the

@@ -433,6 +433,7 @@ def gdr_forward(q, k, v, g, beta, s0=None, *, seq_starts=None, scale=None, norm_
     seq_starts (int32, on the device) packs sequences end to end into B = 1:
     sequence s is tokens seq_starts[s] .. seq_starts[s + 1] - 1.  Rows of y
     outside every sequence are not written.  No output may overlap an input.
+    (A single long document is faster as a row, without seq_starts.)
 
     ckpt is the record gdr_backward consumes.  ``out`` may supply (y, sT,
     ckpt) tensors (None entries are allocated when wanted)."""

@@ -11,7 +11,9 @@
 // chip: at 4 rows of 32 heads of 128 x 128 that is 512 workgroups.
 // Measured: 256 rows of 32 heads of 64 x 64, fp32, 277 MB: 44 us, 6.3 TB/s
 // (above a copy's rate: half of it stays in the last-level cache); 4 rows of
-// 16 / 32 heads of 128 x 128, bf16, 17 MB: 7 us, most of it latency.
+// 16 / 32 heads of 128 x 128, bf16, 17 MB: 7 us, most of it latency.  More tokens
+// cost their chain of row sums: 4 tokens of each of the 256 rows 60 us; 8 of each
+// of 64 rows of 16 / 32 heads of 128 x 128, bf16, 115 us for 285 MB.
 //
 // Thread t owns columns 4 (t mod TPR) .. of row m RPP + t / TPR, m < RPT; row
 // dots are sums over the TPR lanes of a row in a fixed order.

@@ -29,13 +29,17 @@
 // by columns for F.  By rows it meets k_j beta_j rk_j, by columns q and k as
 // passed, exact in bf16.
 //
-// Measured, bf16: 8 x 4096 x 32, K = V = 64: 0.53 ms for 1.7 GB (3.2 TB/s);
-// 4 x 4096 x 8 / 16 heads, K = V = 128: 0.41 ms for 0.9 GB.  The time goes to
-// turns of loading, LDS and products that at three and one workgroups to a
-// compute unit overlap only in part.  Loading the next block, or the next
-// head's first, before the products did not help (443, 470 against 433 us at
-// K = 128), values 64 at a time did (421 us), and S and D by [V][K] (413 mean),
-// two workgroups instead of three at K = 64 took 640 against 619 us.
+// Measured, bf16: 8 x 4096 x 32, K = V = 64: 0.49 ms for 1.8 GB (3.6 TB/s); 4 x
+// 4096 x 8 / 16 heads, K = V = 128: 0.42 ms for 1.0 GB; fp32, 8 x 4096 x 32, K = V =
+// 64: 0.83 ms.  The time goes to turns of loading, LDS and products that at three
+// and one workgroups to a compute unit overlap only in part: the matrix units are
+// busy 0.25 and 0.21 of it, LDS waits for banks in 0.26 and 0.20.  dg without the
+// cancelling sums took whole calls from 1091 to 1131 us at K = 128 and from 1123 to
+// 1128 at K = 64.  When this form was chosen,
+// loading the next block, or the next head's first, before the products did not
+// help (443, 470 against 433 us at K = 128), values 64 at a time did (421), and S
+// and D by [V][K] (413); two workgroups instead of three at K = 64 took 640 against
+// 619 us.
 
 #include "gdr_factor.h"
 

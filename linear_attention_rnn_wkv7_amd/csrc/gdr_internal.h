@@ -34,13 +34,18 @@ struct Map {
 
 // Whether the scans' workgroups make the chunks' triangular factors themselves
 // (gdr_scan.hip) or find them in memory, made by a kernel before (gdr_prep.hip).
-// In memory they cost 26 KB (forward) and 31 KB (reverse) per chunk and head,
-// written and read, against 32 KB of inputs and outputs at K = V = 64 in bf16:
-// there the scan at 8 x 4096 x 32 takes 313 us instead of 394 us and 186 us for
-// the kernel before it.  With wider heads or fp32 the making of a chunk's
-// factors takes longer than its slabs do (fp32, same shape: 820 us against
-// 459 + 264; K = V = 128, 4 x 4096 x 16: 474 against 420 + 43), and with few
-// workgroups the waves that make them would idle the chip.
+// In memory they cost 31 KB per chunk and head, written and read, against 32 KB
+// of inputs and outputs at K = V = 64 in bf16: there calls take, made here
+// against made before, 248 us against 404 (8 x 4096 x 32, forward) and 812 against
+// 982 (backward).  With V = 128 each of a head's two workgroups makes them: 473
+// and 482 us.  In fp32 the making of a chunk's factors takes longer than its slabs
+// do: 750 and 550.  With K = 128 there is no room in LDS.  Below 128 heads in
+// flight it gains little (1 x 960 x 32: 53 and 57 us), and long rows run in
+// segments, which read the factors twice.  Packed sequences count as heads in
+// flight whatever their lengths, which only the device knows (x 32 heads, 24 of
+// 12288 tokens together: 136 and 187 us; 8 of 32768: 322 and 445); where most of
+// them are shorter than a chunk the factors are better made before (300 of 40
+// tokens: 412 and 320; one of 12288 beside 40 of one: 702 and 607).
 inline bool scan_makes_factors(int dtype, int64_t K, int64_t V, int64_t units)
 {
     return dtype == WKV7_BF16 && K == 64 && V <= 64 && units >= 128;
@@ -54,8 +59,9 @@ constexpr int kMakers = 4;
 // factors, a key head's value heads the same q and k: they go to one die, whose
 // cache then holds them for all, unless that leaves a die with more than an
 // eighth above its share and its 32 compute units.  (4 x 4096 x 8 / 16 heads, K =
-// V = 128, bf16, four groups: reverse 332 -> 319 us, forward 315 -> 310; 24 packed
-// sequences of 12288 tokens, 16 / 32 heads, one group: 212 -> 209.)
+// V = 128, bf16, four groups, apart and together: forward 332 and 314 us, reverse
+// 305 and 291; with one group to a head it makes no difference: 24 packed sequences
+// of 12288 tokens, 16 / 32 heads, 224 and 222.)
 struct ScanGrid {
     int64_t slabs;                  // of a workgroup
     int64_t groups, share, total;   // slab groups of a unit, neighbours on a die, workgroups with work

@@ -12,10 +12,11 @@
 // added up by a second kernel in a fixed order.
 //
 // Measured, bf16: epilogue at 8 x 4096 x 32 heads of 64: forward 82 us for 403
-// MB (4.9 TB/s), backward 130 us for 671 MB (5.2) and 16 us for the sums;
-// residual norm at 32768 rows of 2048: forward 96 us for 537 MB (5.6 TB/s),
-// backward with scale 172 us for 805 MB (4.7) and 2 x 7 us.  bf16 rows whose
-// length is no multiple of 8 go by 2 bytes a lane: 1.3 to 2.4 TB/s.
+// MB (4.9 TB/s), backward 128 us for 671 MB (5.2) and 15 us for the sums;
+// residual norm at 32768 rows of 2048: forward 95 us for 537 MB (5.7 TB/s),
+// backward with scale 170 us for 805 MB (4.7) and 2 x 7 us.  bf16 rows whose
+// length is no multiple of 8 go by 2 bytes a lane: at 2047 and 2050 forward 204
+// and 340 us (2.6 and 1.6 TB/s), backward with scale 928 and 992 us (0.9 and 0.8).
 
 #include "gdr_device.h"
 
@@ -250,9 +251,11 @@ __device__ __forceinline__ void put8(T *row, int i, int t, int D, f32x8 x)
 }
 
 // Such a piece as it lies in memory: half the registers for bf16 (backward with
-// scale, 2^26 values in rows of 1024: 271 -> 225 us, 4096: 236 -> 195, 16384: 403
-// -> 245; of 2048, where there were enough: 176 -> 182).  again() hides that the
-// values have been widened before, or the compiler would keep them wide.
+// scale, 2^26 values, wide against as they lie: rows of 1024 271 and 225 us, 4096
+// 236 and 195, 16384 403 and 245, 256 263 and 213, 5120 233 and 187, 8192 203 and
+// 191; only where a row fills its threads and they had registers enough it loses,
+// 512: 203 and 211, 2048: 174 and 182).  again() hides that the values have been
+// widened before, or the compiler would keep them wide.
 template <typename T, bool kVec>
 struct Piece {
     f32x8 x;

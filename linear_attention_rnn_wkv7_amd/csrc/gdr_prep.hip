@@ -1,9 +1,9 @@
 // The triangular factors (gdr_factor.h) of every chunk and value head in
 // memory, for the scans that do not make them themselves.  One wave per chunk
 // and head, four to a workgroup: nothing waits at a barrier.  Bound by what it
-// writes: 26 KB (bf16) per chunk and head against 16 or 32 KB read.  Measured:
-// 6144 chunks and heads, K = 128, bf16: 78 us, 4.6 TB/s; 16384, K = 64, fp32:
-// 214 us, 4 TB/s.
+// moves: 31 KB (bf16) written per chunk and head, 16 or 32 KB read.  Measured:
+// 6560 chunks and heads, K = 128, shared keys, bf16: 81 us for 318 MB, 3.9 TB/s;
+// 16384, K = 64, fp32 (21 KB written): 203 us for 898 MB, 4.4 TB/s.
 
 #include "gdr_factor.h"
 

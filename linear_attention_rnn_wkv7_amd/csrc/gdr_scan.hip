@@ -20,16 +20,17 @@
 // K columns that start as the identity and see no values, which gives the
 // segment's L and M; a small kernel runs through the segments of a row; the
 // second pass starts each from its own state.  (Reverse the same way.)  At 1 x
-// 65536 x 32, K = V = 64, bf16, in 8 segments: 0.39 ms for each of the passes
-// and 0.03 between (the whole call 2.84 ms in one piece, 1.19 in segments when
-// they came).
+// 65536 x 32, K = V = 64, bf16, in 8 segments: 0.35 and 0.46 ms for the passes,
+// 0.03 between and 0.29 for the factors, 1.12 ms in all; in one piece (as packed
+// sequences run) 2.54 ms after the factors.
 //
 // What bounds them.  fp32: the fp32 matrix instruction (8 x 4096 x 32, K = V =
-// 64: 37 GFLOP in 0.39 ms, 95 TFLOP/s of 157).  bf16: the chain of one chunk,
-// about 1100 instructions of one wave at K = 64 and one such wave per SIMD (the
-// same shape: 0.30 and 0.33 ms, 64 steps of about 5 us); at K = 128 twice as
-// many, on half of the SIMDs where there are 64 heads (4 x 4096 x 16: 0.29 and
-// 0.31 ms).
+// 64: 39 GFLOP in 0.34 ms, 112 TFLOP/s of 157; the matrix units are busy 0.7 of
+// the time).  bf16: the chain of one chunk, 750 vector and 170 other instructions
+// of one wave at K = 64 and one such wave per SIMD (8 x 4096 x 32, with the record:
+// 0.30 and 0.32 ms, 64 steps of about 5 us, matrix units busy 0.25 to 0.28); at K =
+// 128 1040 and 270, on half of the SIMDs where there are 64 heads (4 x 4096 x 16:
+// 0.30 and 0.29 ms, busy 0.15).
 
 #include "gdr_factor.h"
 
