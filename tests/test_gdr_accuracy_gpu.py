@@ -5,7 +5,7 @@ import torch
 
 import oracle.gdr as R
 from linear_attention_rnn_wkv7_amd import api
-from test_gdr_gpu import BF16, F32, HALF_STEP, IN, inputs
+from test_gdr_gpu import BF16, F32, HALF_STEP
 
 pytestmark = pytest.mark.gpu
 

@@ -5,7 +5,7 @@ import ctypes
 import torch
 
 import linear_attention_rnn_wkv7_amd as pkg
-from linear_attention_rnn_wkv7_amd import _lib, api
+from linear_attention_rnn_wkv7_amd import _lib
 
 
 def test_norm_workspace_sizes():

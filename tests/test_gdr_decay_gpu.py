@@ -10,7 +10,6 @@ import pytest
 import torch
 
 import oracle.gdr as R
-from linear_attention_rnn_wkv7_amd import api
 from test_gdr_gpu import BF16, F32, IN, REL, inputs, run
 
 pytestmark = pytest.mark.gpu
