@@ -27,6 +27,10 @@ GDR_EXPORTS = ("gdr_checkpoint_bytes", "gdr_forward_workspace_bytes", "gdr_backw
                "gdr_epilogue_forward", "gdr_epilogue_backward")
 RESIDUAL_NORM_EXPORTS = ("residual_norm_workspace_bytes", "residual_norm_forward",
                          "residual_norm_backward")
+# ... include/attention.h
+ATTENTION_EXPORTS = ("attn_record_bytes", "attn_backward_workspace_bytes", "attn_forward", "attn_backward",
+                     "qk_norm_workspace_bytes", "qk_norm_forward", "qk_norm_backward", "kv_write", "kv_read",
+                     "attn_decode_workspace_bytes", "attn_decode")
 WKV7_FAULT_RWKV8_DECAY = 2
 
 WKV7_NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -68,6 +72,40 @@ class GdrEpilogueShape(ctypes.Structure):
 class ResidualNormShape(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("nseq", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+QK_NORM_INTERLEAVED = 1   # qk_norm_shape.flags bit
+
+
+class QkNormShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("R", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+KV_CACHE_SAME, KV_CACHE_E4M3 = 0, 1
+
+
+class KvCacheShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("T", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("packed", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32)]
+
+
+class AttnDecodeShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("D", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("cache_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class Wkv7Error(RuntimeError):
@@ -124,6 +162,7 @@ def lib():
     L.rwkv8_backward.argtypes = [s8] + [vp] * 14 + [vp, sz, vp]
     L.rwkv8_backward.restype = i32
     sg, se, sn = (ctypes.POINTER(x) for x in (GdrShape, GdrEpilogueShape, ResidualNormShape))
+    sa, sq, sc, sd = (ctypes.POINTER(x) for x in (AttnShape, QkNormShape, KvCacheShape, AttnDecodeShape))
     i64 = ctypes.c_int64
     for name, args, res in (
             ("gdr_checkpoint_bytes", [sg], sz),
@@ -137,7 +176,18 @@ def lib():
             ("gdr_epilogue_backward", [se] + [vp] * 7 + [vp, sz, vp], i32),
             ("residual_norm_workspace_bytes", [sn], sz),
             ("residual_norm_forward", [sn] + [vp] * 6 + [vp], i32),
-            ("residual_norm_backward", [sn] + [vp] * 10 + [vp, sz, vp], i32)):
+            ("residual_norm_backward", [sn] + [vp] * 10 + [vp, sz, vp], i32),
+            ("attn_record_bytes", [sa], sz),
+            ("attn_backward_workspace_bytes", [sa], sz),
+            ("attn_forward", [sa] + [vp] * 7 + [vp], i32),
+            ("attn_backward", [sa] + [vp] * 11 + [vp, sz, vp], i32),
+            ("qk_norm_workspace_bytes", [sq], sz),
+            ("qk_norm_forward", [sq] + [vp] * 8 + [vp], i32),
+            ("qk_norm_backward", [sq] + [vp] * 12 + [vp, sz, vp], i32),
+            ("kv_write", [sc] + [vp] * 9 + [vp], i32),
+            ("kv_read", [sc] + [vp] * 9 + [vp], i32),
+            ("attn_decode_workspace_bytes", [sd], sz),
+            ("attn_decode", [sd] + [vp] * 8 + [vp, sz, vp], i32)):
         f = getattr(L, name)
         f.argtypes, f.restype = args, res
     _LIB = L

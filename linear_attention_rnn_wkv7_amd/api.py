@@ -658,3 +658,374 @@ def residual_norm_backward(dh, dx_out, x_out, w, y=None, scale=None, *, eps=1e-6
         return grads
 
     return _launch("residual_norm_backward", at, stream, call)
+
+
+# --------------------------------------------------------- softmax attention
+
+def _token_stride(name, t, heads, D, dtype, index, B=None, T=None):
+    """Checks [B, T, heads, D] with heads end to end and rows one after the
+    other; returns the elements from a token to the next (0: contiguous)."""
+    if t is None or t.dim() != 4 or t.dtype != dtype or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor [B, T, heads, D] on cuda:{index}")
+    b, n, h, d = t.shape
+    if d != D or h != heads or (B is not None and (b, n) != (B, T)):
+        raise ValueError(f"{name} must be [{b if B is None else B}, {n if T is None else T}, {heads}, {D}]")
+    if t.is_contiguous():
+        return 0
+    s = t.stride()
+    step = s[1] if n > 1 else s[0] if b > 1 else 0
+    if s[3] != 1 or (h > 1 and s[2] != D) or (b > 1 and s[0] != n * step) or step % 8 != 0 or (step and step < h * D):
+        raise ValueError(f"{name}: a token's heads must lie end to end, tokens and rows at one stride, a multiple of 8")
+    return step
+
+
+def _heads(name, q, k):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+    if q.dtype not in _VEC_DTYPES:
+        raise ValueError(f"{name}: dtype {q.dtype} not supported")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+
+
+def _int32(name, t, shape, index):
+    if t is None or t.dtype != torch.int32 or t.shape != shape or not t.is_cuda or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_sizes(*key):
+    sh = _lib.AttnShape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, _lib.lib().attn_record_bytes(r), _lib.lib().attn_backward_workspace_bytes(r)
+
+
+def _attn_key(B, T, Hq, Hk, D, dtype, nseq=0, strides=(0, 0, 0), scale=None):
+    if scale is None:
+        scale = D ** -0.5 if D > 0 else 1.0   # the library refuses other D
+    return (B, T, Hq, Hk, D, nseq, *strides, _VEC_DTYPES[dtype], 0, float(scale))
+
+
+def attn_record_bytes(B, T, Hq, Hk, D, dtype=torch.bfloat16, nseq=0):
+    return _attn_sizes(*_attn_key(B, T, Hq, Hk, D, dtype, nseq))[2]
+
+
+def attn_backward_workspace_bytes(B, T, Hq, Hk, D, dtype=torch.bfloat16, nseq=0):
+    return _attn_sizes(*_attn_key(B, T, Hq, Hk, D, dtype, nseq))[3]
+
+
+def _attn_dims(q, k, v, seq_starts, scale):
+    _heads("q", q, k)
+    dt, at = q.dtype, q.get_device()
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    if Hk == 0 or Hq == 0 or Hq % Hk != 0:
+        raise ValueError(f"q has {Hq} heads: not a multiple of k's {Hk}")
+    strides = (_token_stride("q", q, Hq, D, dt, at), _token_stride("k", k, Hk, D, dt, at, B, T),
+               _token_stride("v", v, Hk, D, dt, at, B, T))
+    nseq = 0
+    if seq_starts is not None:
+        nseq = seq_starts.numel() - 1
+        if B != 1 or nseq < 1:
+            raise ValueError("seq_starts needs B = 1 and at least two entries")
+        _int32("seq_starts", seq_starts, (nseq + 1,), at)
+    return _attn_sizes(*_attn_key(B, T, Hq, Hk, D, dt, nseq, strides, scale)), (B, T, Hq, D), (B, T, Hk, D), at
+
+
+def attn_forward(q, k, v, *, seq_starts=None, scale=None, want_lse=False, want_record=False, stream=None, out=None):
+    """Causal softmax attention over whole sequences (attn_forward):
+    y_i = sum over j <= i of exp(scale q_i . k_j - lse_i) v_j.  Returns
+    (y, lse, record); unwanted outputs are None.
+
+    q [B, T, Hq, D], k, v [B, T, Hk, D] fp32 or bf16, D 64 or 128, Hq a multiple
+    of Hk; each may be part of a wider tensor (heads end to end, one stride from
+    token to token).  scale defaults to D ** -0.5 and is positive.  lse
+    [B, T, Hq] fp32.
+
+    seq_starts (int32, on the device) packs sequences end to end into B = 1:
+    sequence s is tokens seq_starts[s] .. seq_starts[s + 1] - 1.  Rows of y and
+    lse outside every sequence are not written.  No output may overlap an input.
+
+    attn_backward takes y, lse and (bf16; with fp32 there is none) record.
+    ``out`` may supply (y, lse, record) tensors (None entries are allocated when
+    wanted)."""
+    (_, sh, rec_bytes, _), ys, _, at = _attn_dims(q, k, v, seq_starts, scale)
+    y, lse, rec = out if out is not None else (None, None, None)
+
+    def call(st):
+        y_ = _output("y", y, ys, q.dtype, at)
+        lse_ = _output("lse", lse, ys[:3], torch.float32, at) if want_lse else None
+        rec_ = _output("record", rec, ys, q.dtype, at) if want_record and q.dtype == torch.bfloat16 else None
+        rc = _lib.lib().attn_forward(sh, *map(_at, (q, k, v, seq_starts, y_, lse_, rec_)), st)
+        _lib.check("attn_forward", rc)
+        return y_, lse_, rec_
+
+    return _launch("attn_forward", at, stream, call)
+
+
+def attn_backward(q, k, v, y, lse, dy, record=None, *, seq_starts=None, scale=None, workspace=None, stream=None,
+                  out=None):
+    """The gradients of attn_forward (attn_backward), with the same inputs and
+    options and its y, lse and record: dict(dq, dk, dv), contiguous, dk and dv
+    summed over the query heads that read them.  Without the record y's own
+    rounding to bf16 enters dq and dk."""
+    (_, sh, _, need), ys, ks, at = _attn_dims(q, k, v, seq_starts, scale)
+    _check_like("y", y, ys, q.dtype, at)
+    _check_like("dy", dy, ys, q.dtype, at)
+    _check_like("lse", lse, ys[:3], torch.float32, at)
+    if record is not None and q.dtype != torch.bfloat16:
+        raise ValueError("record is for bf16 inputs")
+    _check_like("record", record, ys, q.dtype, at, optional=True)
+    grads = dict(out) if out is not None else {}
+
+    def call(st):
+        for n, shape in (("dq", ys), ("dk", ks), ("dv", ks)):
+            grads[n] = _output(n, grads.get(n), shape, q.dtype, at)
+        ws, wp, wb = _workspace("attn_backward", workspace, need, at)
+        rc = _lib.lib().attn_backward(sh, *map(_at, (q, k, v, seq_starts, y, lse, record, dy)),
+                                      *(_at(grads[n]) for n in ("dq", "dk", "dv")), wp, wb, st)
+        _lib.check("attn_backward", rc)
+        return grads
+
+    return _launch("attn_backward", at, stream, call)
+
+
+# ----------------------------------------- the norm and rotation before it
+
+@functools.lru_cache(maxsize=256)
+def _qk_norm_sizes(*key):
+    sh = _lib.QkNormShape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, _lib.lib().qk_norm_workspace_bytes(r)
+
+
+def qk_norm_workspace_bytes(B, T, Hq, Hk, D, dtype=torch.bfloat16):
+    """Of qk_norm_backward with weights."""
+    return _qk_norm_sizes(B, T, Hq, Hk, D, 0, 0, 0, _VEC_DTYPES[dtype], 0, 1e-6)[2]
+
+
+def _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved):
+    _heads("q", q, k)
+    dt, at = q.dtype, q.get_device()
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    strides = (_token_stride("q", q, Hq, D, dt, at), _token_stride("k", k, Hk, D, dt, at, B, T))
+    if (wq is None) != (wk is None):
+        raise ValueError("wq and wk come together")
+    _check_like("wq", wq, (D,), torch.float32, at, optional=True)
+    _check_like("wk", wk, (D,), torch.float32, at, optional=True)
+    R = 0
+    if theta is not None:
+        R = 2 * theta.numel()
+        if theta.numel() == 0 or R > D:
+            raise ValueError(f"theta must have 1 to {D // 2} entries")
+        _check_like("theta", theta, (R // 2,), torch.float32, at)
+    if positions is not None:
+        _int32("positions", positions, (B, T), at)
+    key = (B, T, Hq, Hk, D, R, *strides, _VEC_DTYPES[dt], _lib.QK_NORM_INTERLEAVED if interleaved else 0, float(eps))
+    return _qk_norm_sizes(*key), (B, T, Hq, D), (B, T, Hk, D), at
+
+
+def qk_norm_forward(q, k, wq=None, wk=None, theta=None, positions=None, *, eps=1e-6, interleaved=False, stream=None,
+                    out=None):
+    """The norm of queries and keys per head and their rotation, in one pass
+    (qk_norm_forward): n = x / sqrt(mean(x^2) + eps) * w over a head's D
+    entries (no weights: n = x), then the pairs of its first R entries turned by
+    positions * theta (no theta: none).  Returns (q', k'), contiguous.
+
+    q [B, T, Hq, D], k [B, T, Hk, D] fp32 or bf16, D 64 or 128, each may be part
+    of a wider tensor; wq, wk [D], theta [R / 2] fp32, R a multiple of 16 up to
+    D; positions int32 [B, T], by default 0 .. T - 1 in each row.  Pair i is
+    (n[i], n[i + R / 2]), or with ``interleaved`` (n[2 i], n[2 i + 1]).  Angles
+    are formed in fp64.  ``out`` may supply (q', k'); contiguous q and k
+    themselves are allowed there."""
+    (_, sh, _), qs, ks, at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
+    qz, kz = out if out is not None else (None, None)
+
+    def call(st):
+        qz_ = _output("q'", qz, qs, q.dtype, at)
+        kz_ = _output("k'", kz, ks, q.dtype, at)
+        rc = _lib.lib().qk_norm_forward(sh, *map(_at, (q, k, wq, wk, theta, positions, qz_, kz_)), st)
+        _lib.check("qk_norm_forward", rc)
+        return qz_, kz_
+
+    return _launch("qk_norm_forward", at, stream, call)
+
+
+def qk_norm_backward(dqz, dkz, q, k, wq=None, wk=None, theta=None, positions=None, *, eps=1e-6, interleaved=False,
+                     workspace=None, stream=None, out=None):
+    """The gradients of qk_norm_forward from those of q' and k', with its
+    inputs and options: dict(dq, dk, dwq, dwk), the weights' in fp32 and None
+    without weights.  ``out`` may supply them; dq and dk may be dqz and dkz."""
+    (_, sh, need), qs, ks, at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
+    _check_like("dqz", dqz, qs, q.dtype, at)
+    _check_like("dkz", dkz, ks, q.dtype, at)
+    normed = wq is not None
+    grads = dict(out) if out is not None else {}
+
+    def call(st):
+        grads["dq"] = _output("dq", grads.get("dq"), qs, q.dtype, at)
+        grads["dk"] = _output("dk", grads.get("dk"), ks, q.dtype, at)
+        for n in ("dwq", "dwk"):
+            grads[n] = _output(n, grads.get(n), qs[3:], torch.float32, at) if normed else None
+        ws, wp, wb = _workspace("qk_norm_backward", workspace, need if normed else 0, at)
+        rc = _lib.lib().qk_norm_backward(sh, *map(_at, (dqz, dkz, q, k, wq, wk, theta, positions)),
+                                         *(_at(grads[n]) for n in ("dq", "dk", "dwq", "dwk")), wp, wb, st)
+        _lib.check("qk_norm_backward", rc)
+        return grads
+
+    return _launch("qk_norm_backward", at, stream, call)
+
+
+# ----------------------------------------------------------- the paged cache
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dtype, at):
+    """Checks a cache against the type of the tokens; returns pages, Hk, page,
+    D, rows, max_pages and the library's name of its type."""
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_pages must be [pages, Hk, page, D] and table [rows, max_pages]")
+    if k_pages.dtype not in (dtype, _E4M3):
+        raise ValueError(f"k_pages: {k_pages.dtype} does not go with {dtype}: the same, or {_E4M3}")
+    ps = k_pages.shape
+    _check_like("k_pages", k_pages, ps, k_pages.dtype, at)
+    _check_like("v_pages", v_pages, ps, k_pages.dtype, at)
+    rows, most = table.shape
+    _int32("table", table, (rows, most), at)
+    _int32("lens", lens, (rows,), at)
+    small = k_pages.dtype == _E4M3
+    if small:
+        _check_like("k_scale", k_scale, ps[:3], torch.float32, at)
+        _check_like("v_scale", v_scale, ps[:3], torch.float32, at)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale and v_scale are for an 8-bit cache")
+    return (*ps, rows, most, _lib.KV_CACHE_E4M3 if small else _lib.KV_CACHE_SAME)
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_shape(*key):
+    sh = _lib.KvCacheShape(*key)
+    return sh, ctypes.byref(sh)
+
+
+def kv_write(k, v, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *, seq_starts=None, stream=None):
+    """Writes new tokens' keys and values into their pages (kv_write), in place.
+
+    k, v [B, T, Hk, D] fp32 or bf16 (each may be part of a wider tensor): the T
+    last tokens of each of B rows, or with seq_starts (int32 [B + 1], on the
+    device; k and v [1, tokens, Hk, D]) tokens seq_starts[r] .. seq_starts[r + 1]
+    - 1 the last of row r.  Row r holds lens[r] tokens, the new ones among them
+    (int32 [B]), in the pages table[r] (int32 [B, max_pages]), in order.
+    k_pages, v_pages [pages, Hk, page, D] in k's type, or float8_e4m3fn with
+    k_scale, v_scale [pages, Hk, page] fp32: each token's head is stored times
+    448 / max|x|.  page is a power of two from 16 to 256.
+
+    Tokens at positions below 0, past the table or in a page outside the pool
+    are not written.  Two rows may share pages, but not write one place."""
+    if k.dim() != 4 or k.dtype not in _VEC_DTYPES or not k.is_cuda:
+        raise ValueError("k must be an fp32 or bf16 device tensor [B, T, Hk, D]")
+    at, dt = k.get_device(), k.dtype
+    pages, Hk, page, D, rows, most, kind = _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dt, at)
+    B, T = k.shape[:2]
+    sk = _token_stride("k", k, Hk, D, dt, at)
+    sv = _token_stride("v", v, Hk, D, dt, at, B, T)
+    packed = _packed_rows(seq_starts, B, rows, at)
+    _, sh = _cache_shape(rows, T, Hk, D, packed, pages, page, most, sk, sv, _VEC_DTYPES[dt], kind)
+
+    def call(st):
+        rc = _lib.lib().kv_write(sh, *map(_at, (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, seq_starts)), st)
+        _lib.check("kv_write", rc)
+
+    return _launch("kv_write", at, stream, call)
+
+
+def _packed_rows(seq_starts, B, rows, at):
+    if seq_starts is None:
+        if B != rows:
+            raise ValueError(f"{B} rows of tokens for a table of {rows}")
+        return 0
+    if B != 1:
+        raise ValueError("seq_starts needs B = 1")
+    _int32("seq_starts", seq_starts, (rows + 1,), at)
+    return 1
+
+
+def kv_read(k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *, T, seq_starts=None, dtype=None, stream=None,
+            out=None):
+    """The reverse of kv_write (kv_read): the T last tokens of each row, [rows,
+    T, Hk, D], or with seq_starts the seq_starts[r + 1] - seq_starts[r] last ones
+    of row r, end to end, [1, T, Hk, D] (rows outside every sequence are not
+    written).  ``dtype`` is fp32 or bf16: the cache's own, or, by default bf16,
+    what an 8-bit cache's values times their scales are rounded to.  Tokens
+    that kv_write would not write are zeros.  Returns (k, v); ``out`` may supply
+    them."""
+    at = k_pages.get_device()
+    if not k_pages.is_cuda:
+        raise ValueError("k_pages must be a device tensor")
+    if dtype is None:
+        dtype = torch.bfloat16 if k_pages.dtype == _E4M3 else k_pages.dtype
+    if dtype not in _VEC_DTYPES:
+        raise ValueError(f"kv_read: dtype {dtype} not supported")
+    if T < 0:
+        raise ValueError("T is negative")
+    pages, Hk, page, D, rows, most, kind = _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dtype, at)
+    packed = _packed_rows(seq_starts, rows if seq_starts is None else 1, rows, at)
+    shape = (1 if packed else rows, T, Hk, D)
+    _, sh = _cache_shape(rows, T, Hk, D, packed, pages, page, most, 0, 0, _VEC_DTYPES[dtype], kind)
+    k, v = out if out is not None else (None, None)
+
+    def call(st):
+        k_, v_ = _output("k", k, shape, dtype, at), _output("v", v, shape, dtype, at)
+        rc = _lib.lib().kv_read(sh, *map(_at, (k_pages, v_pages, k_scale, v_scale, table, lens, seq_starts, k_, v_)), st)
+        _lib.check("kv_read", rc)
+        return k_, v_
+
+    return _launch("kv_read", at, stream, call)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_sizes(*key):
+    sh = _lib.AttnDecodeShape(*key)
+    r = ctypes.byref(sh)
+    return sh, r, _lib.lib().attn_decode_workspace_bytes(r)
+
+
+def attn_decode_workspace_bytes(B, T, Hq, Hk, D, pages, page, max_pages, dtype=torch.bfloat16):
+    return _decode_sizes(B, T, Hq, Hk, D, pages, page, max_pages, 0, _VEC_DTYPES[dtype], _lib.KV_CACHE_SAME, 1.0)[2]
+
+
+def attn_decode(q, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *, scale=None, workspace=None,
+                stream=None, out=None):
+    """Attention of each row's T last tokens over the paged cache (attn_decode),
+    which holds their keys and values already (kv_write); token t of row b sees
+    the positions below lens[b] - (T - 1 - t).  Returns y [B, T, Hq, D].
+
+    q [B, T, Hq, D] fp32 or bf16 (may be part of a wider tensor); the cache as
+    for kv_write, in q's type or float8_e4m3fn.  scale defaults to D ** -0.5 and
+    is positive.  Positions in a page outside the pool are seen by nobody; a
+    token that sees nothing has y = 0."""
+    if q.dim() != 4 or q.dtype not in _VEC_DTYPES or not q.is_cuda:
+        raise ValueError("q must be an fp32 or bf16 device tensor [B, T, Hq, D]")
+    at, dt = q.get_device(), q.dtype
+    pages, Hk, page, D, rows, most, kind = _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dt, at)
+    B, T, Hq, Dq = ys = q.shape
+    if B != rows:
+        raise ValueError(f"{B} rows of q for a table of {rows}")
+    if Hk == 0 or Hq == 0 or Hq % Hk != 0:
+        raise ValueError(f"q has {Hq} heads: not a multiple of the cache's {Hk}")
+    sq = _token_stride("q", q, Hq, D, dt, at)
+    if scale is None:
+        scale = D ** -0.5 if D > 0 else 1.0
+    _, sh, need = _decode_sizes(B, T, Hq, Hk, D, pages, page, most, sq, _VEC_DTYPES[dt], kind, float(scale))
+
+    def call(st):
+        y = _output("y", out, ys, dt, at)
+        ws, wp, wb = _workspace("attn_decode", workspace, need, at)
+        rc = _lib.lib().attn_decode(sh, *map(_at, (q, k_pages, v_pages, k_scale, v_scale, table, lens, y)), wp, wb, st)
+        _lib.check("attn_decode", rc)
+        return y
+
+    return _launch("attn_decode", at, stream, call)

@@ -1,0 +1,388 @@
+// Attention of new tokens over the paged cache.
+//
+// Bound by the bytes of the cache: the queries of all heads that share a key
+// head (and of all new tokens) go over it together, kDecodeRows to a
+// workgroup, and few of them leave the matrix units idle most of the time, so
+// the weights take part in two bf16 parts at no cost.  The cache of a row is cut
+// into `splits` parts of whole steps; within a workgroup each wave takes
+// every fourth step of the part by itself, with its own running maximum, sum
+// and O^T, without a barrier: the next step's keys and values are on their
+// way to registers while one is computed, and go to LDS of the wave's own.  The
+// waves are joined through LDS, the parts by a second kernel, both in order.
+
+#include "attn_device.h"
+
+namespace wkv7 {
+namespace attn {
+namespace {
+
+template <typename T>
+struct DecArgs {
+    const T *q;
+    const char *k, *v;
+    const float *k_scale, *v_scale;
+    const int32_t *table, *lens;
+    T *y;
+    float *part_o;
+    f32x2 *part_ml;
+    int64_t T_, Hq, Hk, pages, max_pages, q_stride, rows;   // rows: T_ times group
+    int group, log_page, splits;
+    float scale;
+};
+
+struct E4m3 {
+    uint8_t x;
+};
+
+// 16 bytes of the cache as values of T.
+template <typename T, typename C>
+struct Widen;
+template <typename T>
+struct Widen<T, T> {
+    static constexpr int kPieces = 1;   // 16-byte pieces of T
+    __device__ static __forceinline__ void to(f32x4 x, f32x4 (&y)[1]) { y[0] = x; }
+};
+template <>
+struct Widen<bf16, E4m3> {
+    static constexpr int kPieces = 2;
+    __device__ static __forceinline__ void to(f32x4 x, f32x4 (&y)[2])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = x[i];
+            const int u = __builtin_bit_cast(int, f);
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(u, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(u, true);
+            y[i >> 1][2 * (i & 1)] = __builtin_bit_cast(float, pack_bf16(a[0], a[1]));
+            y[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(float, pack_bf16(b[0], b[1]));
+        }
+    }
+};
+template <>
+struct Widen<float, E4m3> {
+    static constexpr int kPieces = 4;
+    __device__ static __forceinline__ void to(f32x4 x, f32x4 (&y)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = x[i];
+            const int u = __builtin_bit_cast(int, f);
+            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(u, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(u, true);
+            y[i] = f32x4{a[0], a[1], b[0], b[1]};
+        }
+    }
+};
+
+// The 32 tokens of a step: two halves of 16, each in one page.
+template <typename T, typename C, int D>
+struct Step {
+    static constexpr int kBytes = 32 * D * (int)sizeof(C), kLoads = kBytes / 1024;
+    static constexpr bool kE4m3 = sizeof(C) == 1;
+    f32x4 k[kLoads], v[kLoads];
+    float ks, vs;       // of token lane % 32
+    bool there[2];      // the halves' pages
+
+    // `n` tokens of the row from tok0 on are there.
+    __device__ __forceinline__ void load(const DecArgs<T> &p, const int32_t *table, int64_t hk, int64_t tok0, int64_t n,
+                                         int lane)
+    {
+        int64_t at[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t tok = tok0 + 16 * i;
+            int page = -1;
+            if (16 * i < n && (tok >> p.log_page) < p.max_pages) page = table[tok >> p.log_page];
+            page = __builtin_amdgcn_readfirstlane(page);
+            there[i] = page >= 0 && page < p.pages;
+            at[i] = ((((there[i] ? page : 0) * p.Hk + hk) << p.log_page) + (tok & ((1 << p.log_page) - 1))) * D;
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int hf = i / (kLoads / 2);
+            k[i] = v[i] = gdr::zero4();
+            if (there[hf]) {
+                const int64_t o = at[hf] * (int64_t)sizeof(C) + (i % (kLoads / 2)) * 1024 + lane * 16;
+                k[i] = *reinterpret_cast<const f32x4 *>(p.k + o);
+                // what lies behind the row's end may be anything, a NaN too
+                const int row = (i * 1024 + lane * 16) / (D * (int)sizeof(C));
+                if (row < n) v[i] = *reinterpret_cast<const f32x4 *>(p.v + o);
+            }
+        }
+        if (kE4m3) {
+            const int hf = (lane >> 4) & 1;
+            ks = vs = 0.f;
+            if ((hf ? there[1] : there[0]) && (lane & 31) < n) {
+                const int64_t o = (hf ? at[1] : at[0]) / D + (lane & 15);
+                ks = p.k_scale[o];
+                vs = p.v_scale[o];
+            }
+        }
+    }
+    // Into LDS as tiles of T.
+    __device__ __forceinline__ void land(char *kt, char *vt, float *scales, int lane) const
+    {
+        using L = Tile<T, D>;
+        using W = Widen<T, C>;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int byte = i * 1024 + lane * 16, row = byte / (D * (int)sizeof(C));
+            const int piece = byte % (D * (int)sizeof(C)) / 16 * W::kPieces;
+            f32x4 x[W::kPieces], y[W::kPieces];
+            W::to(k[i], x);
+            W::to(v[i], y);
+#pragma unroll
+            for (int j = 0; j < W::kPieces; ++j) {
+                *reinterpret_cast<f32x4 *>(kt + L::at(row, piece + j)) = x[j];
+                *reinterpret_cast<f32x4 *>(vt + L::at(row, piece + j)) = y[j];
+            }
+        }
+        if (kE4m3 && lane < 32) {
+            scales[lane] = ks;
+            scales[32 + lane] = vs;
+        }
+    }
+};
+
+// Parts hi and lo of 16 weights' operand.
+template <typename T, int D>
+__device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w, const char *vt, int lane)
+{
+    using L = Tile<T, D>;
+    f32x16 rest;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const uint32_t u = pack_bf16(w[i], w[i + 1]);
+            rest[i] = w[i] - bf16_lo(u);
+            rest[i + 1] = w[i + 1] - bf16_hi(u);
+        }
+    }
+#pragma unroll
+    for (int ss = 0; ss < 2; ++ss) {
+        const Oct<T> a = as_operand<T>(w, ss);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) {
+            const Oct<T> x = L::col(vt, dt, ss, lane);
+            o[dt] = mma(x, a, o[dt]);
+            if constexpr (sizeof(T) == 2) o[dt] = mma(x, as_operand<T>(rest, ss), o[dt]);
+        }
+    }
+}
+
+template <typename T, typename C, int D>
+__global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
+{
+    using L = Tile<T, D>;
+    using S = Step<T, C, D>;
+    constexpr int kTileBytes = kDecodeStep * L::kPitch;
+    // a wave's tiles; then, of each wave, O by rows
+    constexpr int kOut = kDecodeRows * (D + 4) * 4;
+    constexpr int kWave = 2 * kTileBytes > kOut ? 2 * kTileBytes : kOut;
+    __shared__ __attribute__((aligned(16))) char lds[4][kWave];
+    __shared__ __attribute__((aligned(16))) float scales[4][64];
+    __shared__ float stat[4][2][kDecodeRows];   // maximum, sum
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, l32 = lane & 31;
+    const int64_t tiles = (p.rows + kDecodeRows - 1) / kDecodeRows;
+    const int64_t hk = blockIdx.y / tiles, tile = blockIdx.y - hk * tiles, b = blockIdx.z;
+    const int split = blockIdx.x;
+
+    int64_t len = p.lens[b];
+    const int64_t most = p.max_pages << p.log_page;
+    // a token sees `sees` positions; those past the table hold nothing
+    const int64_t r = tile * kDecodeRows + l32;
+    const int64_t t = r / p.group, hq = hk * p.group + (r - t * p.group);
+    const bool live = r < p.rows;
+    const int64_t sees = live ? len - (p.T_ - 1 - t) : 0;
+    len = len < 0 ? 0 : len < most ? len : most;
+    const int64_t steps = (len + kDecodeStep - 1) / kDecodeStep, per = (steps + p.splits - 1) / p.splits;
+    const int64_t last = (split + 1) * per < steps ? (split + 1) * per : steps;
+
+    Oct<T> q[D / 16];
+    {
+        const T *qp = p.q + (b * p.T_ + t) * p.q_stride + hq * D + 8 * half;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            q[ks] = zero_oct<T>();
+            if (live) q[ks] = *reinterpret_cast<const Oct<T> *>(qp + 16 * ks);
+        }
+    }
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
+    float ref = kNegInf, l = 0.f;   // ref: the maximum times c
+    const float c = p.scale * kLog2e;
+    char *kt = lds[wave], *vt = kt + kTileBytes;
+    const int32_t *table = p.table + b * p.max_pages;
+
+    S next;
+    int64_t at = split * per + wave;
+    if (at < last) next.load(p, table, hk, at * kDecodeStep, len - at * kDecodeStep, lane);
+    for (; at < last; at += 4) {
+        next.land(kt, vt, scales[wave], lane);
+        const bool there0 = next.there[0], there1 = next.there[1];
+        if (at + 4 < last) next.load(p, table, hk, (at + 4) * kDecodeStep, len - (at + 4) * kDecodeStep, lane);
+        gdr::wave_sync();
+        f32x16 s = zero16();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) s = mma(L::row(kt, ks, lane), q[ks], s);
+        f32x16 vs;
+        if (S::kE4m3) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(&scales[wave][reg_row(i, half)]);
+                const f32x4 y = *reinterpret_cast<const f32x4 *>(&scales[wave][32 + reg_row(i, half)]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i + j] *= x[j];
+                    vs[i + j] = y[j];
+                }
+            }
+        }
+        float top = kNegInf;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (at * kDecodeStep + reg_row(i, half) >= sees || !(i < 8 ? there0 : there1)) s[i] = kNegInf;
+            top = fmaxf(top, s[i]);
+        }
+        top = fmaxf(ref, half_max(top) * c);
+        const float from = top == kNegInf ? 0.f : top;   // nothing seen yet: all weights 0
+        const float alpha = __builtin_amdgcn_exp2f(ref - from);
+        ref = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -from));
+            sum += s[i];
+        }
+        l = l * alpha + sum;
+        if (S::kE4m3) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] *= vs[i];
+        }
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
+        add_values<T, D>(o, s, vt, lane);
+        gdr::wave_sync();
+    }
+
+    // the four waves
+    l = half_sum(l);
+    if (half == 0) {
+        stat[wave][0][l32] = ref;
+        stat[wave][1][l32] = l;
+    }
+    float *out = reinterpret_cast<float *>(lds[wave]);
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4 *>(out + l32 * (D + 4) + 32 * dt + reg_row(i, half)) =
+                f32x4{o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]};
+    __syncthreads();
+    constexpr int kLanes = D / 4;   // of a row
+    for (int i = threadIdx.x / kLanes; i < kDecodeRows; i += 256 / kLanes) {
+        const int64_t row = tile * kDecodeRows + i;
+        if (row >= p.rows) break;
+        const int col = 4 * (threadIdx.x % kLanes);
+        float top = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[w][0][i]);
+        f32x4 x = gdr::zero4();
+        if (top > kNegInf) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float a = __builtin_amdgcn_exp2f(stat[w][0][i] - top);
+                sum += a * stat[w][1][i];
+                x += a * *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(lds[w]) + i * (D + 4) + col);
+            }
+        }
+        const int64_t tt = row / p.group, to = (b * p.T_ + tt) * p.Hq + hk * p.group + (row - tt * p.group);
+        if (p.part_o) {
+            *reinterpret_cast<f32x4 *>(p.part_o + (to * p.splits + split) * D + col) = x;
+            if (col == 0) p.part_ml[to * p.splits + split] = f32x2{top, sum};
+        } else {
+            x = top > kNegInf ? x * (1.f / sum) : x;
+            *reinterpret_cast<Quad<T> *>(p.y + to * D + col) = __builtin_convertvector(x, Quad<T>);
+        }
+    }
+}
+
+// The parts of a row, in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const float *part_o, const f32x2 *part_ml, T *y, int64_t rows,
+                                                        int splits)
+{
+    constexpr int L = D / 4;
+    const int col = 4 * (threadIdx.x % L);
+    for (int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; row < rows;
+         row += (int64_t)gridDim.x * (256 / L)) {
+        const f32x2 *ml = part_ml + row * splits;
+        float top = kNegInf, sum = 0.f;
+        for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[s][0]);
+        f32x4 x = gdr::zero4();
+        if (top > kNegInf) {
+            for (int s = 0; s < splits; ++s) {
+                const f32x2 st = ml[s];
+                const float a = __builtin_amdgcn_exp2f(st[0] - top);
+                sum += a * st[1];
+                x += a * *reinterpret_cast<const f32x4 *>(part_o + (row * splits + s) * D + col);
+            }
+            x *= 1.f / sum;
+        }
+        *reinterpret_cast<Quad<T> *>(y + row * D + col) = __builtin_convertvector(x, Quad<T>);
+    }
+}
+
+template <typename T, typename C, int D>
+hipError_t launch_t(const DecodeLaunch &a, hipStream_t stream)
+{
+    DecArgs<T> p;
+    p.q = static_cast<const T *>(a.q);
+    p.k = static_cast<const char *>(a.k_pages);
+    p.v = static_cast<const char *>(a.v_pages);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.table = a.table;
+    p.lens = a.lens;
+    p.y = static_cast<T *>(a.y);
+    p.part_o = a.part_o;
+    p.part_ml = reinterpret_cast<f32x2 *>(a.part_ml);
+    p.T_ = a.T;
+    p.Hq = a.Hq;
+    p.Hk = a.Hk;
+    p.pages = a.pages;
+    p.max_pages = a.max_pages;
+    p.q_stride = a.q_stride;
+    p.group = (int)(a.Hq / a.Hk);
+    p.rows = a.T * p.group;
+    p.log_page = __builtin_ctzll((unsigned long long)a.page);
+    p.splits = (int)a.splits;
+    p.scale = a.scale;
+    const int64_t tiles = (p.rows + kDecodeRows - 1) / kDecodeRows;
+    hipLaunchKernelGGL((attn_decode_kernel<T, C, D>), dim3((unsigned)a.splits, (unsigned)(a.Hk * tiles), (unsigned)a.B),
+                       dim3(256), 0, stream, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = a.B * a.T * a.Hq, per = 256 / (D / 4);
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid_of((rows + per - 1) / per)), dim3(256), 0, stream,
+                       p.part_o, p.part_ml, p.y, rows, p.splits);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_d(const DecodeLaunch &a, hipStream_t stream)
+{
+    if (a.cache_dtype == KV_CACHE_E4M3)
+        return a.D == 64 ? launch_t<T, E4m3, 64>(a, stream) : launch_t<T, E4m3, 128>(a, stream);
+    return a.D == 64 ? launch_t<T, T, 64>(a, stream) : launch_t<T, T, 128>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_decode(const DecodeLaunch &a, hipStream_t stream)
+{
+    return a.dtype == WKV7_F32 ? launch_d<float>(a, stream) : launch_d<bf16>(a, stream);
+}
+
+}  // namespace attn
+}  // namespace wkv7

@@ -1,0 +1,106 @@
+// Host-side launch interface between the C ABI of softmax attention
+// (attn_abi.cpp) and its kernels.  Shapes and pointers reaching these
+// functions are validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attention.h"
+
+namespace wkv7 {
+namespace attn {
+
+// Rows of queries (or keys, in the gradients of k and v) of a workgroup.
+constexpr int kTile = 128;
+
+// Where the tiles of the sequences lie.
+struct Seqs {
+    const int32_t *starts;   // packed: [nseq + 1]; else null
+    int64_t T, nseq;         // tokens of a row; sequences
+    int64_t tiles;           // of a row (unpacked)
+    int64_t slots;           // tile slots: rows' tiles, or, packed, an upper bound of them
+};
+
+// Workgroups of a launch whose kernel goes on by the grid where `needed` are more.
+inline unsigned grid_of(int64_t needed) { return (unsigned)(needed < (1 << 20) ? needed : 1 << 20); }
+
+struct Launch {
+    Seqs seqs;
+    int64_t B, Hq, Hk, D;
+    int64_t q_stride, k_stride, v_stride;   // elements
+    int dtype;
+    float scale;
+    const void *q = nullptr, *k = nullptr, *v = nullptr;
+    void *y = nullptr;
+    float *lse = nullptr;
+    void *record = nullptr;
+    // backward
+    const void *dy = nullptr;
+    void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+    float *stats = nullptr;   // [Hq][B T][2]
+};
+
+hipError_t launch_forward(const Launch &a, hipStream_t stream);
+hipError_t launch_backward(const Launch &a, hipStream_t stream);
+
+struct QkNormLaunch {
+    int64_t B, T, Hq, Hk, D, R, q_stride, k_stride;
+    int dtype, interleaved;
+    float eps;
+    const void *q = nullptr, *k = nullptr;
+    const float *wq = nullptr, *wk = nullptr, *theta = nullptr;
+    const int32_t *positions = nullptr;
+    void *qz = nullptr, *kz = nullptr;   // forward: out
+    const void *dqz = nullptr, *dkz = nullptr;
+    void *dq = nullptr, *dk = nullptr;
+    float *dwq = nullptr, *dwk = nullptr, *part = nullptr;
+};
+// Workgroups of a launch over so many tokens (each a range of them).
+inline int64_t qk_norm_parts(int64_t tokens) { return tokens < 1024 ? tokens : 1024; }
+hipError_t launch_qk_norm_forward(const QkNormLaunch &a, hipStream_t stream);
+hipError_t launch_qk_norm_backward(const QkNormLaunch &a, hipStream_t stream);
+
+struct CacheLaunch {
+    int64_t rows, T, Hk, D, pages, page, max_pages, k_stride, v_stride;
+    int64_t tokens;   // of k and v in all
+    int dtype, cache_dtype;
+    const void *k, *v;
+    void *k_out, *v_out;
+    const void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    const int32_t *table, *lens, *starts;
+};
+hipError_t launch_kv_write(const CacheLaunch &a, hipStream_t stream);   // k, v -> k_out, v_out (pages)
+hipError_t launch_kv_read(const CacheLaunch &a, hipStream_t stream);    // pages -> k_out, v_out
+
+struct DecodeLaunch {
+    int64_t B, T, Hq, Hk, D, pages, page, max_pages, q_stride;
+    int64_t splits;
+    int dtype, cache_dtype;
+    float scale;
+    const void *q, *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int32_t *table, *lens;
+    void *y;
+    float *part_o, *part_ml;   // [B T Hq][splits][D] and [..][2], or null with one split
+};
+// Rows of queries that share a key head's pass over the cache.
+constexpr int kDecodeRows = 32;
+// Tokens of a wave's step.
+constexpr int kDecodeStep = 32;
+// Parts of the cache that are read at once: enough for four workgroups to a
+// compute unit, none under 8 steps (of which each wave has two).
+inline int64_t decode_splits(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t capacity)
+{
+    const int64_t rows = T * (Hq / Hk), units = B * Hk * ((rows + kDecodeRows - 1) / kDecodeRows);
+    const int64_t steps = (capacity + kDecodeStep - 1) / kDecodeStep;
+    int64_t n = (1024 + units - 1) / units;
+    if (n > (steps + 7) / 8) n = (steps + 7) / 8;
+    return n < 1 ? 1 : n;
+}
+hipError_t launch_decode(const DecodeLaunch &a, hipStream_t stream);
+
+}  // namespace attn
+}  // namespace wkv7

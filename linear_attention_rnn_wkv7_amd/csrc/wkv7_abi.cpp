@@ -490,7 +490,7 @@ const char *wkv7_status_string(int status)
     case WKV7_ERR_INVALID: return "invalid argument";
     case WKV7_ERR_UNSUPPORTED:
         return "unsupported: a size that the call does not take (wkv7: head size not 16 or 64; gdr.h, "
-               "residual_norm.h: their limits), or a requested form (chunked, fused inputs) that does not "
+               "residual_norm.h, attention.h: their limits), or a requested form (chunked, fused inputs) that does not "
                "apply to this shape";
     case WKV7_ERR_WORKSPACE: return "workspace missing or too small";
     case WKV7_ERR_HIP: return "HIP launch failed";
