@@ -11,6 +11,8 @@
 // 5): dq would otherwise be a sum over workgroups, by atomics in an order of
 // their own.
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace wkv7 {
@@ -65,14 +67,16 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(BwdArgs<T> p)
 constexpr int kRows = 64;   // of q and dy, or of k and v, in LDS at a time
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 1) attn_dkdv_kernel(BwdArgs<T> p)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_dkdv_kernel(BwdArgs<T> p)
 {
     using L = Tile<T, D>;
-    constexpr int kBytes = kRows * L::kPitch;
-    __shared__ __attribute__((aligned(1024))) char lds[2][2][kBytes];   // [buffer][q, dy]
+    constexpr int kBytes = L::bytes(kRows);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][q, dy]
     __shared__ __attribute__((aligned(16))) float table[2][2][kRows];   // [buffer][lse, D]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, l32 = lane & 31;
+    L tl;
+    tl.init(lane);
     int64_t slot, hk;
     unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
     const Place at = locate(p.seqs, slot);
@@ -93,76 +97,91 @@ __global__ void __launch_bounds__(256, 1) attn_dkdv_kernel(BwdArgs<T> p)
     for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = zero16();
     const float c = p.scale * kLog2e;
 
-    const int first = at.at / kRows, last = (at.len + kRows - 1) / kRows, per = last - first;
-    const int64_t steps = (int64_t)per * p.group;
+    // 32 rows of queries for the wave's keys; kMask where some see not all of them.
+    auto rows = [&](const char *qt, const char *yt, const float *lses, const float *ds_, int r0, auto mask)
+                    __attribute__((always_inline)) {
+        constexpr bool kMask = decltype(mask)::value;
+        f32x16 s = zero16(), ds = zero16();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(qt, ks), k[ks], s);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) ds = mma(tl.row(yt, ks), v[ks], ds);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const f32x4 lse = *reinterpret_cast<const f32x4 *>(lses + reg_row(i, half));
+            const f32x4 dd = *reinterpret_cast<const f32x4 *>(ds_ + reg_row(i, half));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(s[i + j], c, -lse[j]));
+                s[i + j] = w;
+                ds[i + j] = w * (ds[i + j] - dd[j]);
+            }
+        }
+        if constexpr (kMask) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = r0 + reg_row(i, half);
+                if (r < key) s[i] = ds[i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int ss = 0; ss < 2; ++ss) {
+            const Oct<T> w = as_operand<T>(s, ss), dw = as_operand<T>(ds, ss);
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) {
+                dv[dt] = mma(tl.col(yt, dt, ss), w, dv[dt]);
+                dk[dt] = mma(tl.col(qt, dt, ss), dw, dk[dt]);
+            }
+        }
+    };
+
+    const int first = at.at / kRows, last = (at.len + kRows - 1) / kRows;
+    const int64_t h_end = (hk + 1) * p.group;
     Copy<T, D, kRows, 4> cq, cy;
     cq.init(p.q_stride, wave, lane);
     cy.init(p.Hq * D, wave, lane);
     const unsigned base = lds_address(lds);
     f32x2 ahead;
-    auto issue = [&](int buffer, int64_t h, int row0) {
-        const int rows = at.len - row0;
+    auto issue = [&](int buffer, int64_t h, int block) __attribute__((always_inline)) {
+        const int row0 = block * kRows, rows = at.len - row0;
         cq.issue(base + buffer * 2 * kBytes, p.q + (at.tok + row0) * p.q_stride + h * D, rows, wave, lane);
         cy.issue(base + buffer * 2 * kBytes + kBytes, p.dy + ((at.tok + row0) * p.Hq + h) * D, rows, wave, lane);
-        if (wave == 0) ahead = p.stats[h * p.tokens + at.tok + row0 + (lane < rows ? lane : rows - 1)];
+        if (wave == 0) {   // rows that are not there have no weights
+            ahead = f32x2{-kNegInf, 0.f};
+            if (lane < rows) ahead = p.stats[h * p.tokens + at.tok + row0 + lane];
+        }
     };
-    auto land = [&](int buffer) {
+    // Waits for block `block` of head h and sends for the next one.
+    int buffer = 1;
+    auto arrive = [&](int64_t h, int block) __attribute__((always_inline)) {
+        buffer ^= 1;
+        wait_dma();
         if (wave == 0) {
             table[buffer][0][lane] = ahead[0];
             table[buffer][1][lane] = ahead[1];
         }
-    };
-    int64_t h = hk * p.group;
-    int block = first;
-    issue(0, h, block * kRows);
-    for (int64_t n = 0; n < steps; ++n) {
-        const int buffer = n & 1;
-        wait_dma();
-        land(buffer);
         __syncthreads();
-        const int row0 = block * kRows;
-        if (++block == last) {
-            block = first;
-            ++h;
+        if (block + 1 < last)
+            issue(buffer ^ 1, h, block + 1);
+        else if (h + 1 < h_end)
+            issue(buffer ^ 1, h + 1, first);
+    };
+    issue(0, hk * p.group, first);
+    for (int64_t h = hk * p.group; h < h_end; ++h) {
+        int block = first;
+        for (; block < last && block < first + kTile / kRows; ++block) {
+            arrive(h, block);
+            for (int t = 0; t < 2; ++t)
+                if (block * kRows + 32 * t + 31 >= key0 && key0 < at.len)
+                    rows(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                         &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t, std::true_type{});
         }
-        if (n + 1 < steps) issue(buffer ^ 1, h, block * kRows);
+        for (; block < last; ++block) {   // these rows see every key
+            arrive(h, block);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int r0 = row0 + 32 * t;
-            if (r0 + 31 < key0 || r0 >= at.len || key0 >= at.len) continue;
-            const char *qt = lds[buffer][0] + 32 * t * L::kPitch, *yt = lds[buffer][1] + 32 * t * L::kPitch;
-            f32x16 s = zero16(), ds = zero16();
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s = mma(L::row(qt, ks, lane), k[ks], s);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) ds = mma(L::row(yt, ks, lane), v[ks], ds);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const f32x4 lse = *reinterpret_cast<const f32x4 *>(&table[buffer][0][32 * t + reg_row(i, half)]);
-                const f32x4 dd = *reinterpret_cast<const f32x4 *>(&table[buffer][1][32 * t + reg_row(i, half)]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float w = __builtin_amdgcn_exp2f(fmaf(s[i + j], c, -lse[j]));
-                    s[i + j] = w;
-                    ds[i + j] = w * (ds[i + j] - dd[j]);
-                }
-            }
-            if (r0 < key0 + 31 || r0 + 32 > at.len) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = r0 + reg_row(i, half);
-                    if (r < key || r >= at.len) s[i] = ds[i] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int ss = 0; ss < 2; ++ss) {
-                const Oct<T> w = as_operand<T>(s, ss), dw = as_operand<T>(ds, ss);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) {
-                    dv[dt] = mma(L::col(yt, dt, ss, lane), w, dv[dt]);
-                    dk[dt] = mma(L::col(qt, dt, ss, lane), dw, dk[dt]);
-                }
-            }
+            for (int t = 0; t < 2; ++t)
+                rows(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                     &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t, std::false_type{});
         }
     }
     if (key >= at.len) return;
@@ -183,10 +202,12 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(BwdArgs<T> p)
 {
     using L = Tile<T, D>;
-    constexpr int kBytes = kRows * L::kPitch;
-    __shared__ __attribute__((aligned(1024))) char lds[2][2][kBytes];   // [buffer][k, v]
+    constexpr int kBytes = L::bytes(kRows);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, l32 = lane & 31;
+    L tl;
+    tl.init(lane);
     int64_t slot, h;
     unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
     const Place at = locate(p.seqs, slot);
@@ -210,6 +231,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) dq[dt] = zero16();
     const float c = p.scale * kLog2e;
+    // 32 keys for the wave's rows; kMask where some row does not see all of them.
+    auto keys = [&](const char *kt, const char *vt, int key0, auto mask) __attribute__((always_inline)) {
+        constexpr bool kMask = decltype(mask)::value;
+        f32x16 s = zero16(), ds = zero16();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(kt, ks), q[ks], s);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) ds = mma(tl.row(vt, ks), dy[ks], ds);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ds[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -st[0])) * (ds[i] - st[1]);
+        if constexpr (kMask) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (key0 + reg_row(i, half) > row) ds[i] = 0.f;
+        }
+#pragma unroll
+        for (int ss = 0; ss < 2; ++ss) {
+            const Oct<T> w = as_operand<T>(ds, ss);
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(tl.col(kt, dt, ss), w, dq[dt]);
+        }
+    };
+
     const int end = at.at + kTile < at.len ? at.at + kTile : at.len;
     const int blocks = (end + kRows - 1) / kRows;
     Copy<T, D, kRows, 4> ck, cv;
@@ -218,7 +262,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
     const unsigned base = lds_address(lds);
     ck.issue(base, kp, at.len, wave, lane);
     cv.issue(base + kBytes, vp, at.len, wave, lane);
-    for (int n = 0; n < blocks; ++n) {
+    auto arrive = [&](int n) __attribute__((always_inline)) {
         wait_dma();
         __syncthreads();
         if (n + 1 < blocks) {
@@ -227,31 +271,20 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
             ck.issue(to, kp + next * p.k_stride, at.len - (int)next, wave, lane);
             cv.issue(to + kBytes, vp + next * p.v_stride, at.len - (int)next, wave, lane);
         }
+        return lds[n & 1];
+    };
+    int n = 0;
+    for (; n < at.at / kRows; ++n) {   // every row sees all of these
+        const auto *kv = arrive(n);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int key0 = n * kRows + 32 * t;
-            if (key0 > row0 + 31 || row0 >= at.len) continue;
-            const char *kt = lds[n & 1][0] + 32 * t * L::kPitch, *vt = lds[n & 1][1] + 32 * t * L::kPitch;
-            f32x16 s = zero16(), ds = zero16();
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s = mma(L::row(kt, ks, lane), q[ks], s);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) ds = mma(L::row(vt, ks, lane), dy[ks], ds);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                ds[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -st[0])) * (ds[i] - st[1]);
-            if (key0 + 31 > row0) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (key0 + reg_row(i, half) > row) ds[i] = 0.f;
-            }
-#pragma unroll
-            for (int ss = 0; ss < 2; ++ss) {
-                const Oct<T> w = as_operand<T>(ds, ss);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(L::col(kt, dt, ss, lane), w, dq[dt]);
-            }
-        }
+        for (int t = 0; t < 2; ++t)
+            keys(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t, std::false_type{});
+    }
+    for (; n < blocks; ++n) {
+        const auto *kv = arrive(n);
+        for (int t = 0; t < 2; ++t)
+            if (n * kRows + 32 * t <= row0 + 31 && row0 < at.len)
+                keys(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t, std::true_type{});
     }
     if (row >= at.len) return;
     const int64_t to = ((at.tok + row) * p.Hq + h) * D;

@@ -144,9 +144,8 @@ struct Step {
 
 // Parts hi and lo of 16 weights' operand.
 template <typename T, int D>
-__device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w, const char *vt, int lane)
+__device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w, const Tile<T, D> &tl, const char *vt)
 {
-    using L = Tile<T, D>;
     f32x16 rest;
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -161,7 +160,7 @@ __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w,
         const Oct<T> a = as_operand<T>(w, ss);
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) {
-            const Oct<T> x = L::col(vt, dt, ss, lane);
+            const Oct<T> x = tl.col(vt, dt, ss);
             o[dt] = mma(x, a, o[dt]);
             if constexpr (sizeof(T) == 2) o[dt] = mma(x, as_operand<T>(rest, ss), o[dt]);
         }
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
 {
     using L = Tile<T, D>;
     using S = Step<T, C, D>;
-    constexpr int kTileBytes = kDecodeStep * L::kPitch;
+    constexpr int kTileBytes = L::bytes(kDecodeStep);
     // a wave's tiles; then, of each wave, O by rows
     constexpr int kOut = kDecodeRows * (D + 4) * 4;
     constexpr int kWave = 2 * kTileBytes > kOut ? 2 * kTileBytes : kOut;
@@ -182,6 +181,8 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
     __shared__ float stat[4][2][kDecodeRows];   // maximum, sum
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, l32 = lane & 31;
+    L tl;
+    tl.init(lane);
     const int64_t tiles = (p.rows + kDecodeRows - 1) / kDecodeRows;
     const int64_t hk = blockIdx.y / tiles, tile = blockIdx.y - hk * tiles, b = blockIdx.z;
     const int split = blockIdx.x;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
         gdr::wave_sync();
         f32x16 s = zero16();
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) s = mma(L::row(kt, ks, lane), q[ks], s);
+        for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(kt, ks), q[ks], s);
         f32x16 vs;
         if (S::kE4m3) {
 #pragma unroll
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
         }
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
-        add_values<T, D>(o, s, vt, lane);
+        add_values<T, D>(o, s, tl, vt);
         gdr::wave_sync();
     }
 

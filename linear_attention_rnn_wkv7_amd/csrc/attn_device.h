@@ -108,44 +108,71 @@ __device__ __forceinline__ float half_sum(float x)
     return h.a + h.b;
 }
 
-// Rows of D entries in LDS, in 16-byte pieces.  Piece p of row t lies at p ^
-// swizzle(t): 16 rows' reads of one piece meet each bank once, and so do the
-// transposing read's 4 rows of four pieces.  (Rows cannot be padded: copies
-// straight into LDS lay 64 pieces end to end.)
+// Rows of D entries in LDS, in 16-byte pieces, 64 of them to a group: what one
+// copy straight into LDS lays end to end.  Groups are 16 or 32 bytes apart, and
+// piece p of row t lies at p ^ x(t) in its row: so the 16 rows that a read of one
+// piece of 32 rows takes at a time (those with (t / 4) % 8 among 0, 3, 5, 6, then
+// the others) meet each bank once, and so do the transposing read's 4 rows of four
+// pieces, while a lane's address is one of a few, made once, and a constant.
 template <typename T, int D>
 struct Tile {
     static constexpr int kPitch = D * (int)sizeof(T), kPieces = kPitch / 16, kPerCopy = 64 / kPieces;
+    static constexpr int kGroup = 1024 + (kPieces == 8 ? 32 : 16);
+    static constexpr int bytes(int rows) { return rows / kPerCopy * kGroup; }
 
-    __device__ static __forceinline__ int swizzle(int t)
+    __device__ static __forceinline__ int x(int t)
     {
-        if (kPieces == 8) return ((t >> 1) & 1) << 2 | ((t >> 2) & 3);
-        if (kPieces == 16) return (t & 3) << 2 | ((t >> 2) & 3);
-        return t & 15;
+        if (kPieces == 8) return ((t >> 1) & 1) << 2 | ((t >> 2) & 1);
+        if (kPieces == 16) return (t & 3) << 2;
+        return (t & 1) << 3;
     }
-    __device__ static __forceinline__ int at(int t, int piece) { return t * kPitch + ((piece ^ swizzle(t)) << 4); }
+    __device__ static __forceinline__ int at(int t, int piece)
+    {
+        return t / kPerCopy * kGroup + t % kPerCopy * kPitch + ((piece ^ x(t)) << 4);
+    }
+
+    static constexpr int kRowBases = kPieces == 32 ? 2 : 4;
+    static constexpr int kColBases = sizeof(T) == 2 ? D / 32 : kPieces == 32 ? 2 : 4;
+    int row_base[kRowBases], col_base[kColBases];
+    __device__ __forceinline__ void init(int lane)
+    {
+        const int l32 = lane & 31, half = lane >> 5;
+        const int step = sizeof(T) == 2 && kPieces == 8 ? 2 : kPieces == 32 ? 8 : 4;   // pieces from a base to the next
+#pragma unroll
+        for (int i = 0; i < kRowBases; ++i) row_base[i] = at(l32, step * i + half * (int)sizeof(T) / 2);
+#pragma unroll
+        for (int i = 0; i < kColBases; ++i) {
+            if (sizeof(T) == 2) {
+                const int c = 2 * (lane & 16) + 8 * (lane & 3);
+                col_base[i] = at(4 * half + ((lane >> 2) & 3), 4 * i + (c >> 4)) + (c & 15);
+            } else {
+                col_base[i] = at(4 * half, (l32 >> 2) ^ (kPieces == 32 ? 8 : 4) * i) + 4 * (lane & 3);
+            }
+        }
+    }
 
     // Row lane % 32 of `lds` as an operand: entries 16 ks + 8 half ..
-    __device__ static __forceinline__ Oct<T> row(const char *lds, int ks, int lane)
+    __device__ __forceinline__ Oct<T> row(const char *lds, int ks) const
     {
-        const int t = lane & 31, half = lane >> 5;
         if constexpr (sizeof(T) == 2) {
-            return *reinterpret_cast<const bf16x8 *>(lds + at(t, 2 * ks + half));
+            const int o = kPieces == 8 ? row_base[ks & 3] : row_base[(ks >> 1) & 3] + (ks & 1) * 32;
+            return *reinterpret_cast<const bf16x8 *>(lds + o);
         } else {
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(lds + at(t, 4 * ks + 2 * half));
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(lds + at(t, 4 * ks + 2 * half + 1));
+            const int o = kPieces == 16 ? row_base[ks & 3]
+                                        : row_base[(ks >> 1) & 1] + (ks & 1) * 64 + (ks >> 2) * 256;
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(lds + o);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(lds + o + 16);
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
     // Column 32 dt + lane % 32 as an operand: rows 16 s .. of `lds` in the order above.
-    __device__ static __forceinline__ Oct<T> col(const char *lds, int dt, int s, int lane)
+    __device__ __forceinline__ Oct<T> col(const char *lds, int dt, int s) const
     {
-        const int half = lane >> 5;
         if constexpr (sizeof(T) == 2) {
             bf16x4 x[2];
-            const int t = 4 * half + ((lane >> 2) & 3), c = 2 * (lane & 31 & 16) + 8 * (lane & 3);
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
-                const char *p = lds + at(16 * s + 8 * jj + t, 4 * dt + (c >> 4)) + (c & 15);
+                const char *p = lds + col_base[dt] + (16 * s + 8 * jj) / kPerCopy * kGroup;
                 x[jj] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
                     (__attribute__((address_space(3))) bf16x4 *)(const __attribute__((address_space(3))) char *)p);
             }
@@ -154,8 +181,11 @@ struct Tile {
             f32x8 x;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int t = 16 * s + 8 * (j >> 2) + 4 * half + (j & 3);
-                x[j] = *reinterpret_cast<const float *>(lds + at(t, 8 * dt + ((lane & 31) >> 2)) + 4 * (lane & 3));
+                const int t = 16 * s + 8 * (j >> 2) + (j & 3);
+                const int o = t / kPerCopy * kGroup + t % kPerCopy * kPitch +
+                              (kPieces == 16 ? col_base[(j & 3) ^ 2 * dt]
+                                             : col_base[(j & 1) ^ (dt & 1)] + (dt >> 1) * 256);
+                x[j] = *reinterpret_cast<const float *>(lds + o);
             }
             return x;
         }
@@ -167,34 +197,34 @@ struct Tile {
 template <typename T, int D, int N, int kWaves>
 struct Copy {
     using L = Tile<T, D>;
-    static constexpr int kCopies = N * L::kPitch / 1024, kEach = kCopies / kWaves;
-    static_assert(kCopies % kWaves == 0, "whole copies");
-    uint32_t off[kEach];   // of this lane's pieces from the first row
-    uint32_t to;           // LDS address of the wave's first copy within the rows
-    uint32_t stride;       // bytes
+    static constexpr int kEach = N / L::kPerCopy / kWaves;
+    static_assert(kEach * kWaves * L::kPerCopy == N, "whole copies");
+    uint32_t off;      // of this lane's piece from the first row of a copy
+    uint32_t to;       // LDS address of the wave's first copy within the rows
+    uint32_t stride;   // bytes
 
     __device__ __forceinline__ void init(int64_t stride_elements, int wave, int lane)
     {
         stride = (uint32_t)(stride_elements * (int64_t)sizeof(T));
-        to = wave * kEach * 1024;
-#pragma unroll
-        for (int n = 0; n < kEach; ++n) {
-            const int t = (wave * kEach + n) * L::kPerCopy + lane / L::kPieces;
-            off[n] = (uint32_t)t * stride + (((lane % L::kPieces) ^ L::swizzle(t)) << 4);
-        }
+        to = wave * kEach * L::kGroup;
+        const int t = lane / L::kPieces;
+        off = (uint32_t)t * stride + (((lane % L::kPieces) ^ L::x(t)) << 4);
     }
     // `rows` (at least one) of them are there; the others repeat the last.
     __device__ __forceinline__ void issue(unsigned lds, const T *src, int rows, int wave, int lane) const
     {
+        const char *base = reinterpret_cast<const char *>(src);
+        const int first = wave * kEach * L::kPerCopy;
         if (rows >= N) {
 #pragma unroll
-            for (int n = 0; n < kEach; ++n) dma16_split(src, off[n], lds + to + n * 1024);
+            for (int n = 0; n < kEach; ++n)
+                dma16_split(base + (int64_t)(first + n * L::kPerCopy) * stride, off, lds + to + n * L::kGroup);
         } else {
 #pragma unroll
             for (int n = 0; n < kEach; ++n) {
-                const int t = (wave * kEach + n) * L::kPerCopy + lane / L::kPieces;
-                const uint32_t back = t < rows ? 0 : (uint32_t)(t - rows + 1) * stride;
-                dma16_split(src, off[n] - back, lds + to + n * 1024);
+                const int t = first + n * L::kPerCopy + lane / L::kPieces, u = t < rows ? t : rows - 1;
+                dma16_split(base, (uint32_t)u * stride + (((lane % L::kPieces) ^ L::x(t)) << 4),
+                            lds + to + n * L::kGroup);
             }
         }
     }

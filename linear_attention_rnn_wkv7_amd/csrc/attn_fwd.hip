@@ -2,12 +2,15 @@
 //
 // One pass over the keys with the running maximum m and sum l of each row:
 //     s = c (q . k),  c = scale log2 e;   p = 2^(s - m);   l += p;   O += p v
-// and y = O / l, lse = (m + log2 l) ln 2.  When a row's maximum grows, l and O
-// are multiplied by 2^(old - new).
+// and y = O / l, lse = (m + log2 l) ln 2.  Where m has to change, l and O are
+// multiplied by 2^(old - new); it need not be the maximum itself, and follows that
+// only when p would pass 2^8.
 //
 // A workgroup of four waves has kTile rows of one head, 32 to a wave, which
 // hold q (operand) and O^T (results) in registers; keys and values go by 64
 // through two buffers in LDS, the next copied while one is computed.
+
+#include <type_traits>
 
 #include "attn_device.h"
 
@@ -33,10 +36,12 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(FwdArgs<T> p)
 {
     using L = Tile<T, D>;
-    constexpr int kBytes = kKeys * L::kPitch;
-    __shared__ __attribute__((aligned(1024))) char lds[2][2][kBytes];   // [buffer][k, v]
+    constexpr int kBytes = L::bytes(kKeys);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, l32 = lane & 31;
+    L tl;
+    tl.init(lane);
     int64_t slot, h;
     unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
     const Place at = locate(p.seqs, slot);
@@ -58,34 +63,17 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
     float ref = kNegInf, l = 0.f;   // ref: the maximum times c
     const float c = p.scale * kLog2e;
 
-    const int end = at.at + kTile < at.len ? at.at + kTile : at.len;   // keys that any row sees
-    const int blocks = (end + kKeys - 1) / kKeys;
-    Copy<T, D, kKeys, 4> ck, cv;
-    ck.init(p.k_stride, wave, lane);
-    cv.init(p.v_stride, wave, lane);
-    const unsigned base = lds_address(lds);
-    ck.issue(base, kp, at.len, wave, lane);
-    cv.issue(base + kBytes, vp, at.len, wave, lane);
-    for (int n = 0; n < blocks; ++n) {
-        wait_dma();
-        __syncthreads();
-        if (n + 1 < blocks) {
-            const unsigned to = base + ((n + 1) & 1) * 2 * kBytes;
-            const int64_t next = (int64_t)(n + 1) * kKeys;
-            ck.issue(to, kp + next * p.k_stride, at.len - (int)next, wave, lane);
-            cv.issue(to + kBytes, vp + next * p.v_stride, at.len - (int)next, wave, lane);
-        }
-        const char *kt = lds[n & 1][0], *vt = lds[n & 1][1];
-        const int key0 = n * kKeys;
-        if (key0 > row0 + 31 || row0 >= at.len) continue;
+    // One block of keys for the wave's rows; kMask where some row does not see all.
+    auto block = [&](const char *kt, const char *vt, int key0, auto mask) __attribute__((always_inline)) {
+        constexpr bool kMask = decltype(mask)::value;
         f32x16 s[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             s[t] = zero16();
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) s[t] = mma(L::row(kt + 32 * t * L::kPitch, ks, lane), q[ks], s[t]);
+            for (int ks = 0; ks < D / 16; ++ks) s[t] = mma(tl.row(kt + L::bytes(32) * t, ks), q[ks], s[t]);
         }
-        if (key0 + kKeys - 1 > row0) {
+        if constexpr (kMask) {
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -97,28 +85,62 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-        top = fmaxf(ref, half_max(top) * c);
-        const float alpha = __builtin_amdgcn_exp2f(ref - top);
-        ref = top;
-        float sum = 0.f;
+        top = half_max(top) * c;
+        // a row keeps its reference until its maximum is 2^8 times what that stands for
+        const bool grown = top > ref + 8.f;
+        if (__any(grown)) {
+            const float to = grown ? top : ref, alpha = __builtin_amdgcn_exp2f(grown ? ref - to : 0.f);
+            ref = to;
+            l *= alpha;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -ref));
-                sum += s[t][i];
+                sum[t] += s[t][i];
             }
-        l = l * alpha + sum;
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int ss = 0; ss < 2; ++ss) {
                 const Oct<T> w = as_operand<T>(s[t], ss);
 #pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(L::col(vt, dt, 2 * t + ss, lane), w, o[dt]);
+                for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(tl.col(vt, dt, 2 * t + ss), w, o[dt]);
             }
+        }
+        l += sum[0] + sum[1];
+    };
+
+    const int end = at.at + kTile < at.len ? at.at + kTile : at.len;   // keys that any row sees
+    const int blocks = (end + kKeys - 1) / kKeys;
+    Copy<T, D, kKeys, 4> ck, cv;
+    ck.init(p.k_stride, wave, lane);
+    cv.init(p.v_stride, wave, lane);
+    const unsigned base = lds_address(lds);
+    ck.issue(base, kp, at.len, wave, lane);
+    cv.issue(base + kBytes, vp, at.len, wave, lane);
+    // Waits for block n, sends for the next one, and gives block n's place.
+    auto arrive = [&](int n) __attribute__((always_inline)) {
+        wait_dma();
+        __syncthreads();
+        if (n + 1 < blocks) {
+            const unsigned to = base + ((n + 1) & 1) * 2 * kBytes;
+            const int64_t next = (int64_t)(n + 1) * kKeys;
+            ck.issue(to, kp + next * p.k_stride, at.len - (int)next, wave, lane);
+            cv.issue(to + kBytes, vp + next * p.v_stride, at.len - (int)next, wave, lane);
+        }
+        return lds[n & 1];
+    };
+    int n = 0;
+    for (; n < at.at / kKeys; ++n) {   // every row sees all of these
+        const auto *kv = arrive(n);
+        block(kv[0], kv[1], n * kKeys, std::false_type{});
+    }
+    for (; n < blocks; ++n) {
+        const auto *kv = arrive(n);
+        if (n * kKeys <= row0 + 31 && row0 < at.len) block(kv[0], kv[1], n * kKeys, std::true_type{});
     }
     if (row >= at.len) return;
     l = half_sum(l);
