@@ -7,7 +7,7 @@
 // every token and head into a table; dk and dv, a workgroup to kTile keys,
 // which goes over the queries behind them, of every query head that reads the
 // key head, in order; dq, a workgroup to kTile queries, which goes over the keys
-// before them.  The scores and dy . v are formed twice (7 products instead of
+// before them; narrow forms of both for few of them.  The scores and dy . v are formed twice (7 products instead of
 // 5): dq would otherwise be a sum over workgroups, by atomics in an order of
 // their own.
 
@@ -66,24 +66,20 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(BwdArgs<T> p)
 
 constexpr int kRows = 64;   // of q and dy, or of k and v, in LDS at a time
 
+// 32 keys of a wave.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_dkdv_kernel(BwdArgs<T> p)
-{
-    using L = Tile<T, D>;
-    constexpr int kBytes = L::bytes(kRows);
-    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][q, dy]
-    __shared__ __attribute__((aligned(16))) float table[2][2][kRows];   // [buffer][lse, D]
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = lane >> 5, l32 = lane & 31;
-    L tl;
-    tl.init(lane);
-    int64_t slot, hk;
-    unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
-    const Place at = locate(p.seqs, slot);
-    if (at.len == 0) return;
-    const int key0 = at.at + 32 * wave, key = key0 + l32;
+struct Keys {
+    Tile<T, D> tl;
     Oct<T> k[D / 16], v[D / 16];
+    f32x16 dk[D / 32], dv[D / 32];
+    float c;
+    int key, half;
+
+    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int hk, int key0, int lane)
     {
+        tl.init(lane);
+        half = lane >> 5;
+        key = key0 + (lane & 31);
         const int64_t r = at.tok + (key < at.len ? key : at.len - 1);
         const T *kp = p.k + r * p.k_stride + hk * D + 8 * half, *vp = p.v + r * p.v_stride + hk * D + 8 * half;
 #pragma unroll
@@ -91,16 +87,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
             k[ks] = *reinterpret_cast<const Oct<T> *>(kp + 16 * ks);
             v[ks] = *reinterpret_cast<const Oct<T> *>(vp + 16 * ks);
         }
-    }
-    f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = zero16();
-    const float c = p.scale * kLog2e;
-
-    // 32 rows of queries for the wave's keys; kMask where some see not all of them.
-    auto rows = [&](const char *qt, const char *yt, const float *lses, const float *ds_, int r0, auto mask)
-                    __attribute__((always_inline)) {
-        constexpr bool kMask = decltype(mask)::value;
+        for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = zero16();
+        c = p.scale * kLog2e;
+    }
+    // 32 rows of queries from r0 on, with their table of lse and D; kMask where some see not all keys.
+    template <bool kMask>
+    __device__ __forceinline__ void rows(const char *qt, const char *yt, const float *lses, const float *dots, int r0)
+    {
         f32x16 s = zero16(), ds = zero16();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(qt, ks), k[ks], s);
@@ -109,20 +103,18 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
             const f32x4 lse = *reinterpret_cast<const f32x4 *>(lses + reg_row(i, half));
-            const f32x4 dd = *reinterpret_cast<const f32x4 *>(ds_ + reg_row(i, half));
+            const f32x4 dot = *reinterpret_cast<const f32x4 *>(dots + reg_row(i, half));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float w = __builtin_amdgcn_exp2f(fmaf(s[i + j], c, -lse[j]));
                 s[i + j] = w;
-                ds[i + j] = w * (ds[i + j] - dd[j]);
+                ds[i + j] = w * (ds[i + j] - dot[j]);
             }
         }
         if constexpr (kMask) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = r0 + reg_row(i, half);
-                if (r < key) s[i] = ds[i] = 0.f;
-            }
+            for (int i = 0; i < 16; ++i)
+                if (r0 + reg_row(i, half) < key) s[i] = ds[i] = 0.f;
         }
 #pragma unroll
         for (int ss = 0; ss < 2; ++ss) {
@@ -133,16 +125,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
                 dk[dt] = mma(tl.col(qt, dt, ss), dw, dk[dt]);
             }
         }
-    };
+    }
+};
 
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_dkdv_kernel(BwdArgs<T> p)
+{
+    using L = Tile<T, D>;
+    constexpr int kBytes = L::bytes(kRows);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];     // [buffer][q, dy]
+    __shared__ __attribute__((aligned(16))) float table[2][2][kRows];   // [buffer][lse, D]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int slot, hk;
+    unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
+    const Place at = locate<kTile>(p.seqs, slot, lane);
+    if (at.len == 0) return;
     const int first = at.at / kRows, last = (at.len + kRows - 1) / kRows;
-    const int64_t h_end = (hk + 1) * p.group;
+    const int h0 = hk * p.group, h_end = h0 + p.group;
     Copy<T, D, kRows, 4> cq, cy;
     cq.init(p.q_stride, wave, lane);
     cy.init(p.Hq * D, wave, lane);
     const unsigned base = lds_address(lds);
     f32x2 ahead;
-    auto issue = [&](int buffer, int64_t h, int block) __attribute__((always_inline)) {
+    auto issue = [&](int buffer, int h, int block) __attribute__((always_inline)) {
         const int row0 = block * kRows, rows = at.len - row0;
         cq.issue(base + buffer * 2 * kBytes, p.q + (at.tok + row0) * p.q_stride + h * D, rows, wave, lane);
         cy.issue(base + buffer * 2 * kBytes + kBytes, p.dy + ((at.tok + row0) * p.Hq + h) * D, rows, wave, lane);
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
     };
     // Waits for block `block` of head h and sends for the next one.
     int buffer = 1;
-    auto arrive = [&](int64_t h, int block) __attribute__((always_inline)) {
+    auto arrive = [&](int h, int block) __attribute__((always_inline)) {
         buffer ^= 1;
         wait_dma();
         if (wave == 0) {
@@ -166,58 +171,125 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
         else if (h + 1 < h_end)
             issue(buffer ^ 1, h + 1, first);
     };
-    issue(0, hk * p.group, first);
-    for (int64_t h = hk * p.group; h < h_end; ++h) {
+    issue(0, h0, first);
+    const int key0 = at.at + 32 * wave;
+    Keys<T, D> w;
+    w.init(p, at, hk, key0, lane);
+    for (int h = h0; h < h_end; ++h) {
         int block = first;
         for (; block < last && block < first + kTile / kRows; ++block) {
             arrive(h, block);
             for (int t = 0; t < 2; ++t)
                 if (block * kRows + 32 * t + 31 >= key0 && key0 < at.len)
-                    rows(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                         &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t, std::true_type{});
+                    w.template rows<true>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                          &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t);
         }
         for (; block < last; ++block) {   // these rows see every key
             arrive(h, block);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                rows(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                     &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t, std::false_type{});
+                w.template rows<false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                       &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t);
         }
     }
-    if (key >= at.len) return;
-    const int64_t to = ((at.tok + key) * p.Hk + hk) * D;
+    if (w.key >= at.len) return;
+    const int64_t to = ((at.tok + w.key) * p.Hk + hk) * D;
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const int64_t e = to + 32 * dt + reg_row(i, half);
-            const f32x4 a = f32x4{dk[dt][i], dk[dt][i + 1], dk[dt][i + 2], dk[dt][i + 3]} * p.scale;
-            const f32x4 b = f32x4{dv[dt][i], dv[dt][i + 1], dv[dt][i + 2], dv[dt][i + 3]};
+            const int64_t e = to + 32 * dt + reg_row(i, w.half);
+            const f32x4 a = f32x4{w.dk[dt][i], w.dk[dt][i + 1], w.dk[dt][i + 2], w.dk[dt][i + 3]} * p.scale;
+            const f32x4 b = f32x4{w.dv[dt][i], w.dv[dt][i + 1], w.dv[dt][i + 2], w.dv[dt][i + 3]};
             *reinterpret_cast<Quad<T> *>(p.dk + e) = __builtin_convertvector(a, Quad<T>);
             *reinterpret_cast<Quad<T> *>(p.dv + e) = __builtin_convertvector(b, Quad<T>);
         }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(BwdArgs<T> p)
+// The sum of the four waves' results, by rows of `count` tokens, times `by`.
+template <typename T, int D, int kWave>
+__device__ __forceinline__ void join(const char (&lds)[4][kWave], T *out, int64_t stride, int count, float by)
 {
-    using L = Tile<T, D>;
-    constexpr int kBytes = L::bytes(kRows);
-    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
+    constexpr int kLanes = D / 4;
+    const int col = 4 * (threadIdx.x % kLanes);
+    for (int i = threadIdx.x / kLanes; i < count; i += 256 / kLanes) {
+        const f32x4 x = (get_row<D>(lds[0], i, col) + get_row<D>(lds[1], i, col)) +
+                        (get_row<D>(lds[2], i, col) + get_row<D>(lds[3], i, col));
+        *reinterpret_cast<Quad<T> *>(out + i * stride + col) = __builtin_convertvector(x * by, Quad<T>);
+    }
+}
+
+// The narrow form: a wave has every fourth 32 rows of all the heads.
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 1) attn_dkdv_narrow_kernel(BwdArgs<T> p)
+{
+    using O = Own<T, D>;
+    __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
+    __shared__ __attribute__((aligned(16))) float table[4][2][32];   // lse, D
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = lane >> 5, l32 = lane & 31;
-    L tl;
-    tl.init(lane);
-    int64_t slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
-    const Place at = locate(p.seqs, slot);
+    int slot, hk;
+    unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
+    const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
-    const int64_t hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
-    const int row0 = at.at + 32 * wave, row = row0 + l32;
+    const int first = at.at / 32, per = (at.len + 31) / 32 - first;
+    const int steps = per * p.group;   // fits: few workgroups of kTile keys, so few tokens
+    Copy<T, D, 32, 1> cq, cy;
+    cq.init(p.q_stride, 0, lane);
+    cy.init(p.Hq * D, 0, lane);
+    const unsigned base = lds_address(lds[wave]);
+    f32x2 ahead;
+    auto send = [&](int n) __attribute__((always_inline)) {
+        const int g = n / per, h = hk * p.group + g, row0 = (first + n - g * per) * 32, rows = at.len - row0;
+        const unsigned to = base + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        cq.issue(to, p.q + (at.tok + row0) * p.q_stride + h * D, rows, 0, lane);
+        cy.issue(to + O::kBytes, p.dy + ((at.tok + row0) * p.Hq + h) * D, rows, 0, lane);
+        ahead = f32x2{-kNegInf, 0.f};   // rows that are not there have no weights
+        if ((lane & 31) < rows) ahead = p.stats[h * p.tokens + at.tok + row0 + (lane & 31)];
+    };
+    if (wave < steps) send(wave);
+    Keys<T, D> w;
+    w.init(p, at, hk, at.at, lane);
+    for (int n = wave; n < steps; n += 4) {
+        wait_dma();
+        table[wave][lane >> 5][lane & 31] = ahead[lane >> 5];
+        gdr::wave_sync();
+        if (O::kBuffers == 2 && n + 4 < steps) send(n + 4);
+        const char *qy = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        const int at_row = n % per;
+        if (at_row == 0)
+            w.template rows<true>(qy, qy + O::kBytes, table[wave][0], table[wave][1], first * 32);
+        else
+            w.template rows<false>(qy, qy + O::kBytes, table[wave][0], table[wave][1], (first + at_row) * 32);
+        gdr::wave_sync();
+        reads_done();
+        if (O::kBuffers == 1 && n + 4 < steps) send(n + 4);
+    }
+    const int count = at.len - at.at < kNarrow ? at.len - at.at : kNarrow;
+    const int64_t to = ((at.tok + at.at) * p.Hk + hk) * D;
+    put_rows<D>(lds[wave], w.dk, lane);
+    __syncthreads();
+    join<T, D>(lds, p.dk + to, p.Hk * D, count, p.scale);
+    __syncthreads();
+    put_rows<D>(lds[wave], w.dv, lane);
+    __syncthreads();
+    join<T, D>(lds, p.dv + to, p.Hk * D, count, 1.f);
+}
+
+// 32 rows of a wave.
+template <typename T, int D>
+struct Rows {
+    Tile<T, D> tl;
     Oct<T> q[D / 16], dy[D / 16];
+    f32x16 dq[D / 32];
     f32x2 st;
+    float c;
+    int row, half;
+
+    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int h, int row0, int lane)
     {
+        tl.init(lane);
+        half = lane >> 5;
+        row = row0 + (lane & 31);
         const int64_t r = at.tok + (row < at.len ? row : at.len - 1);
         const T *qp = p.q + r * p.q_stride + h * D + 8 * half, *yp = p.dy + (r * p.Hq + h) * D + 8 * half;
 #pragma unroll
@@ -226,14 +298,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
             dy[ks] = *reinterpret_cast<const Oct<T> *>(yp + 16 * ks);
         }
         st = p.stats[h * p.tokens + r];
-    }
-    f32x16 dq[D / 32];
 #pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) dq[dt] = zero16();
-    const float c = p.scale * kLog2e;
-    // 32 keys for the wave's rows; kMask where some row does not see all of them.
-    auto keys = [&](const char *kt, const char *vt, int key0, auto mask) __attribute__((always_inline)) {
-        constexpr bool kMask = decltype(mask)::value;
+        for (int dt = 0; dt < D / 32; ++dt) dq[dt] = zero16();
+        c = p.scale * kLog2e;
+    }
+    // 32 keys from key0 on; kMask where some row does not see all of them.
+    template <bool kMask>
+    __device__ __forceinline__ void keys(const char *kt, const char *vt, int key0)
+    {
         f32x16 s = zero16(), ds = zero16();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(kt, ks), q[ks], s);
@@ -252,8 +324,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(tl.col(kt, dt, ss), w, dq[dt]);
         }
-    };
+    }
+};
 
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(BwdArgs<T> p)
+{
+    using L = Tile<T, D>;
+    constexpr int kBytes = L::bytes(kRows);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int slot, h;
+    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    const Place at = locate<kTile>(p.seqs, slot, lane);
+    if (at.len == 0) return;
+    const int hk = h / p.group;
+    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
     const int end = at.at + kTile < at.len ? at.at + kTile : at.len;
     const int blocks = (end + kRows - 1) / kRows;
     Copy<T, D, kRows, 4> ck, cv;
@@ -262,6 +348,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
     const unsigned base = lds_address(lds);
     ck.issue(base, kp, at.len, wave, lane);
     cv.issue(base + kBytes, vp, at.len, wave, lane);
+    const int row0 = at.at + 32 * wave;
+    Rows<T, D> r;
+    r.init(p, at, h, row0, lane);
     auto arrive = [&](int n) __attribute__((always_inline)) {
         wait_dma();
         __syncthreads();
@@ -278,23 +367,67 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
         const auto *kv = arrive(n);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            keys(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t, std::false_type{});
+            r.template keys<false>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t);
     }
     for (; n < blocks; ++n) {
         const auto *kv = arrive(n);
         for (int t = 0; t < 2; ++t)
             if (n * kRows + 32 * t <= row0 + 31 && row0 < at.len)
-                keys(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t, std::true_type{});
+                r.template keys<true>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t);
     }
-    if (row >= at.len) return;
-    const int64_t to = ((at.tok + row) * p.Hq + h) * D;
+    if (r.row >= at.len) return;
+    const int64_t to = ((at.tok + r.row) * p.Hq + h) * D;
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-            const f32x4 x = f32x4{dq[dt][i], dq[dt][i + 1], dq[dt][i + 2], dq[dt][i + 3]} * p.scale;
-            *reinterpret_cast<Quad<T> *>(p.dq + to + 32 * dt + reg_row(i, half)) = __builtin_convertvector(x, Quad<T>);
+            const f32x4 x = f32x4{r.dq[dt][i], r.dq[dt][i + 1], r.dq[dt][i + 2], r.dq[dt][i + 3]} * p.scale;
+            *reinterpret_cast<Quad<T> *>(p.dq + to + 32 * dt + reg_row(i, r.half)) = __builtin_convertvector(x, Quad<T>);
         }
+}
+
+// The narrow form: a wave has every fourth 32 keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 1) attn_dq_narrow_kernel(BwdArgs<T> p)
+{
+    using O = Own<T, D>;
+    __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int slot, h;
+    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    const Place at = locate<kNarrow>(p.seqs, slot, lane);
+    if (at.len == 0) return;
+    const int hk = h / p.group;
+    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    Copy<T, D, 32, 1> ck, cv;
+    ck.init(p.k_stride, 0, lane);
+    cv.init(p.v_stride, 0, lane);
+    const unsigned base = lds_address(lds[wave]);
+    const int last = at.at / 32;
+    auto send = [&](int n) __attribute__((always_inline)) {
+        const unsigned to = base + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        const int64_t first = (int64_t)n * 32;
+        ck.issue(to, kp + first * p.k_stride, at.len - (int)first, 0, lane);
+        cv.issue(to + O::kBytes, vp + first * p.v_stride, at.len - (int)first, 0, lane);
+    };
+    if (wave <= last) send(wave);
+    Rows<T, D> r;
+    r.init(p, at, h, at.at, lane);
+    for (int n = wave; n <= last; n += 4) {
+        wait_dma();
+        if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
+        const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        if (n < last)
+            r.template keys<false>(kv, kv + O::kBytes, n * 32);
+        else
+            r.template keys<true>(kv, kv + O::kBytes, n * 32);
+        reads_done();
+        if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+    }
+    put_rows<D>(lds[wave], r.dq, lane);
+    __syncthreads();
+    const int count = at.len - at.at < kNarrow ? at.len - at.at : kNarrow;
+    join<T, D>(lds, p.dq + ((at.tok + at.at) * p.Hq + h) * D, p.Hq * D, count, p.scale);
 }
 
 template <typename T, int D>
@@ -327,10 +460,20 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
                        stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_dkdv_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hk)), dim3(256), 0, stream, p);
+    BwdArgs<T> few = p;
+    few.seqs = narrow(a.seqs, a.B);
+    if (is_narrow(a.seqs.slots * a.Hk))
+        hipLaunchKernelGGL((attn_dkdv_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hk)), dim3(256), 0, stream,
+                           few);
+    else
+        hipLaunchKernelGGL((attn_dkdv_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hk)), dim3(256), 0, stream, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_dq_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
+    if (is_narrow(a.seqs.slots * a.Hq))
+        hipLaunchKernelGGL((attn_dq_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hq)), dim3(256), 0, stream,
+                           few);
+    else
+        hipLaunchKernelGGL((attn_dq_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -255,49 +255,103 @@ struct Place {
     int len, at;
 };
 
-// Packed sequence s starts at slot floor(start / kTile) + s: that keeps the
-// sequences' slots apart and below T / kTile + nseq without a sum over the
-// sequences before.  A slot behind its sequence's last tile has at >= len.
-__device__ __forceinline__ Place locate(const Seqs &m, int64_t slot)
+// Tile `slot` of tiles of kRows tokens.  Packed sequence s starts at slot
+// floor(start / kRows) + s: that keeps the sequences' slots apart and below T /
+// kRows + nseq without a sum over the sequences before.  A slot behind its
+// sequence's last tile has len = 0.  The last sequence whose first slot is not
+// behind `slot` is found by the wave's lanes, 64 sequences (or ranges of them) at a time.
+template <int kRows>
+__device__ __forceinline__ Place locate(const Seqs &m, int slot, int lane)
 {
-    int64_t lo, hi, at;
+    int64_t lo, hi;
+    int at;
     if (!m.starts) {
-        const int64_t row = slot / m.tiles;
+        const int row = (uint32_t)slot / (uint32_t)m.tiles;
         lo = row * m.T;
         hi = lo + m.T;
-        at = slot - row * m.tiles;
+        at = slot - row * (int)m.tiles;
     } else {
-        int64_t a = 0, b = m.nseq - 1;   // the last sequence whose first slot is <= slot
-        while (a < b) {
-            const int64_t mid = (a + b + 1) >> 1;
-            seq_range(m, mid, lo, hi);
-            if (lo / kTile + mid <= slot)
-                a = mid;
-            else
-                b = mid - 1;
+        const int nseq = (int)m.nseq;
+        int first = 0, step = 1;
+        while (step * 64 < nseq) step *= 64;
+        for (; step; step /= 64) {
+            const int s = first + lane * step;
+            bool before = false;
+            if (s < nseq) {
+                const int start = m.starts[s];
+                before = (start < 0 ? 0 : start > m.T ? (int)m.T : start) / kRows + s <= slot;
+            }
+            const int n = __popcll(__ballot(before));   // none: tokens before the first sequence
+            first += (n > 0 ? n - 1 : 0) * step;
         }
-        seq_range(m, a, lo, hi);
-        at = slot - (lo / kTile + a);
+        first = __builtin_amdgcn_readfirstlane(first);
+        seq_range(m, first, lo, hi);
+        at = slot - (int)(lo / kRows) - first;
     }
     const int64_t len = hi - lo;
-    if (at < 0 || at * kTile >= len) return {lo, 0, 0};
-    return {lo, (int)len, (int)(at * kTile)};
+    if (at < 0 || (int64_t)at * kRows >= len) return {lo, 0, 0};
+    return {lo, (int)len, at * kRows};
 }
 
 // Block -> (slot, head).  Rows' last tiles, which see the most, start first.
 // Workgroups go to the 8 dies in turn: of the units (row, head) of one tile,
 // neighbours, which read the same keys, go to one die, whose cache then holds
 // them for all.
-__device__ __forceinline__ void unit_of(const Seqs &m, int64_t B, int64_t heads, bool last_first, int64_t id,
-                                        int64_t &slot, int64_t &head)
+__device__ __forceinline__ void unit_of(const Seqs &m, int64_t B, int64_t heads_, bool last_first, uint32_t id,
+                                        int &slot, int &head)
 {
-    const int64_t units = m.starts ? heads : B * heads;
-    int64_t tile = id / units, u = id - tile * units;
+    const uint32_t heads = (uint32_t)heads_, units = m.starts ? heads : (uint32_t)(B * heads_);
+    uint32_t tile = id / units, u = id - tile * units;
     if (units % 8 == 0) u = u % 8 * (units / 8) + u / 8;
-    const int64_t tiles = m.starts ? m.slots : m.tiles;
+    const uint32_t tiles = (uint32_t)(m.starts ? m.slots : m.tiles);
     if (last_first) tile = tiles - 1 - tile;
-    head = u % heads;
-    slot = m.starts ? tile : u / heads * m.tiles + tile;
+    const uint32_t b = u / heads;
+    head = (int)(u - b * heads);
+    slot = (int)(m.starts ? tile : b * (uint32_t)m.tiles + tile);
+}
+
+// Where few workgroups of kTile rows would leave compute units without one, a
+// workgroup has kNarrow rows and its four waves share what they have to go over.
+constexpr int kNarrow = 32;
+inline Seqs narrow(const Seqs &s, int64_t B)
+{
+    Seqs n = s;
+    n.tiles = (s.T + kNarrow - 1) / kNarrow;
+    n.slots = s.starts ? s.T / kNarrow + s.nseq : B * n.tiles;
+    return n;
+}
+
+// A wave's own tiles in a narrow workgroup: two arrays of 32 rows, twice where
+// LDS has room.
+template <typename T, int D>
+struct Own {
+    static constexpr int kBytes = Tile<T, D>::bytes(32);
+    static constexpr int kBuffers = 4 * 2 * 2 * kBytes <= 140 * 1024 ? 2 : 1;
+    // then the waves' results, by rows, are joined there
+    static constexpr int kOut = 32 * (D + 4) * 4;
+    static constexpr int kWave = kBuffers * 2 * kBytes > kOut ? kBuffers * 2 * kBytes : kOut;
+};
+
+// Between a wave's reads of LDS and copies to the same place.
+__device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// A result by columns (its column on lane % 32) into LDS by rows of that, and the
+// sum of the four waves' over them, in order.
+template <int D>
+__device__ __forceinline__ void put_rows(char *lds, const f32x16 (&x)[D / 32], int lane)
+{
+    float *out = reinterpret_cast<float *>(lds) + (lane & 31) * (D + 4);
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<f32x4 *>(out + 32 * dt + reg_row(i, lane >> 5)) =
+                f32x4{x[dt][i], x[dt][i + 1], x[dt][i + 2], x[dt][i + 3]};
+}
+template <int D>
+__device__ __forceinline__ f32x4 get_row(const char *lds, int row, int col)
+{
+    return *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(lds) + row * (D + 4) + col);
 }
 
 }  // namespace attn

@@ -8,7 +8,8 @@
 //
 // A workgroup of four waves has kTile rows of one head, 32 to a wave, which
 // hold q (operand) and O^T (results) in registers; keys and values go by 64
-// through two buffers in LDS, the next copied while one is computed.
+// through two buffers in LDS, the next copied while one is computed.  The narrow
+// form, for few rows, has 32 of them, and each wave every fourth 32 keys.
 
 #include <type_traits>
 
@@ -32,57 +33,52 @@ struct FwdArgs {
 
 constexpr int kKeys = 64;
 
+// 32 rows of a wave.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(FwdArgs<T> p)
-{
-    using L = Tile<T, D>;
-    constexpr int kBytes = L::bytes(kKeys);
-    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int half = lane >> 5, l32 = lane & 31;
-    L tl;
-    tl.init(lane);
-    int64_t slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
-    const Place at = locate(p.seqs, slot);
-    if (at.len == 0) return;
-    const int64_t hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
-
-    const int row0 = at.at + 32 * wave, row = row0 + l32;
+struct Rows {
+    Tile<T, D> tl;
     Oct<T> q[D / 16];
+    f32x16 o[D / 32];
+    float ref, l, c;   // ref: what stands for the maximum, times c
+    int row, half;
+
+    __device__ __forceinline__ void init(const FwdArgs<T> &p, const Place &at, int h, int row0, int lane)
     {
+        tl.init(lane);
+        half = lane >> 5;
+        row = row0 + (lane & 31);
         const int r = row < at.len ? row : at.len - 1;
         const T *qp = p.q + (at.tok + r) * p.q_stride + h * D + 8 * half;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) q[ks] = *reinterpret_cast<const Oct<T> *>(qp + 16 * ks);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
+        ref = kNegInf;
+        l = 0.f;
+        c = p.scale * kLog2e;
     }
-    f32x16 o[D / 32];
+    // 32 N keys from key0 on; kMask where some row does not see all.
+    template <int N, bool kMask>
+    __device__ __forceinline__ void keys(const char *kt, const char *vt, int key0)
+    {
+        using L = Tile<T, D>;
+        f32x16 s[N];
 #pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
-    float ref = kNegInf, l = 0.f;   // ref: the maximum times c
-    const float c = p.scale * kLog2e;
-
-    // One block of keys for the wave's rows; kMask where some row does not see all.
-    auto block = [&](const char *kt, const char *vt, int key0, auto mask) __attribute__((always_inline)) {
-        constexpr bool kMask = decltype(mask)::value;
-        f32x16 s[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < N; ++t) {
             s[t] = zero16();
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) s[t] = mma(tl.row(kt + L::bytes(32) * t, ks), q[ks], s[t]);
         }
         if constexpr (kMask) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < N; ++t)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (key0 + 32 * t + reg_row(i, half) > row) s[t][i] = kNegInf;
         }
         float top = s[0][0];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < N; ++t)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
         top = half_max(top) * c;
@@ -95,9 +91,10 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
         }
-        float sum[2] = {0.f, 0.f};
+        float sum[N];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < N; ++t) {
+            sum[t] = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -ref));
@@ -109,9 +106,38 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
 #pragma unroll
                 for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(tl.col(vt, dt, 2 * t + ss), w, o[dt]);
             }
+            l += sum[t];
         }
-        l += sum[0] + sum[1];
-    };
+    }
+};
+
+// Four values of y at entry e, and what their rounding takes away.
+template <typename T>
+__device__ __forceinline__ void store_y(const FwdArgs<T> &p, int64_t e, f32x4 x)
+{
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4 *>(p.y + e) = x;
+    } else {
+        const bf16x4 r = __builtin_convertvector(x, bf16x4);
+        *reinterpret_cast<bf16x4 *>(p.y + e) = r;
+        if (p.record)
+            *reinterpret_cast<bf16x4 *>(p.record + e) =
+                __builtin_convertvector(x - __builtin_convertvector(r, f32x4), bf16x4);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(FwdArgs<T> p)
+{
+    constexpr int kBytes = Tile<T, D>::bytes(kKeys);
+    __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int slot, h;
+    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    const Place at = locate<kTile>(p.seqs, slot, lane);
+    if (at.len == 0) return;
+    const int hk = h / p.group;
+    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
 
     const int end = at.at + kTile < at.len ? at.at + kTile : at.len;   // keys that any row sees
     const int blocks = (end + kKeys - 1) / kKeys;
@@ -121,6 +147,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
     const unsigned base = lds_address(lds);
     ck.issue(base, kp, at.len, wave, lane);
     cv.issue(base + kBytes, vp, at.len, wave, lane);
+    const int row0 = at.at + 32 * wave;
+    Rows<T, D> r;
+    r.init(p, at, h, row0, lane);
     // Waits for block n, sends for the next one, and gives block n's place.
     auto arrive = [&](int n) __attribute__((always_inline)) {
         wait_dma();
@@ -136,33 +165,87 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
     int n = 0;
     for (; n < at.at / kKeys; ++n) {   // every row sees all of these
         const auto *kv = arrive(n);
-        block(kv[0], kv[1], n * kKeys, std::false_type{});
+        r.template keys<2, false>(kv[0], kv[1], n * kKeys);
     }
     for (; n < blocks; ++n) {
         const auto *kv = arrive(n);
-        if (n * kKeys <= row0 + 31 && row0 < at.len) block(kv[0], kv[1], n * kKeys, std::true_type{});
+        if (n * kKeys <= row0 + 31 && row0 < at.len) r.template keys<2, true>(kv[0], kv[1], n * kKeys);
     }
-    if (row >= at.len) return;
-    l = half_sum(l);
-    const float inv = 1.f / l;
-    const int64_t to = (at.tok + row) * p.Hq + h;
-    if (p.lse && half == 0) p.lse[to] = (ref + __builtin_amdgcn_logf(l)) * kLn2;
+    if (r.row >= at.len) return;
+    const float l = half_sum(r.l), inv = 1.f / l;
+    const int64_t to = (at.tok + r.row) * p.Hq + h;
+    if (p.lse && r.half == 0) p.lse[to] = (r.ref + __builtin_amdgcn_logf(l)) * kLn2;
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const f32x4 x = f32x4{o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]} * inv;
-            const int64_t e = to * D + 32 * dt + reg_row(i, half);
-            if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<f32x4 *>(p.y + e) = x;
-            } else {
-                const bf16x4 r = __builtin_convertvector(x, bf16x4);
-                *reinterpret_cast<bf16x4 *>(p.y + e) = r;
-                if (p.record)
-                    *reinterpret_cast<bf16x4 *>(p.record + e) =
-                        __builtin_convertvector(x - __builtin_convertvector(r, f32x4), bf16x4);
-            }
+        for (int i = 0; i < 16; i += 4)
+            store_y(p, to * D + 32 * dt + reg_row(i, r.half),
+                    f32x4{r.o[dt][i], r.o[dt][i + 1], r.o[dt][i + 2], r.o[dt][i + 3]} * inv);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256, 1) attn_fwd_narrow_kernel(FwdArgs<T> p)
+{
+    using O = Own<T, D>;
+    __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
+    __shared__ float stat[4][2][kNarrow];   // reference, sum
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int slot, h;
+    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    const Place at = locate<kNarrow>(p.seqs, slot, lane);
+    if (at.len == 0) return;
+    const int hk = h / p.group;
+    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    Copy<T, D, 32, 1> ck, cv;
+    ck.init(p.k_stride, 0, lane);
+    cv.init(p.v_stride, 0, lane);
+    const unsigned base = lds_address(lds[wave]);
+    const int last = at.at / 32;   // 32 keys to a step, the last of them masked
+    auto send = [&](int n) __attribute__((always_inline)) {
+        const unsigned to = base + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        const int64_t first = (int64_t)n * 32;
+        ck.issue(to, kp + first * p.k_stride, at.len - (int)first, 0, lane);
+        cv.issue(to + O::kBytes, vp + first * p.v_stride, at.len - (int)first, 0, lane);
+    };
+    if (wave <= last) send(wave);
+    Rows<T, D> r;
+    r.init(p, at, h, at.at, lane);
+    for (int n = wave; n <= last; n += 4) {
+        wait_dma();
+        if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
+        const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+        if (n < last)
+            r.template keys<1, false>(kv, kv + O::kBytes, n * 32);
+        else
+            r.template keys<1, true>(kv, kv + O::kBytes, n * 32);
+        reads_done();
+        if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+    }
+    r.l = half_sum(r.l);
+    if (r.half == 0) {
+        stat[wave][0][lane] = r.ref;
+        stat[wave][1][lane] = r.l;
+    }
+    put_rows<D>(lds[wave], r.o, lane);
+    __syncthreads();
+    constexpr int kLanes = D / 4;
+    for (int i = threadIdx.x / kLanes; i < kNarrow && at.at + i < at.len; i += 256 / kLanes) {
+        const int col = 4 * (threadIdx.x % kLanes);
+        float top = kNegInf, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[w][0][i]);
+        f32x4 x = gdr::zero4();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w > last) break;
+            const float a = __builtin_amdgcn_exp2f(stat[w][0][i] - top);
+            l += a * stat[w][1][i];
+            x += a * get_row<D>(lds[w], i, col);
         }
+        const int64_t to = (at.tok + at.at + i) * p.Hq + h;
+        if (p.lse && col == 0) p.lse[to] = (top + __builtin_amdgcn_logf(l)) * kLn2;
+        store_y(p, to * D + col, x * (1.f / l));
+    }
 }
 
 template <typename T, int D>
@@ -184,7 +267,13 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.v_stride = a.v_stride;
     p.group = (int)(a.Hq / a.Hk);
     p.scale = a.scale;
-    hipLaunchKernelGGL((attn_fwd_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
+    if (is_narrow(a.seqs.slots * a.Hq)) {
+        p.seqs = narrow(a.seqs, a.B);
+        hipLaunchKernelGGL((attn_fwd_narrow_kernel<T, D>), dim3((unsigned)(p.seqs.slots * a.Hq)), dim3(256), 0, stream,
+                           p);
+    } else {
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
+    }
     return hipGetLastError();
 }
 

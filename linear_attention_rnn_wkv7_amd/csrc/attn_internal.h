@@ -26,6 +26,13 @@ struct Seqs {
 // Workgroups of a launch whose kernel goes on by the grid where `needed` are more.
 inline unsigned grid_of(int64_t needed) { return (unsigned)(needed < (1 << 20) ? needed : 1 << 20); }
 
+// Whether a launch of so many workgroups of kTile rows takes the narrow form
+// instead (attn_device.h).
+#ifndef ATTN_NARROW
+#define ATTN_NARROW 256
+#endif
+inline bool is_narrow(int64_t workgroups) { return workgroups < ATTN_NARROW; }
+
 struct Launch {
     Seqs seqs;
     int64_t B, Hq, Hk, D;
