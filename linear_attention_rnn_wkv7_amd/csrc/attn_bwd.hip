@@ -156,41 +156,42 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_d
             if (lane < rows) ahead = p.stats[h * p.tokens + at.tok + row0 + lane];
         }
     };
-    // Waits for block `block` of head h and sends for the next one.
-    int buffer = 1;
-    auto arrive = [&](int h, int block) __attribute__((always_inline)) {
+    // From the last rows to the first, and head by head within: so the workgroups
+    // of a key head, which start together, read the same rows at the same time.
+    // Waits for the next block of rows and sends for the one behind it.
+    int buffer = 1, block = last - 1, h = h0, row0 = 0;
+    auto arrive = [&]() __attribute__((always_inline)) {
         buffer ^= 1;
+        row0 = block * kRows;
         wait_dma();
         if (wave == 0) {
             table[buffer][0][lane] = ahead[0];
             table[buffer][1][lane] = ahead[1];
         }
         __syncthreads();
-        if (block + 1 < last)
-            issue(buffer ^ 1, h, block + 1);
-        else if (h + 1 < h_end)
-            issue(buffer ^ 1, h + 1, first);
+        if (++h == h_end) {
+            h = h0;
+            --block;
+        }
+        if (block >= first) issue(buffer ^ 1, h, block);
     };
-    issue(0, h0, first);
+    issue(0, h0, block);
     const int key0 = at.at + 32 * wave;
     Keys<T, D> w;
     w.init(p, at, hk, key0, lane);
-    for (int h = h0; h < h_end; ++h) {
-        int block = first;
-        for (; block < last && block < first + kTile / kRows; ++block) {
-            arrive(h, block);
-            for (int t = 0; t < 2; ++t)
-                if (block * kRows + 32 * t + 31 >= key0 && key0 < at.len)
-                    w.template rows<true>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                                          &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t);
-        }
-        for (; block < last; ++block) {   // these rows see every key
-            arrive(h, block);
+    while (block >= first + kTile / kRows) {   // these rows see every key
+        arrive();
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-                w.template rows<false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                                       &table[buffer][0][32 * t], &table[buffer][1][32 * t], block * kRows + 32 * t);
-        }
+        for (int t = 0; t < 2; ++t)
+            w.template rows<false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                   &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t);
+    }
+    while (block >= first) {
+        arrive();
+        for (int t = 0; t < 2; ++t)
+            if (row0 + 32 * t + 31 >= key0 && key0 < at.len)
+                w.template rows<true>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                      &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t);
     }
     if (w.key >= at.len) return;
     const int64_t to = ((at.tok + w.key) * p.Hk + hk) * D;
@@ -462,14 +463,14 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     if (e != hipSuccess) return e;
     BwdArgs<T> few = p;
     few.seqs = narrow(a.seqs, a.B);
-    if (is_narrow(a.seqs.slots * a.Hk))
+    if (is_narrow(a.seqs.slots * a.Hk, a.dtype))
         hipLaunchKernelGGL((attn_dkdv_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hk)), dim3(256), 0, stream,
                            few);
     else
         hipLaunchKernelGGL((attn_dkdv_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hk)), dim3(256), 0, stream, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (is_narrow(a.seqs.slots * a.Hq))
+    if (is_narrow(a.seqs.slots * a.Hq, a.dtype))
         hipLaunchKernelGGL((attn_dq_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hq)), dim3(256), 0, stream,
                            few);
     else

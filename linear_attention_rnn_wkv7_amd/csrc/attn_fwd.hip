@@ -267,7 +267,7 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.v_stride = a.v_stride;
     p.group = (int)(a.Hq / a.Hk);
     p.scale = a.scale;
-    if (is_narrow(a.seqs.slots * a.Hq)) {
+    if (is_narrow(a.seqs.slots * a.Hq, a.dtype)) {
         p.seqs = narrow(a.seqs, a.B);
         hipLaunchKernelGGL((attn_fwd_narrow_kernel<T, D>), dim3((unsigned)(p.seqs.slots * a.Hq)), dim3(256), 0, stream,
                            p);

@@ -27,11 +27,12 @@ struct Seqs {
 inline unsigned grid_of(int64_t needed) { return (unsigned)(needed < (1 << 20) ? needed : 1 << 20); }
 
 // Whether a launch of so many workgroups of kTile rows takes the narrow form
-// instead (attn_device.h).
-#ifndef ATTN_NARROW
-#define ATTN_NARROW 256
-#endif
-inline bool is_narrow(int64_t workgroups) { return workgroups < ATTN_NARROW; }
+// instead (attn_device.h).  Forward and backward, us, wide and narrow: bf16, 1 x
+// 2048 x 8 heads of 64 (128 workgroups) 29 and 19, 81 and 48; x 16 (256) 30 and 27,
+// 83 and 85; of 128: 43 and 33, 129 and 80; 48 and 63, 140 and 156.  fp32, x 16 of 64
+// (256) 149 and 106, 505 and 325; of 128 270 and 186, 907 and 628; 4 x 512 x 32 (512)
+// of 64 59 and 79; 1 x 4096 x 16 (512) 405 and 393.
+inline bool is_narrow(int64_t workgroups, int dtype) { return workgroups < (dtype == WKV7_F32 ? 512 : 256); }
 
 struct Launch {
     Seqs seqs;
