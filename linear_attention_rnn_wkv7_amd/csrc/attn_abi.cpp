@@ -164,6 +164,7 @@ int check(const kv_cache_shape *s, wkv7::attn::CacheLaunch *L)
     if (rc != WKV7_OK) return rc;
     if (s->rows > INT32_MAX || s->T > INT32_MAX) return WKV7_ERR_UNSUPPORTED;
     L->tokens = s->packed ? s->T : s->rows * s->T;
+    if (L->tokens > INT32_MAX) return WKV7_ERR_UNSUPPORTED;
     if ((rc = check_stride(s->k_stride, s->Hk, s->D, L->tokens, &L->k_stride)) != WKV7_OK) return rc;
     if ((rc = check_stride(s->v_stride, s->Hk, s->D, L->tokens, &L->v_stride)) != WKV7_OK) return rc;
     L->rows = s->rows;

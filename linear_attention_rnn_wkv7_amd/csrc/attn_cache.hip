@@ -23,32 +23,35 @@ struct CacheArgs {
     float *ks, *vs;
     const int32_t *table, *lens, *starts;
     int64_t rows, T_, Hk, pages, max_pages, k_stride, v_stride, tokens;
-    int log_page;
+    int log_page, small;
 };
 
-// Where a token lies: its place in a head's first row of the pool, or -1.
-template <typename T>
-__device__ __forceinline__ bool find(const CacheArgs<T> &a, int64_t tok, int64_t &page, int64_t &offset, bool &owned)
+// Where a token lies: its page, and its place there, if it has one; owned: whether
+// it is a row's at all.  L lanes look for one token.
+template <int L, typename T>
+__device__ __forceinline__ bool find(const CacheArgs<T> &a, uint32_t tok, int &page, int &offset, bool &owned)
 {
-    int64_t r, i, n;
+    int r, i, n;
     if (!a.starts) {
-        r = tok / a.T_;
-        i = tok - r * a.T_;
-        n = a.T_;
+        r = (int)(tok / (uint32_t)a.T_);
+        i = (int)(tok - (uint32_t)r * (uint32_t)a.T_);
+        n = (int)a.T_;
     } else {
-        int64_t lo = 0, hi = a.rows - 1;   // the last row that starts at or before it
-        while (lo < hi) {
-            const int64_t mid = (lo + hi + 1) >> 1;
-            if (a.starts[mid] <= tok)
-                lo = mid;
-            else
-                hi = mid - 1;
+        // the last row that starts at or before it: each lane asks at one place of the range
+        const int lane = threadIdx.x % L, shift = (threadIdx.x & 63) / L * L;
+        int step = 1;
+        while ((int64_t)step * L < a.rows) step *= L;
+        for (r = 0; step; step /= L) {
+            const int64_t s = r + (int64_t)lane * step;
+            const bool before = s < a.rows && a.starts[s] <= (int)tok;
+            const int count = __popcll(__ballot(before) >> shift & ((1ull << L) - 1));
+            r += (count > 0 ? count - 1 : 0) * step;
         }
-        r = lo;
-        int64_t b = a.starts[r], e = a.starts[r + 1];
-        b = b < 0 ? 0 : b > a.tokens ? a.tokens : b;
-        e = e < b ? b : e > a.tokens ? a.tokens : e;
-        i = tok - b;
+        const int all = (int)a.tokens;
+        int b = a.starts[r], e = a.starts[r + 1];
+        b = b < 0 ? 0 : b > all ? all : b;
+        e = e < b ? b : e > all ? all : e;
+        i = (int)tok - b;
         n = e - b;
     }
     owned = i >= 0 && i < n;
@@ -56,9 +59,30 @@ __device__ __forceinline__ bool find(const CacheArgs<T> &a, int64_t tok, int64_t
     const int64_t pos = (int64_t)a.lens[r] - n + i;
     if (pos < 0 || (pos >> a.log_page) >= a.max_pages) return false;
     page = a.table[r * a.max_pages + (pos >> a.log_page)];
-    offset = pos & ((1 << a.log_page) - 1);
+    offset = (int)pos & ((1 << a.log_page) - 1);
     return page >= 0 && page < a.pages;
 }
+
+// x / by, correctly rounded.  r is 1 / by, correctly rounded, and the first quotient
+// is off by less than two units in the last place; each step adds the exact rest's
+// share, after which the quotient is off by less than one, and then rounded as it
+// should be (Markstein), unless by is one of the numbers whose last bits are all
+// set or the rest leaves the normal range: those are divided.
+struct Divide {
+    float by, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divide(float b) : by(b), r(1.f / b)
+    {
+        const uint32_t u = __builtin_bit_cast(uint32_t, b);
+        plain = !(b > 0x1p-60f && b < 0x1p60f) || (u & 0x7fffff) == 0x7fffff;
+    }
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        float q = x * r;
+        q = fmaf(fmaf(-q, by, x), r, q);
+        return fmaf(fmaf(-q, by, x), r, q);
+    }
+};
 
 template <int L>
 __device__ __forceinline__ float lanes_max(float x)
@@ -69,9 +93,8 @@ __device__ __forceinline__ float lanes_max(float x)
 }
 
 template <typename T>
-__device__ __forceinline__ f32x8 load8(const T *p)
+__device__ __forceinline__ f32x8 wide(Oct<T> x)
 {
-    const Oct<T> x = *reinterpret_cast<const Oct<T> *>(p);
     if constexpr (sizeof(T) == 4)
         return x;
     else
@@ -79,12 +102,12 @@ __device__ __forceinline__ f32x8 load8(const T *p)
 }
 
 template <typename T, int D, bool kE4m3>
-__device__ __forceinline__ void put(const T *src, char *pages, float *scales, int64_t row, int col)
+__device__ __forceinline__ void put(Oct<T> src, char *pages, float *scales, int64_t row, int col)
 {
     if constexpr (!kE4m3) {
-        *reinterpret_cast<Oct<T> *>(pages + (row * D + col) * (int64_t)sizeof(T)) = *reinterpret_cast<const Oct<T> *>(src);
+        *reinterpret_cast<Oct<T> *>(pages + (row * D + col) * (int64_t)sizeof(T)) = src;
     } else {
-        const f32x8 x = load8(src);
+        const f32x8 x = wide<T>(src);
         float top = 0.f, odd = 0.f;   // odd: NaN with an infinity or NaN among x, or 0
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -96,8 +119,16 @@ __device__ __forceinline__ void put(const T *src, char *pages, float *scales, in
         for (int d = 1; d < D / 8; d <<= 1) odd += __shfl_xor(odd, d);
         const float scale = top * (1.f / kE4m3Max) + odd, by = scale > 0.f ? scale : 1.f;
         float z[8];
+        const Divide divide(by);
+        if (divide.plain) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = fminf(fmaxf(x[j] / by, -kE4m3Max), kE4m3Max);
+            for (int j = 0; j < 8; ++j) z[j] = x[j] / by;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = divide(x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = fminf(fmaxf(z[j], -kE4m3Max), kE4m3Max);
         int lo = 0, hi = 0;
         lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[0], z[1], lo, false);
         lo = __builtin_amdgcn_cvt_pk_fp8_f32(z[2], z[3], lo, true);
@@ -134,15 +165,25 @@ __global__ void __launch_bounds__(256) kv_kernel(CacheArgs<T> a)
     const int col = 8 * (threadIdx.x % L);
     for (int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; id < a.tokens * a.Hk;   // whole heads
          id += (int64_t)gridDim.x * (256 / L)) {
-        const int64_t tok = id / a.Hk, h = id - tok * a.Hk;
-        int64_t page = 0, offset = 0;
+        uint32_t tok;
+        if (a.small)   // 32 bits hold every index of a token's head
+            tok = (uint32_t)id / (uint32_t)a.Hk;
+        else
+            tok = (uint32_t)(id / a.Hk);
+        const int64_t h = id - tok * a.Hk;
+        Oct<T> k, v;   // on their way while the place is looked for
+        if constexpr (kWrite) {
+            k = *reinterpret_cast<const Oct<T> *>(a.k + tok * a.k_stride + h * D + col);
+            v = *reinterpret_cast<const Oct<T> *>(a.v + tok * a.v_stride + h * D + col);
+        }
+        int page = 0, offset = 0;
         bool owned;
-        const bool there = find(a, tok, page, offset, owned);
+        const bool there = find<L>(a, tok, page, offset, owned);
         const int64_t row = ((page * a.Hk + h) << a.log_page) + offset;
         if constexpr (kWrite) {
             if (!there) continue;
-            put<T, D, kE4m3>(a.k + tok * a.k_stride + h * D + col, a.kp_out, a.ks, row, col);
-            put<T, D, kE4m3>(a.v + tok * a.v_stride + h * D + col, a.vp_out, a.vs, row, col);
+            put<T, D, kE4m3>(k, a.kp_out, a.ks, row, col);
+            put<T, D, kE4m3>(v, a.vp_out, a.vs, row, col);
         } else {
             if (!owned) continue;
             get<T, D, kE4m3>(a.k_out + id * D + col, a.kp, a.ks, row, col, there);
@@ -177,6 +218,7 @@ hipError_t launch_t(const CacheLaunch &a, bool write, hipStream_t stream)
     p.v_stride = a.v_stride;
     p.tokens = a.tokens;
     p.log_page = __builtin_ctzll((unsigned long long)a.page);
+    p.small = a.tokens * a.Hk < (int64_t(1) << 32);
     const int64_t per = 256 / (D / 8);
     const dim3 grid(grid_of((a.tokens * a.Hk + per - 1) / per));
     if (write)

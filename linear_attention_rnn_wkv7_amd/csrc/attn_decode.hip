@@ -51,9 +51,10 @@ struct Widen<bf16, E4m3> {
         for (int i = 0; i < 4; ++i) {
             const float f = x[i];
             const int u = __builtin_bit_cast(int, f);
-            const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(u, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(u, true);
-            y[i >> 1][2 * (i & 1)] = __builtin_bit_cast(float, pack_bf16(a[0], a[1]));
-            y[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(float, pack_bf16(b[0], b[1]));
+            const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.f, false);
+            const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u, 1.f, true);
+            y[i >> 1][2 * (i & 1)] = __builtin_bit_cast(float, a);
+            y[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(float, b);
         }
     }
 };
@@ -308,29 +309,54 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
     }
 }
 
-// The parts of a row, in order.
+// The parts of a row: a workgroup to a row, D / 4 lanes to a part, every
+// 256 / (D / 4)th of them to the same lanes; then those, in order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const float *part_o, const f32x2 *part_ml, T *y, int64_t rows,
                                                         int splits)
 {
-    constexpr int L = D / 4;
-    const int col = 4 * (threadIdx.x % L);
-    for (int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; row < rows;
-         row += (int64_t)gridDim.x * (256 / L)) {
+    constexpr int L = D / 4, G = 256 / L;
+    __shared__ __attribute__((aligned(16))) f32x4 red[G][L];
+    __shared__ float tops[G], sums[G];
+    const int lane = threadIdx.x % L, g = threadIdx.x / L;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const f32x2 *ml = part_ml + row * splits;
+        const float *po = part_o + row * splits * D + 4 * lane;
         float top = kNegInf, sum = 0.f;
-        for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[s][0]);
         f32x4 x = gdr::zero4();
+        for (int s = g; s < splits; s += G) top = fmaxf(top, ml[s][0]);
         if (top > kNegInf) {
-            for (int s = 0; s < splits; ++s) {
+            for (int s = g; s < splits; s += G) {
                 const f32x2 st = ml[s];
                 const float a = __builtin_amdgcn_exp2f(st[0] - top);
                 sum += a * st[1];
-                x += a * *reinterpret_cast<const f32x4 *>(part_o + (row * splits + s) * D + col);
+                x += a * *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
             }
-            x *= 1.f / sum;
         }
-        *reinterpret_cast<Quad<T> *>(y + row * D + col) = __builtin_convertvector(x, Quad<T>);
+        red[g][lane] = x;
+        if (lane == 0) {
+            tops[g] = top;
+            sums[g] = sum;
+        }
+        __syncthreads();
+        if (g == 0) {
+            top = kNegInf;
+#pragma unroll
+            for (int i = 0; i < G; ++i) top = fmaxf(top, tops[i]);
+            sum = 0.f;
+            x = gdr::zero4();
+            if (top > kNegInf) {
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    const float a = __builtin_amdgcn_exp2f(tops[i] - top);
+                    sum += a * sums[i];
+                    x += a * red[i][lane];
+                }
+                x *= 1.f / sum;
+            }
+            *reinterpret_cast<Quad<T> *>(y + row * D + 4 * lane) = __builtin_convertvector(x, Quad<T>);
+        }
+        __syncthreads();
     }
 }
 
@@ -364,8 +390,8 @@ hipError_t launch_t(const DecodeLaunch &a, hipStream_t stream)
                        dim3(256), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t rows = a.B * a.T * a.Hq, per = 256 / (D / 4);
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid_of((rows + per - 1) / per)), dim3(256), 0, stream,
+    const int64_t rows = a.B * a.T * a.Hq;
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(grid_of(rows)), dim3(256), 0, stream,
                        p.part_o, p.part_ml, p.y, rows, p.splits);
     return hipGetLastError();
 }

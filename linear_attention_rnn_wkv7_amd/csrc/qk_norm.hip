@@ -10,6 +10,8 @@
 // Gradients of the weights are kept in registers over a workgroup's tokens and
 // added up by a second kernel in a fixed order.
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace wkv7 {
@@ -119,33 +121,50 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(NormArgs<T> a)
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 1.f;
             if (a.w[m]) w = load8(a.w[m] + col);
-            // whole wavefronts take part in every round: heads behind the last repeat it
-            for (int i0 = 0; i0 < n * H; i0 += N) {
-                const bool live = i0 + grp < n * H;
-                const int i = live ? i0 + grp : n * H - 1;
-                const int t = i / H, h = i - t * H;
-                const int64_t tok = t0 + t;
-                const f32x8 x = load8(a.x[m] + tok * a.stride[m] + (int64_t)h * D + col);
-                const int64_t to = (tok * H + h) * D + col;
-                float r = 1.f;
-                if (a.w[m]) r = 1.f / sqrtf(lanes_sum<L>(sum8(x * x)) * (1.f / D) + a.eps);
-                f32x8 z;
-                if constexpr (!kBackward) {
-                    z = x * r * w;
-                    if (a.theta) z = turn<D>(z, cs[t], sn[t], lane, a.R, a.interleaved, 1.f);
-                } else {
-                    f32x8 dn = load8(a.dz[m] + to);
-                    if (a.theta) dn = turn<D>(dn, cs[t], sn[t], lane, a.R, a.interleaved, -1.f);
-                    z = dn;
-                    if (a.w[m]) {
-                        const f32x8 xn = x * r;
-                        if (live) dw[m] += dn * xn;
-                        dn *= w;
-                        z = r * (dn - xn * (lanes_sum<L>(sum8(dn * xn)) * (1.f / D)));
-                    }
+            // Heads i0 + grp, and N further, of these tokens.  Whole wavefronts take part:
+            // heads behind the last repeat it.
+            auto round = [&](int i0, auto count) __attribute__((always_inline)) {
+                constexpr int U = decltype(count)::value;
+                bool live[U];
+                int t[U];
+                int64_t to[U];
+                f32x8 x[U], dz[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    live[u] = i0 + u * N + grp < n * H;
+                    const int i = live[u] ? i0 + u * N + grp : n * H - 1;
+                    t[u] = (uint32_t)i / (uint32_t)H;
+                    const int h = i - t[u] * H;
+                    const int64_t tok = t0 + t[u];
+                    to[u] = (tok * H + h) * D + col;
+                    x[u] = load8(a.x[m] + tok * a.stride[m] + (int64_t)h * D + col);
+                    if constexpr (kBackward) dz[u] = load8(a.dz[m] + to[u]);
                 }
-                if (live) *reinterpret_cast<Oct<T> *>(a.out[m] + to) = __builtin_convertvector(z, Oct<T>);
-            }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float r = 1.f;
+                    if (a.w[m]) r = 1.f / sqrtf(lanes_sum<L>(sum8(x[u] * x[u])) * (1.f / D) + a.eps);
+                    f32x8 z;
+                    if constexpr (!kBackward) {
+                        z = x[u] * r * w;
+                        if (a.theta) z = turn<D>(z, cs[t[u]], sn[t[u]], lane, a.R, a.interleaved, 1.f);
+                    } else {
+                        f32x8 dn = dz[u];
+                        if (a.theta) dn = turn<D>(dn, cs[t[u]], sn[t[u]], lane, a.R, a.interleaved, -1.f);
+                        z = dn;
+                        if (a.w[m]) {
+                            const f32x8 xn = x[u] * r;
+                            if (live[u]) dw[m] += dn * xn;
+                            dn *= w;
+                            z = r * (dn - xn * (lanes_sum<L>(sum8(dn * xn)) * (1.f / D)));
+                        }
+                    }
+                    if (live[u]) *reinterpret_cast<Oct<T> *>(a.out[m] + to[u]) = __builtin_convertvector(z, Oct<T>);
+                }
+            };
+            int i0 = 0;
+            for (; i0 + N < n * H; i0 += 2 * N) round(i0, std::integral_constant<int, 2>{});
+            if (i0 < n * H) round(i0, std::integral_constant<int, 1>{});
         }
     }
     if constexpr (kBackward) {
@@ -164,21 +183,23 @@ __global__ void __launch_bounds__(256) qk_norm_kernel(NormArgs<T> a)
     }
 }
 
-// dw[m][col] = sum over the parts: a workgroup to 16 columns, 16 ranges of
-// parts in a row each, then those.
+// dw[m][col] = sum over the parts: a workgroup to 4 columns, 64 lanes to each,
+// every 64th part to the same lane; then those, in order.
 template <int D>
 __global__ void __launch_bounds__(256) qk_norm_sum_kernel(const float *part, int64_t parts, float *dwq, float *dwk)
 {
-    __shared__ float red[16][17];
-    const int col = threadIdx.x & 15, r = threadIdx.x >> 4;
-    const int64_t at = (int64_t)blockIdx.x * 16 + col;
+    __shared__ float red[64][5];
+    const int col = threadIdx.x & 3, r = threadIdx.x >> 2;
+    const int64_t at = (int64_t)blockIdx.x * 4 + col;
     float s = 0.f;
-    for (int64_t i = r; i < parts; i += 16) s += part[i * 2 * D + at];
+#pragma unroll 4
+    for (int64_t i = r; i < parts; i += 64) s += part[i * 2 * D + at];
     red[r][col] = s;
     __syncthreads();
     if (r) return;
     s = 0.f;
-    for (int i = 0; i < 16; ++i) s += red[i][col];
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) s += red[i][col];
     (at < D ? dwq : dwk)[at % D] = s;
 }
 
@@ -203,7 +224,8 @@ hipError_t launch_t(const QkNormLaunch &a, bool backward, hipStream_t stream)
     p.stride[1] = a.k_stride;
     p.T_ = a.T;
     p.tokens = a.B * a.T;
-    const int64_t parts = qk_norm_parts(p.tokens);
+    // the forward leaves nothing to add up: as many workgroups as a compute unit holds
+    const int64_t parts = backward ? qk_norm_parts(p.tokens) : p.tokens < 2048 ? p.tokens : 2048;
     p.per = (p.tokens + parts - 1) / parts;
     p.R = (int)a.R;
     p.interleaved = a.interleaved;
@@ -215,7 +237,7 @@ hipError_t launch_t(const QkNormLaunch &a, bool backward, hipStream_t stream)
     hipLaunchKernelGGL((qk_norm_kernel<T, D, true>), dim3((unsigned)parts), dim3(256), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.wq) return e;
-    hipLaunchKernelGGL((qk_norm_sum_kernel<D>), dim3(2 * D / 16), dim3(256), 0, stream, a.part, parts, a.dwq, a.dwk);
+    hipLaunchKernelGGL((qk_norm_sum_kernel<D>), dim3(2 * D / 4), dim3(256), 0, stream, a.part, parts, a.dwq, a.dwk);
     return hipGetLastError();
 }
 
