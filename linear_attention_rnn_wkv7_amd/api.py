@@ -315,7 +315,7 @@ def _raw_stream(index):
 def _launch(name, index, stream, call):
     """call(stream handle) with the device of the tensors as the current one and
     ``stream``, if given, as its stream (also for what it allocates)."""
-    if stream is None and index == torch.cuda.current_device():
+    if stream is None and index == torch._C._cuda_getDevice():
         return call(_raw_stream(index))
     if stream is not None and stream.device.index != index:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors on cuda:{index}")
@@ -330,8 +330,8 @@ def _at(t):
 def _check_like(name, t, shape, dtype, index, optional=False):
     if t is None and optional:
         return
-    if t is None or t.shape != shape or t.dtype != dtype or not t.is_cuda or t.get_device() != index \
-            or not t.is_contiguous():
+    # (the device of a tensor that is not on one is -1)
+    if t is None or t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
 
 
@@ -665,10 +665,10 @@ def residual_norm_backward(dh, dx_out, x_out, w, y=None, scale=None, *, eps=1e-6
 def _token_stride(name, t, heads, D, dtype, index, B=None, T=None):
     """Checks [B, T, heads, D] with heads end to end and rows one after the
     other; returns the elements from a token to the next (0: contiguous)."""
-    if t is None or t.dim() != 4 or t.dtype != dtype or not t.is_cuda or t.get_device() != index:
+    if t is None or t.dtype is not dtype or t.get_device() != index or t.dim() != 4:
         raise ValueError(f"{name} must be a {dtype} tensor [B, T, heads, D] on cuda:{index}")
     b, n, h, d = t.shape
-    if d != D or h != heads or (B is not None and (b, n) != (B, T)):
+    if d != D or h != heads or (B is not None and (b != B or n != T)):
         raise ValueError(f"{name} must be [{b if B is None else B}, {n if T is None else T}, {heads}, {D}]")
     if t.is_contiguous():
         return 0
@@ -689,9 +689,17 @@ def _heads(name, q, k):
 
 
 def _int32(name, t, shape, index):
-    if t is None or t.dtype != torch.int32 or t.shape != shape or not t.is_cuda or t.get_device() != index \
-            or not t.is_contiguous():
+    if t is None or t.dtype is not torch.int32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{index}")
+
+
+def _output_like(name, t, like, index):
+    """A caller's output, checked, or a new one, of another tensor's shape and
+    type (which takes half the time of one from a shape)."""
+    if t is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _check_like(name, t, like.shape, like.dtype, index)
+    return t
 
 
 @functools.lru_cache(maxsize=256)
@@ -730,7 +738,7 @@ def _attn_dims(q, k, v, seq_starts, scale):
         if B != 1 or nseq < 1:
             raise ValueError("seq_starts needs B = 1 and at least two entries")
         _int32("seq_starts", seq_starts, (nseq + 1,), at)
-    return _attn_sizes(*_attn_key(B, T, Hq, Hk, D, dt, nseq, strides, scale)), (B, T, Hq, D), (B, T, Hk, D), at
+    return _attn_sizes(*_attn_key(B, T, Hq, Hk, D, dt, nseq, strides, scale)), q.shape, at
 
 
 def attn_forward(q, k, v, *, seq_starts=None, scale=None, want_lse=False, want_record=False, stream=None, out=None):
@@ -750,13 +758,13 @@ def attn_forward(q, k, v, *, seq_starts=None, scale=None, want_lse=False, want_r
     attn_backward takes y, lse and (bf16; with fp32 there is none) record.
     ``out`` may supply (y, lse, record) tensors (None entries are allocated when
     wanted)."""
-    (_, sh, rec_bytes, _), ys, _, at = _attn_dims(q, k, v, seq_starts, scale)
+    (_, sh, _, _), ys, at = _attn_dims(q, k, v, seq_starts, scale)
     y, lse, rec = out if out is not None else (None, None, None)
 
     def call(st):
-        y_ = _output("y", y, ys, q.dtype, at)
+        y_ = _output_like("y", y, q, at)
         lse_ = _output("lse", lse, ys[:3], torch.float32, at) if want_lse else None
-        rec_ = _output("record", rec, ys, q.dtype, at) if want_record and q.dtype == torch.bfloat16 else None
+        rec_ = _output_like("record", rec, q, at) if want_record and q.dtype == torch.bfloat16 else None
         rc = _lib.lib().attn_forward(sh, *map(_at, (q, k, v, seq_starts, y_, lse_, rec_)), st)
         _lib.check("attn_forward", rc)
         return y_, lse_, rec_
@@ -770,7 +778,7 @@ def attn_backward(q, k, v, y, lse, dy, record=None, *, seq_starts=None, scale=No
     options and its y, lse and record: dict(dq, dk, dv), contiguous, dk and dv
     summed over the query heads that read them.  Without the record y's own
     rounding to bf16 enters dq and dk."""
-    (_, sh, _, need), ys, ks, at = _attn_dims(q, k, v, seq_starts, scale)
+    (_, sh, _, need), ys, at = _attn_dims(q, k, v, seq_starts, scale)
     _check_like("y", y, ys, q.dtype, at)
     _check_like("dy", dy, ys, q.dtype, at)
     _check_like("lse", lse, ys[:3], torch.float32, at)
@@ -780,8 +788,8 @@ def attn_backward(q, k, v, y, lse, dy, record=None, *, seq_starts=None, scale=No
     grads = dict(out) if out is not None else {}
 
     def call(st):
-        for n, shape in (("dq", ys), ("dk", ks), ("dv", ks)):
-            grads[n] = _output(n, grads.get(n), shape, q.dtype, at)
+        for n, like in (("dq", q), ("dk", k), ("dv", v)):
+            grads[n] = _output_like(n, grads.get(n), like, at)
         ws, wp, wb = _workspace("attn_backward", workspace, need, at)
         rc = _lib.lib().attn_backward(sh, *map(_at, (q, k, v, seq_starts, y, lse, record, dy)),
                                       *(_at(grads[n]) for n in ("dq", "dk", "dv")), wp, wb, st)
@@ -824,7 +832,7 @@ def _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved):
     if positions is not None:
         _int32("positions", positions, (B, T), at)
     key = (B, T, Hq, Hk, D, R, *strides, _VEC_DTYPES[dt], _lib.QK_NORM_INTERLEAVED if interleaved else 0, float(eps))
-    return _qk_norm_sizes(*key), (B, T, Hq, D), (B, T, Hk, D), at
+    return _qk_norm_sizes(*key), at
 
 
 def qk_norm_forward(q, k, wq=None, wk=None, theta=None, positions=None, *, eps=1e-6, interleaved=False, stream=None,
@@ -840,13 +848,14 @@ def qk_norm_forward(q, k, wq=None, wk=None, theta=None, positions=None, *, eps=1
     (n[i], n[i + R / 2]), or with ``interleaved`` (n[2 i], n[2 i + 1]).  Angles
     are formed in fp64.  ``out`` may supply (q', k'); contiguous q and k
     themselves are allowed there."""
-    (_, sh, _), qs, ks, at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
+    (_, sh, _), at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
     qz, kz = out if out is not None else (None, None)
 
     def call(st):
-        qz_ = _output("q'", qz, qs, q.dtype, at)
-        kz_ = _output("k'", kz, ks, q.dtype, at)
-        rc = _lib.lib().qk_norm_forward(sh, *map(_at, (q, k, wq, wk, theta, positions, qz_, kz_)), st)
+        qz_ = _output_like("q'", qz, q, at)
+        kz_ = _output_like("k'", kz, k, at)
+        rc = _lib.lib().qk_norm_forward(sh, q.data_ptr(), k.data_ptr(), _at(wq), _at(wk), _at(theta), _at(positions),
+                                        qz_.data_ptr(), kz_.data_ptr(), st)
         _lib.check("qk_norm_forward", rc)
         return qz_, kz_
 
@@ -858,17 +867,17 @@ def qk_norm_backward(dqz, dkz, q, k, wq=None, wk=None, theta=None, positions=Non
     """The gradients of qk_norm_forward from those of q' and k', with its
     inputs and options: dict(dq, dk, dwq, dwk), the weights' in fp32 and None
     without weights.  ``out`` may supply them; dq and dk may be dqz and dkz."""
-    (_, sh, need), qs, ks, at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
-    _check_like("dqz", dqz, qs, q.dtype, at)
-    _check_like("dkz", dkz, ks, q.dtype, at)
+    (_, sh, need), at = _qk_norm_dims(q, k, wq, wk, theta, positions, eps, interleaved)
+    _check_like("dqz", dqz, q.shape, q.dtype, at)
+    _check_like("dkz", dkz, k.shape, q.dtype, at)
     normed = wq is not None
     grads = dict(out) if out is not None else {}
 
     def call(st):
-        grads["dq"] = _output("dq", grads.get("dq"), qs, q.dtype, at)
-        grads["dk"] = _output("dk", grads.get("dk"), ks, q.dtype, at)
-        for n in ("dwq", "dwk"):
-            grads[n] = _output(n, grads.get(n), qs[3:], torch.float32, at) if normed else None
+        grads["dq"] = _output_like("dq", grads.get("dq"), q, at)
+        grads["dk"] = _output_like("dk", grads.get("dk"), k, at)
+        for n, w in (("dwq", wq), ("dwk", wk)):
+            grads[n] = _output_like(n, grads.get(n), w, at) if normed else None
         ws, wp, wb = _workspace("qk_norm_backward", workspace, need if normed else 0, at)
         rc = _lib.lib().qk_norm_backward(sh, *map(_at, (dqz, dkz, q, k, wq, wk, theta, positions)),
                                          *(_at(grads[n]) for n in ("dq", "dk", "dwq", "dwk")), wp, wb, st)
@@ -890,13 +899,14 @@ def _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dtype, at):
         raise ValueError("k_pages must be [pages, Hk, page, D] and table [rows, max_pages]")
     if k_pages.dtype not in (dtype, _E4M3):
         raise ValueError(f"k_pages: {k_pages.dtype} does not go with {dtype}: the same, or {_E4M3}")
-    ps = k_pages.shape
-    _check_like("k_pages", k_pages, ps, k_pages.dtype, at)
-    _check_like("v_pages", v_pages, ps, k_pages.dtype, at)
-    rows, most = table.shape
-    _int32("table", table, (rows, most), at)
-    _int32("lens", lens, (rows,), at)
-    small = k_pages.dtype == _E4M3
+    ps, kind = k_pages.shape, k_pages.dtype
+    if k_pages.get_device() != at or not k_pages.is_contiguous():
+        raise ValueError(f"k_pages must be a contiguous tensor on cuda:{at}")
+    _check_like("v_pages", v_pages, ps, kind, at)
+    rows, most = ts = table.shape
+    _int32("table", table, ts, at)
+    _int32("lens", lens, ts[:1], at)
+    small = kind is _E4M3
     if small:
         _check_like("k_scale", k_scale, ps[:3], torch.float32, at)
         _check_like("v_scale", v_scale, ps[:3], torch.float32, at)
@@ -936,7 +946,8 @@ def kv_write(k, v, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *,
     _, sh = _cache_shape(rows, T, Hk, D, packed, pages, page, most, sk, sv, _VEC_DTYPES[dt], kind)
 
     def call(st):
-        rc = _lib.lib().kv_write(sh, *map(_at, (k, v, k_pages, v_pages, k_scale, v_scale, table, lens, seq_starts)), st)
+        rc = _lib.lib().kv_write(sh, k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _at(k_scale),
+                                 _at(v_scale), table.data_ptr(), lens.data_ptr(), _at(seq_starts), st)
         _lib.check("kv_write", rc)
 
     return _launch("kv_write", at, stream, call)
@@ -1011,7 +1022,7 @@ def attn_decode(q, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *,
         raise ValueError("q must be an fp32 or bf16 device tensor [B, T, Hq, D]")
     at, dt = q.get_device(), q.dtype
     pages, Hk, page, D, rows, most, kind = _cache_dims(k_pages, v_pages, table, lens, k_scale, v_scale, dt, at)
-    B, T, Hq, Dq = ys = q.shape
+    B, T, Hq, _ = q.shape
     if B != rows:
         raise ValueError(f"{B} rows of q for a table of {rows}")
     if Hk == 0 or Hq == 0 or Hq % Hk != 0:
@@ -1022,9 +1033,10 @@ def attn_decode(q, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *,
     _, sh, need = _decode_sizes(B, T, Hq, Hk, D, pages, page, most, sq, _VEC_DTYPES[dt], kind, float(scale))
 
     def call(st):
-        y = _output("y", out, ys, dt, at)
+        y = _output_like("y", out, q, at)
         ws, wp, wb = _workspace("attn_decode", workspace, need, at)
-        rc = _lib.lib().attn_decode(sh, *map(_at, (q, k_pages, v_pages, k_scale, v_scale, table, lens, y)), wp, wb, st)
+        rc = _lib.lib().attn_decode(sh, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _at(k_scale), _at(v_scale),
+                                    table.data_ptr(), lens.data_ptr(), y.data_ptr(), wp, wb, st)
         _lib.check("attn_decode", rc)
         return y
 
