@@ -36,7 +36,7 @@
  * are held in fp32 or more.  With bf16 inputs the weights of v (and, in the
  * gradients, those of k, q and dy) take part in their products rounded to
  * bf16, one rounding of half a step each, as large as that of the outputs;
- * attn_decode carries them in two bf16 parts.  fp32 inputs use the fp32 matrix
+ * attn_decode carries them in two bf16 parts, over an 8-bit cache in one.  fp32 inputs use the fp32 matrix
  * instruction throughout.  Outputs are rounded once.  Results are the same bit
  * for bit from run to run: no sum depends on the order in which workgroups
  * run.  A key after a token has no weight there whatever it holds; an infinity
@@ -163,8 +163,8 @@ typedef struct {
  * tokens of row r (T, or seq_starts[r + 1] - seq_starts[r]), token i goes to
  * position lens[r] - n + i.  lens counts the new tokens.  A token whose
  * position is below 0 or past the table, or whose page is not in [0, pages), is
- * not written.  Places that two rows share must not be written by both in one
- * call (what they hold is then undefined).
+ * not written.  One place must not be written twice in a call, by two rows that
+ * share a page or by one that names a page twice: what it holds is then undefined.
  *
  * 8 bits: scale = max|x| * (1 / 448 rounded to fp32) over the D entries of a
  * token's head, in fp32, stored e4m3(x / scale), the quotient rounded to fp32,

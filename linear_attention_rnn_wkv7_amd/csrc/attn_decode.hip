@@ -3,7 +3,8 @@
 // Bound by the bytes of the cache: the queries of all heads that share a key
 // head (and of all new tokens) go over it together, kDecodeRows to a
 // workgroup, and few of them leave the matrix units idle most of the time, so
-// the weights take part in two bf16 parts at no cost.  The cache of a row is cut
+// the weights take part in two bf16 parts at no cost (over an 8-bit cache, which
+// is bound by instructions, in one).  The cache of a row is cut
 // into `splits` parts of whole steps; within a workgroup each wave takes
 // every fourth step of the part by itself, with its own running maximum, sum
 // and O^T, without a barrier: the next step's keys and values are on their
@@ -143,12 +144,13 @@ struct Step {
     }
 };
 
-// Parts hi and lo of 16 weights' operand.
-template <typename T, int D>
+// O += the weights' products with the values: in two bf16 parts, or in one where
+// the values have been rounded to 8 bits before.
+template <typename T, int D, bool kParts>
 __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w, const Tile<T, D> &tl, const char *vt)
 {
     f32x16 rest;
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (kParts) {
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
             const uint32_t u = pack_bf16(w[i], w[i + 1]);
@@ -159,17 +161,25 @@ __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w,
 #pragma unroll
     for (int ss = 0; ss < 2; ++ss) {
         const Oct<T> a = as_operand<T>(w, ss);
+        Oct<T> b;
+        if constexpr (kParts) b = as_operand<T>(rest, ss);
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) {
             const Oct<T> x = tl.col(vt, dt, ss);
             o[dt] = mma(x, a, o[dt]);
-            if constexpr (sizeof(T) == 2) o[dt] = mma(x, as_operand<T>(rest, ss), o[dt]);
+            if constexpr (kParts) o[dt] = mma(x, b, o[dt]);
         }
     }
 }
 
+// Waves on a SIMD that the registers are divided for.  2 rows of 131072 tokens, 4 new
+// ones, 32 / 8 heads, bf16, one and two: heads of 64 109 and 119 us, of 128 206 and
+// 196, in 8 bits 80 and 81, 228 and 139.
+template <typename T, int D>
+constexpr int kDecodeOccupancy = sizeof(T) == 2 ? (D == 64 ? 1 : 2) : (D == 64 ? 2 : 1);
+
 template <typename T, typename C, int D>
-__global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
+__global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_kernel(DecArgs<T> p)
 {
     using L = Tile<T, D>;
     using S = Step<T, C, D>;
@@ -217,9 +227,9 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
     const int32_t *table = p.table + b * p.max_pages;
 
     S next;
-    int64_t at = split * per + wave;
-    if (at < last) next.load(p, table, hk, at * kDecodeStep, len - at * kDecodeStep, lane);
-    for (; at < last; at += 4) {
+    const int64_t begin = split * per + wave;
+    if (begin < last) next.load(p, table, hk, begin * kDecodeStep, len - begin * kDecodeStep, lane);
+    auto step = [&](int64_t at) __attribute__((always_inline)) {
         next.land(kt, vt, scales[wave], lane);
         const bool there0 = next.there[0], there1 = next.there[1];
         if (at + 4 < last) next.load(p, table, hk, (at + 4) * kDecodeStep, len - (at + 4) * kDecodeStep, lane);
@@ -227,45 +237,58 @@ __global__ void __launch_bounds__(256, 1) attn_decode_kernel(DecArgs<T> p)
         f32x16 s = zero16();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) s = mma(tl.row(kt, ks), q[ks], s);
-        f32x16 vs;
         if (S::kE4m3) {
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const f32x4 x = *reinterpret_cast<const f32x4 *>(&scales[wave][reg_row(i, half)]);
-                const f32x4 y = *reinterpret_cast<const f32x4 *>(&scales[wave][32 + reg_row(i, half)]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i + j] *= x[j];
-                    vs[i + j] = y[j];
-                }
+                for (int j = 0; j < 4; ++j) s[i + j] *= x[j];
             }
         }
-        float top = kNegInf;
+        // Where some token sees not all of the step.  (The empty asm keeps the branch: as
+        // selects this would be done in every step.)
+        if (!(there0 && there1 && (at + 1) * kDecodeStep <= len - (p.T_ - 1))) {
+            asm volatile("");
+            const int64_t seen = sees - at * kDecodeStep;
+            const int here = seen < 0 ? 0 : seen < kDecodeStep ? (int)seen : kDecodeStep;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (at * kDecodeStep + reg_row(i, half) >= sees || !(i < 8 ? there0 : there1)) s[i] = kNegInf;
-            top = fmaxf(top, s[i]);
+            for (int i = 0; i < 16; ++i)
+                if (reg_row(i, half) >= here || !(i < 8 ? there0 : there1)) s[i] = kNegInf;
         }
-        top = fmaxf(ref, half_max(top) * c);
-        const float from = top == kNegInf ? 0.f : top;   // nothing seen yet: all weights 0
-        const float alpha = __builtin_amdgcn_exp2f(ref - from);
-        ref = top;
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        top = half_max(top) * c;
+        // a row keeps its reference until its maximum is 2^8 times what that stands for
+        const bool grown = top > ref + 8.f;
+        if (__any(grown)) {
+            asm volatile("");
+            const float to = grown ? top : ref, alpha = __builtin_amdgcn_exp2f(grown ? ref - to : 0.f);
+            ref = to;
+            l *= alpha;
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
+        }
+        const float from = ref == kNegInf ? 0.f : ref;   // nothing seen yet: all weights 0
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -from));
             sum += s[i];
         }
-        l = l * alpha + sum;
+        l += sum;
         if (S::kE4m3) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] *= vs[i];
-        }
+            for (int i = 0; i < 16; i += 4) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(&scales[wave][32 + reg_row(i, half)]);
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
-        add_values<T, D>(o, s, tl, vt);
+                for (int j = 0; j < 4; ++j) s[i + j] *= x[j];
+            }
+        }
+        add_values<T, D, sizeof(T) == 2 && !S::kE4m3>(o, s, tl, vt);
         gdr::wave_sync();
-    }
+    };
+    for (int64_t at = begin; at < last; at += 4) step(at);
 
     // the four waves
     l = half_sum(l);

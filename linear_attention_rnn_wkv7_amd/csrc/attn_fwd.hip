@@ -7,7 +7,7 @@
 // only when p would pass 2^8.
 //
 // A workgroup of four waves has kTile rows of one head, 32 to a wave, which
-// hold q (operand) and O^T (results) in registers; keys and values go by 64
+// hold q (operand) and O^T (results) in registers; keys and values go by blocks
 // through two buffers in LDS, the next copied while one is computed.  The narrow
 // form, for few rows, has 32 of them, and each wave every fourth 32 keys.
 
@@ -31,7 +31,12 @@ struct FwdArgs {
     float scale;
 };
 
-constexpr int kKeys = 64;
+// Keys of a block.  With wide heads in bf16, 32 of them make room for a third
+// workgroup on the compute unit, which pays where the rows are short: 12288 tokens
+// in 24 prompts, 32 / 8 heads of 128, 137 us with 64 and 128 with 32; 4 x 4096 x 16 /
+// 4 290 and 279.  Heads of 64 (four workgroups either way) 666 and 714 (8 x 4096 x 32).
+template <typename T, int D>
+constexpr int kKeysOf = sizeof(T) == 2 && D == 128 ? 32 : 64;
 
 // 32 rows of a wave.
 template <typename T, int D>
@@ -127,9 +132,9 @@ __device__ __forceinline__ void store_y(const FwdArgs<T> &p, int64_t e, f32x4 x)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(FwdArgs<T> p)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) attn_fwd_kernel(FwdArgs<T> p)
 {
-    constexpr int kBytes = Tile<T, D>::bytes(kKeys);
+    constexpr int kKeys = kKeysOf<T, D>, kBytes = Tile<T, D>::bytes(kKeys);
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
@@ -165,11 +170,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_fwd_kernel(F
     int n = 0;
     for (; n < at.at / kKeys; ++n) {   // every row sees all of these
         const auto *kv = arrive(n);
-        r.template keys<2, false>(kv[0], kv[1], n * kKeys);
+        r.template keys<kKeys / 32, false>(kv[0], kv[1], n * kKeys);
     }
     for (; n < blocks; ++n) {
         const auto *kv = arrive(n);
-        if (n * kKeys <= row0 + 31 && row0 < at.len) r.template keys<2, true>(kv[0], kv[1], n * kKeys);
+        if (n * kKeys <= row0 + 31 && row0 < at.len) r.template keys<kKeys / 32, true>(kv[0], kv[1], n * kKeys);
     }
     if (r.row >= at.len) return;
     const float l = half_sum(r.l), inv = 1.f / l;
