@@ -674,7 +674,8 @@ def _token_stride(name, t, heads, D, dtype, index, B=None, T=None):
         return 0
     s = t.stride()
     step = s[1] if n > 1 else s[0] if b > 1 else 0
-    if s[3] != 1 or (h > 1 and s[2] != D) or (b > 1 and s[0] != n * step) or step % 8 != 0 or (step and step < h * D):
+    if s[3] != 1 or (h > 1 and s[2] != D) or (b > 1 and s[0] != n * step) or step % 8 != 0 \
+            or (b * n > 1 and step < h * D):
         raise ValueError(f"{name}: a token's heads must lie end to end, tokens and rows at one stride, a multiple of 8")
     return step
 
@@ -934,7 +935,8 @@ def kv_write(k, v, k_pages, v_pages, table, lens, k_scale=None, v_scale=None, *,
     448 / max|x|.  page is a power of two from 16 to 256.
 
     Tokens at positions below 0, past the table or in a page outside the pool
-    are not written.  Two rows may share pages, but not write one place."""
+    are not written.  Two rows may share pages, but one place must not be written
+    twice in a call."""
     if k.dim() != 4 or k.dtype not in _VEC_DTYPES or not k.is_cuda:
         raise ValueError("k must be an fp32 or bf16 device tensor [B, T, Hk, D]")
     at, dt = k.get_device(), k.dtype
