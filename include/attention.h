@@ -36,12 +36,12 @@
  * are held in fp32 or more.  With bf16 inputs the weights of v (and, in the
  * gradients, those of k, q and dy) take part in their products rounded to
  * bf16, one rounding of half a step each, as large as that of the outputs;
- * attn_decode carries them in two bf16 parts, over an 8-bit cache in one.  fp32 inputs use the fp32 matrix
- * instruction throughout.  Outputs are rounded once.  Results are the same bit
- * for bit from run to run: no sum depends on the order in which workgroups
- * run.  A key after a token has no weight there whatever it holds; an infinity
- * or NaN in its v (in the gradients, in the q or dy of a token before a key)
- * may still reach the outputs of tokens less than 64 before it.
+ * attn_decode carries them in two bf16 parts, over an 8-bit cache in one.  fp32
+ * inputs use the fp32 matrix instruction throughout.  Outputs are rounded once.
+ * Results are the same bit for bit from run to run: no sum depends on the order
+ * in which workgroups run.  A key after a token has no weight there whatever it
+ * holds; an infinity or NaN in its v (in the gradients, in the q or dy of a token
+ * before a key) may still reach the outputs of tokens less than 64 before it.
  *
  * Ownership, execution and errors as for wkv7.h: device pointers owned by the
  * caller, work enqueued on `stream`, nothing allocated or synchronised, every
@@ -61,7 +61,7 @@ extern "C" {
 
 typedef struct {
     int64_t B;      /* batch, >= 0; 1 when nseq > 0 */
-    int64_t T;      /* tokens of a row, 0 to 2^31 - 1 */
+    int64_t T;      /* tokens of a row, 0 to 2^30 */
     int64_t Hq;     /* query heads: a multiple of Hk, at most 65535 */
     int64_t Hk;     /* key heads, >= 0 */
     int64_t D;      /* head size: 64 or 128 */
@@ -187,7 +187,8 @@ int kv_read(const kv_cache_shape *shape, const void *k_pages, const void *v_page
  * already: token t of row b sees the positions below lens[b] - (T - 1 - t).
  * Positions past the table or in a page that is not in [0, pages) are seen by
  * nobody, and what lies there, or behind lens in a page, is not used.  A token
- * that sees nothing has y = 0.  lens below 0 count as 0. */
+ * that sees nothing, or nothing but scores of minus infinity, has y = 0.  lens
+ * below 0 count as 0. */
 typedef struct {
     int64_t B;           /* rows, at most 65535 */
     int64_t T;           /* new tokens of each row, >= 0 */

@@ -172,6 +172,12 @@ __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w,
     }
 }
 
+// A token that has seen nothing has 0.
+__device__ __forceinline__ f32x4 quotient(f32x4 x, float sum)
+{
+    return sum == 0.f ? gdr::zero4() : x * (1.f / sum);
+}
+
 // Waves on a SIMD that the registers are divided for.  2 rows of 131072 tokens, 4 new
 // ones, 32 / 8 heads, bf16, one and two: heads of 64 109 and 119 us, of 128 206 and
 // 196, in 8 bits 80 and 81, 228 and 139.
@@ -198,13 +204,16 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
     const int64_t hk = blockIdx.y / tiles, tile = blockIdx.y - hk * tiles, b = blockIdx.z;
     const int split = blockIdx.x;
 
-    int64_t len = p.lens[b];
-    const int64_t most = p.max_pages << p.log_page;
-    // a token sees `sees` positions; those past the table hold nothing
+    const int64_t past = p.lens[b] - p.T_, most = p.max_pages << p.log_page;
+    // a token sees `sees` positions, the tile's first and last `all` and `len` of them;
+    // those past the table hold nothing
     const int64_t r = tile * kDecodeRows + l32;
     const int64_t t = r / p.group, hq = hk * p.group + (r - t * p.group);
     const bool live = r < p.rows;
-    const int64_t sees = live ? len - (p.T_ - 1 - t) : 0;
+    const int64_t sees = live ? past + t + 1 : 0;
+    const int64_t end = (tile + 1) * kDecodeRows < p.rows ? (tile + 1) * kDecodeRows : p.rows;
+    const int64_t all = past + tile * kDecodeRows / p.group + 1;
+    int64_t len = past + (end - 1) / p.group + 1;
     len = len < 0 ? 0 : len < most ? len : most;
     const int64_t steps = (len + kDecodeStep - 1) / kDecodeStep, per = (steps + p.splits - 1) / p.splits;
     const int64_t last = (split + 1) * per < steps ? (split + 1) * per : steps;
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
     f32x16 o[D / 32];
 #pragma unroll
     for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
-    float ref = kNegInf, l = 0.f;   // ref: the maximum times c
+    float ref = kLowest, l = 0.f;   // ref: the maximum times c
     const float c = p.scale * kLog2e;
     char *kt = lds[wave], *vt = kt + kTileBytes;
     const int32_t *table = p.table + b * p.max_pages;
@@ -247,7 +256,7 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
         }
         // Where some token sees not all of the step.  (The empty asm keeps the branch: as
         // selects this would be done in every step.)
-        if (!(there0 && there1 && (at + 1) * kDecodeStep <= len - (p.T_ - 1))) {
+        if (!(there0 && there1 && (at + 1) * kDecodeStep <= len && (at + 1) * kDecodeStep <= all)) {
             asm volatile("");
             const int64_t seen = sees - at * kDecodeStep;
             const int here = seen < 0 ? 0 : seen < kDecodeStep ? (int)seen : kDecodeStep;
@@ -269,11 +278,10 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt) o[dt] *= alpha;
         }
-        const float from = ref == kNegInf ? 0.f : ref;   // nothing seen yet: all weights 0
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -from));
+            s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -ref));
             sum += s[i];
         }
         l += sum;
@@ -296,38 +304,29 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
         stat[wave][0][l32] = ref;
         stat[wave][1][l32] = l;
     }
-    float *out = reinterpret_cast<float *>(lds[wave]);
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<f32x4 *>(out + l32 * (D + 4) + 32 * dt + reg_row(i, half)) =
-                f32x4{o[dt][i], o[dt][i + 1], o[dt][i + 2], o[dt][i + 3]};
+    put_rows<D>(lds[wave], o, lane);
     __syncthreads();
     constexpr int kLanes = D / 4;   // of a row
     for (int i = threadIdx.x / kLanes; i < kDecodeRows; i += 256 / kLanes) {
         const int64_t row = tile * kDecodeRows + i;
         if (row >= p.rows) break;
         const int col = 4 * (threadIdx.x % kLanes);
-        float top = kNegInf, sum = 0.f;
+        float top = kLowest, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[w][0][i]);
         f32x4 x = gdr::zero4();
-        if (top > kNegInf) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float a = __builtin_amdgcn_exp2f(stat[w][0][i] - top);
-                sum += a * stat[w][1][i];
-                x += a * *reinterpret_cast<const f32x4 *>(reinterpret_cast<const float *>(lds[w]) + i * (D + 4) + col);
-            }
+        for (int w = 0; w < 4; ++w) {
+            const float a = __builtin_amdgcn_exp2f(stat[w][0][i] - top);
+            sum += a * stat[w][1][i];
+            x += a * get_row<D>(lds[w], i, col);
         }
         const int64_t tt = row / p.group, to = (b * p.T_ + tt) * p.Hq + hk * p.group + (row - tt * p.group);
         if (p.part_o) {
             *reinterpret_cast<f32x4 *>(p.part_o + (to * p.splits + split) * D + col) = x;
             if (col == 0) p.part_ml[to * p.splits + split] = f32x2{top, sum};
         } else {
-            x = top > kNegInf ? x * (1.f / sum) : x;
-            *reinterpret_cast<Quad<T> *>(p.y + to * D + col) = __builtin_convertvector(x, Quad<T>);
+            *reinterpret_cast<Quad<T> *>(p.y + to * D + col) = __builtin_convertvector(quotient(x, sum), Quad<T>);
         }
     }
 }
@@ -345,16 +344,14 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const float *part_o, con
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const f32x2 *ml = part_ml + row * splits;
         const float *po = part_o + row * splits * D + 4 * lane;
-        float top = kNegInf, sum = 0.f;
+        float top = kLowest, sum = 0.f;
         f32x4 x = gdr::zero4();
         for (int s = g; s < splits; s += G) top = fmaxf(top, ml[s][0]);
-        if (top > kNegInf) {
-            for (int s = g; s < splits; s += G) {
-                const f32x2 st = ml[s];
-                const float a = __builtin_amdgcn_exp2f(st[0] - top);
-                sum += a * st[1];
-                x += a * *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
-            }
+        for (int s = g; s < splits; s += G) {
+            const f32x2 st = ml[s];
+            const float a = __builtin_amdgcn_exp2f(st[0] - top);
+            sum += a * st[1];
+            x += a * *reinterpret_cast<const f32x4 *>(po + (int64_t)s * D);
         }
         red[g][lane] = x;
         if (lane == 0) {
@@ -363,21 +360,18 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const float *part_o, con
         }
         __syncthreads();
         if (g == 0) {
-            top = kNegInf;
+            top = kLowest;
 #pragma unroll
             for (int i = 0; i < G; ++i) top = fmaxf(top, tops[i]);
             sum = 0.f;
             x = gdr::zero4();
-            if (top > kNegInf) {
 #pragma unroll
-                for (int i = 0; i < G; ++i) {
-                    const float a = __builtin_amdgcn_exp2f(tops[i] - top);
-                    sum += a * sums[i];
-                    x += a * red[i][lane];
-                }
-                x *= 1.f / sum;
+            for (int i = 0; i < G; ++i) {
+                const float a = __builtin_amdgcn_exp2f(tops[i] - top);
+                sum += a * sums[i];
+                x += a * red[i][lane];
             }
-            *reinterpret_cast<Quad<T> *>(y + row * D + 4 * lane) = __builtin_convertvector(x, Quad<T>);
+            *reinterpret_cast<Quad<T> *>(y + row * D + 4 * lane) = __builtin_convertvector(quotient(x, sum), Quad<T>);
         }
         __syncthreads();
     }

@@ -32,6 +32,9 @@ using gdr::to_f32;
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNegInf = -__builtin_huge_valf();
+// Where a running maximum starts: below every score, and 0 away from itself, so
+// that scores of minus infinity have weight 0 before there is another.
+constexpr float kLowest = -__FLT_MAX__;
 
 template <typename T>
 using Oct = typename gdr::Num<T>::Oct;

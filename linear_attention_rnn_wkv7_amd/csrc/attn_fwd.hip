@@ -58,7 +58,7 @@ struct Rows {
         for (int ks = 0; ks < D / 16; ++ks) q[ks] = *reinterpret_cast<const Oct<T> *>(qp + 16 * ks);
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
-        ref = kNegInf;
+        ref = kLowest;
         l = 0.f;
         c = p.scale * kLog2e;
     }
@@ -236,13 +236,12 @@ __global__ void __launch_bounds__(256, 1) attn_fwd_narrow_kernel(FwdArgs<T> p)
     constexpr int kLanes = D / 4;
     for (int i = threadIdx.x / kLanes; i < kNarrow && at.at + i < at.len; i += 256 / kLanes) {
         const int col = 4 * (threadIdx.x % kLanes);
-        float top = kNegInf, l = 0.f;
+        float top = kLowest, l = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[w][0][i]);
         f32x4 x = gdr::zero4();
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (w > last) break;
             const float a = __builtin_amdgcn_exp2f(stat[w][0][i] - top);
             l += a * stat[w][1][i];
             x += a * get_row<D>(lds[w], i, col);

@@ -7,6 +7,10 @@ many.  Rounding errors of a sum add up like a random walk, sqrt(n) steps of
 2^-24 of its size, those of a score become errors of a weight relative to it, and
 twice that covers the exponential's own: F32 = 2 * 6 * sqrt(max(D, T)) * 2^-24
 of the root mean square of the terms' sizes x_1, 16 times that for a single element.
+dS = P (dy . v - D) is a difference of two sums of D products, each off by up to
+F32 times |dy| . |v| (y is a mean of v: for D, |dy| . y_1), however small the
+difference is: with a single key it is 0, and what is left are the two errors.
+So dq and dk are also allowed 2 F32 x_d1.
 
 bf16: one rounding of half a step, 2^-8, of the result and one of each weight:
 at most 2^-8 (|x| + x_1) for an element, on top of the bar of fp32.  Roundings are
@@ -44,15 +48,17 @@ def check(got, want, label, *, D, T, record=True, names=("y", "lse", "dq", "dk",
         half = HALF_STEP[got[n].dtype]
         size = want[n + "_1"][keep] if n + "_1" in want else w.abs() + 1
         rms = float(size.norm()) / size.numel() ** 0.5
-        extra = 0.0
+        extra = cancelled = 0.0
+        if n + "_d1" in want:
+            extra = cancelled = 2 * bar * want[n + "_d1"][keep]
         if half and n + "_d" in want:
             own = (2.0 ** -16 if record else 2.0 ** -8) * want[n + "_d"][keep]
-            extra = half * want[n + "_d1"][keep] + own
+            extra = half * want[n + "_d1"][keep] + own + cancelled
         err = (g - w).abs()
         most = half * (w.abs() + size) * (1 + half) + extra + 16 * bar * rms + 1e-30
         print(f"{label}: {n} {float(err.norm()) / max(float(w.norm()), 1e-30):.2e}", flush=True)
         assert (err <= most).all(), f"{label}: {n} off by {float((err / most).max()):.2f} bars"
-        two = bar * float(size.norm()) + 1e-30
+        two = bar * float(size.norm()) + (float(cancelled.norm()) if n + "_d1" in want else 0.0) + 1e-30
         if half:
             terms = want[n + "_2"][keep] if n + "_2" in want else torch.zeros_like(w)
             two += 1.5 * half * math.sqrt((float(w.norm()) ** 2 + float(terms.norm()) ** 2) / 3)
@@ -220,6 +226,86 @@ def test_nan_in_later_tokens():
     assert torch.equal(api.attn_forward(d["q"], d["k"], d["v"])[0][:, :301], clean[:, :301])
     d["v"][:, 301] = math.inf
     assert torch.equal(api.attn_forward(d["q"], d["k"], d["v"])[0][:, :301 - 63], clean[:, :301 - 63])
+
+
+WIDE = [
+    # B, T, Hq, Hk, D, dtype: enough workgroups of 128 rows for the forms that share the keys
+    (8, 130, 16, 16, 64, BF16), (2, 300, 96, 48, 128, BF16), (3, 389, 24, 8, 128, BF16),
+    (16, 200, 32, 16, 64, F32), (6, 257, 32, 32, 128, F32), (1, 1, 520, 520, 64, F32), (257, 1, 2, 1, 128, BF16),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=["-".join(map(str, c)).replace("torch.", "") for c in WIDE])
+def test_many_workgroups(case):
+    B, T, Hq, Hk, D, dt = case
+    print(f"case {case}", flush=True)
+    d = inputs(B, T, Hq, Hk, D, dt, fused=B == 3)
+    check(run(d), reference(d), str(case), D=D, T=T)
+
+
+@pytest.mark.parametrize("dt, D, Hq, Hk", [(BF16, 64, 6, 3), (BF16, 128, 4, 4), (F32, 64, 8, 8), (F32, 128, 16, 8)])
+def test_many_workgroups_packed(dt, D, Hq, Hk):
+    gen = torch.Generator().manual_seed(14)
+    n = torch.randint(0, 200, (60,), generator=gen)
+    n[7], n[8], n[20], n[40] = 0, 1, 128, 385
+    starts = [5] + (5 + n.cumsum(0)).tolist()
+    T = starts[-1] + 9
+    d = inputs(1, T, Hq, Hk, D, dt, seed=15)
+    check(run(d, starts=starts), reference(d, starts=starts), f"{dt} {D}", D=D, T=385)
+
+
+def test_nothing_to_do():
+    for B, T in ((0, 5), (3, 0), (0, 0)):
+        q, k = torch.zeros(B, T, 4, 64, device="cuda"), torch.zeros(B, T, 2, 64, device="cuda")
+        y, lse, rec = api.attn_forward(q, k, k, want_lse=True, want_record=True)
+        assert y.shape == q.shape and lse.shape == q.shape[:3] and rec is None
+        g = api.attn_backward(q, k, k, y, lse, q)
+        assert g["dq"].shape == q.shape and g["dk"].shape == k.shape
+        w = torch.ones(64, device="cuda")
+        assert api.qk_norm_forward(q, k, w, w)[0].shape == q.shape
+        g = api.qk_norm_backward(q, k, q, k, w, w)
+        assert (g["dwq"] == 0).all() and (g["dwk"] == 0).all()
+        c = cache(max(B, 1), 2, 16, 2, 64, F32, F32)
+        if B == 0:
+            c["table"] = c["table"][:0]
+        ln = torch.ones(B, dtype=torch.int32, device="cuda")
+        before = c["k_pages"].clone()
+        api.kv_write(k, k, *cargs(c, ln))
+        assert torch.equal(before, c["k_pages"])
+        assert api.kv_read(*cargs(c, ln), T=T)[0].shape == k.shape
+        assert api.attn_decode(q, *cargs(c, ln)).shape == q.shape
+
+
+def test_scores_of_minus_infinity():
+    """Keys whose scores are minus infinity have no weight, also where no other
+    came before them; a token with no other key has NaN."""
+    for dt, B in ((BF16, 1), (F32, 1), (BF16, 130), (F32, 130)):
+        d = inputs(B, 200, 2, 1, 64, dt, seed=16)
+        d["q"].abs_().add_(0.1)
+        d["k"][:, :90] = -math.inf
+        y, lse, _ = api.attn_forward(d["q"], d["k"], d["v"], want_lse=True)
+        assert torch.isnan(y[:, :90]).all() and (lse[:, :90] == -math.inf).all()
+        want = R.attention(d["q"][:, 90:], d["k"][:, 90:], d["v"][:, 90:], d["dy"][:, 90:])
+        check(dict(y=y[:, 90:], lse=lse[:, 90:]), want, f"{dt} {B}", D=64, T=200)
+
+
+def test_offsets_past_32_bits():
+    """Parts of rows so wide that the last tokens' elements are past 2^31."""
+    x = torch.empty(1, 600, 65536, 64, dtype=BF16, device="cuda")
+    d = inputs(1, 600, 4, 2, 64, BF16, seed=17)
+    far = dict(q=x[:, :, 40000:40004], k=x[:, :, 65000:65002], v=x[:, :, 65534:], dy=d["dy"])
+    for n in "qkv":
+        far[n].copy_(d[n])
+    a, b = run(d), run(far)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    theta = (10000.0 ** (-torch.arange(0, 64, 2) / 64)).float().cuda()
+    w = torch.ones(64, device="cuda")
+    for i, j in zip(api.qk_norm_forward(d["q"], d["k"], w, w, theta), api.qk_norm_forward(far["q"], far["k"], w, w, theta)):
+        assert torch.equal(i, j)
+    g, h = (api.qk_norm_backward(a["dq"], a["dk"], t["q"], t["k"], w, w, theta) for t in (d, far))
+    for n in g:
+        assert torch.equal(g[n], h[n]), n
 
 
 def test_same_bits_every_time():
@@ -538,6 +624,76 @@ def test_decode_bad_pages(kind):
     assert ((y.cpu().double() - want["y"]).abs() <= decode_bar(want, 64, 64, BF16, kind)).all()
 
 
+@pytest.mark.parametrize("kind", [F32, E4M3])
+def test_decode_many_tokens(kind):
+    """More new tokens than a workgroup has; what a later one holds does not reach
+    those 64 before it, and a token's NaN stays its own."""
+    T, n = 150, 331
+    c = cache(2, 24, 16, 2, 64, F32, kind, seed=37)
+    gen = torch.Generator().manual_seed(38)
+    q = randn(gen, 2, T, 6, 64).cuda()
+    lens = [n, 100]         # the second row's first 50 tokens see nothing
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    y = api.attn_decode(q, *cargs(c, ln))
+    want = R.decode(q, dense(c, "k"), dense(c, "v"), c["table"].tolist(), lens)
+    assert ((y.cpu().double() - want["y"]).abs() <= decode_bar(want, 64, n, F32, kind)).all()
+    assert (y[1, :50] == 0).all()
+    page, at = int(c["table"][0, 320 // 16]), 320 % 16
+    if kind is E4M3:
+        c["v_scale"][page, :, at] = math.nan
+    else:
+        c["v_pages"][page, :, at] = math.nan
+    q[0, 3, 1] = math.nan
+    z = api.attn_decode(q, *cargs(c, ln))
+    assert torch.isnan(z[0, T - (n - 320):]).all() and torch.isnan(z[0, 3, 1]).all()
+    z[0, 3, 1] = y[0, 3, 1]
+    keep = T - (n - 320) - 64
+    assert torch.equal(z[0, :keep], y[0, :keep]) and torch.equal(z[1], y[1])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_decode_scores_of_minus_infinity(dt):
+    c = cache(1, 9, 32, 1, 64, dt, dt, seed=39)
+    k = torch.zeros(1, 288, 1, 64, dtype=dt, device="cuda")
+    gen = torch.Generator().manual_seed(40)
+    k.copy_(randn(gen, 1, 288, 1, 64))
+    v = randn(gen, 1, 288, 1, 64).to(dt).cuda()
+    q = (randn(gen, 1, 1, 4, 64).abs() + 0.1).to(dt).cuda()
+    ln = torch.tensor([288], dtype=torch.int32, device="cuda")
+    api.kv_write(k, v, *cargs(c, ln))
+    for b in c["table"][0, :5].tolist():
+        c["k_pages"][b] = -math.inf
+    y = api.attn_decode(q, *cargs(c, ln))
+    want = R.decode(q, dense(c, "k"), dense(c, "v"), [[-1] * 5 + c["table"][0, 5:].tolist()], [288])
+    assert ((y.cpu().double() - want["y"]).abs() <= decode_bar(want, 64, 288, dt, dt)).all()
+
+
+@pytest.mark.parametrize("kind", [BF16, E4M3])
+def test_cache_past_32_bits(kind):
+    """Pages whose elements lie past 2^31 in the pool."""
+    Hk, D, page, pages = 8, 128, 256, 2 ** 13 + 40
+    shape = (pages, Hk, page, D)
+    c = dict(k_pages=torch.empty(shape, dtype=kind, device="cuda"), v_pages=torch.empty(shape, dtype=kind, device="cuda"),
+             k_scale=None, v_scale=None)
+    if kind is E4M3:
+        c.update({m: torch.empty(shape[:3], device="cuda") for m in ("k_scale", "v_scale")})
+    c["table"] = torch.arange(pages - 6, pages, dtype=torch.int32, device="cuda").view(2, 3)
+    gen = torch.Generator().manual_seed(42)
+    k, v = (randn(gen, 2, 600, Hk, D).to(BF16).cuda() for _ in range(2))
+    q = randn(gen, 2, 1, 16, D).to(BF16).cuda()
+    ln = torch.tensor([600, 600], dtype=torch.int32, device="cuda")
+    small = {m: x if x is None else x[-6:].clone() for m, x in c.items()}
+    small["table"] = c["table"] - (pages - 6)
+    out = []
+    for x in (c, small):
+        api.kv_write(k, v, *cargs(x, ln))
+        out.append((*api.kv_read(*cargs(x, ln), T=600, dtype=BF16), api.attn_decode(q, *cargs(x, ln))))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+    if kind is BF16:
+        assert torch.equal(out[0][0], k) and torch.equal(out[0][1], v)
+
+
 def test_decode_shared_pages():
     """Two rows with one prefix: the same pages in both rows of the table."""
     c = cache(2, 4, 16, 1, 64, BF16, BF16, seed=35)
@@ -670,3 +826,57 @@ def test_training_step_captured():
         torch.cuda.synchronize()
         for n in want:
             assert torch.equal(got[n], want[n]), (i, n)
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured calls with one workspace, replayed in turn with eager calls between."""
+    c = cache(4, 40, 16, 2, 64, BF16, BF16, seed=70)
+    gen = torch.Generator().manual_seed(71)
+    q = [randn(gen, 4, 1 + i, 8, 64).to(BF16).cuda() for i in range(2)]
+    d = inputs(2, 200, 4, 2, 64, BF16, seed=72)
+    lens = torch.tensor([600, 17, 3, 333], dtype=torch.int32, device="cuda")
+    need = max(*(api.attn_decode_workspace_bytes(4, 1 + i, 8, 2, 64, c["k_pages"].shape[0], 16, 40) for i in range(2)),
+               api.attn_backward_workspace_bytes(2, 200, 4, 2, 64))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    args = [d[n] for n in "qkv"]
+    y, lse, rec = api.attn_forward(*args, want_lse=True, want_record=True)
+    calls = [lambda: dict(y=api.attn_decode(q[0], *cargs(c, lens), workspace=ws)),
+             lambda: dict(y=api.attn_decode(q[1], *cargs(c, lens), workspace=ws)),
+             lambda: api.attn_backward(*args, y, lse, d["dy"], rec, workspace=ws)]
+    want = [{n: x.clone() for n, x in f().items()} for f in calls]
+    graphs, got = [], []
+    for f in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(f())
+        graphs.append(g)
+    for i in range(6):
+        ws.fill_(255)
+        for j in ((i, i + 1, i + 2, i) if i % 2 else (i + 2, i)):
+            graphs[j % 3].replay()
+            for n in want[j % 3]:
+                assert torch.equal(got[j % 3][n], want[j % 3][n]), (i, j, n)
+                got[j % 3][n].zero_()
+        assert torch.equal(calls[i % 2]()["y"], want[i % 2]["y"])
+
+
+def test_two_streams_at_once():
+    d = [inputs(2, 900, 8, 4, 64, BF16, seed=80 + i) for i in range(2)]
+    want = [run(x) for x in d]
+    c = cache(3, 60, 16, 2, 128, BF16, BF16, seed=82)
+    gen = torch.Generator().manual_seed(83)
+    q = randn(gen, 3, 1, 8, 128).to(BF16).cuda()
+    lens = torch.tensor([900, 17, 400], dtype=torch.int32, device="cuda")
+    y = api.attn_decode(q, *cargs(c, lens))
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for x, s in zip(d, streams):
+            with torch.cuda.stream(s):
+                got.append((run(x), api.attn_decode(q, *cargs(c, lens))))
+    torch.cuda.synchronize()
+    for i, (g, z) in enumerate(got):
+        assert torch.equal(z, y), i
+        for n in g:
+            assert torch.equal(g[n], want[i % 2][n]), (i, n)
