@@ -7,9 +7,9 @@
 // every token and head into a table; dk and dv, a workgroup to kTile keys,
 // which goes over the queries behind them, of every query head that reads the
 // key head, in order; dq, a workgroup to kTile queries, which goes over the keys
-// before them; narrow forms of both for few of them.  The scores and dy . v are formed twice (7 products instead of
-// 5): dq would otherwise be a sum over workgroups, by atomics in an order of
-// their own.
+// before them; narrow forms of both for few of them.  The scores and dy . v are
+// formed twice (7 products instead of 5): dq would otherwise be a sum over
+// workgroups, by atomics in an order of their own.
 
 #include <type_traits>
 
@@ -128,8 +128,9 @@ struct Keys {
     }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 && D == 64 ? 2 : 1) attn_dkdv_kernel(BwdArgs<T> p)
+// kWaves: on a SIMD, that the registers are divided for.
+template <typename T, int D, int kWaves>
+__global__ void __launch_bounds__(256, kWaves) attn_dkdv_kernel(BwdArgs<T> p)
 {
     using L = Tile<T, D>;
     constexpr int kBytes = L::bytes(kRows);
@@ -463,11 +464,18 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     if (e != hipSuccess) return e;
     BwdArgs<T> few = p;
     few.seqs = narrow(a.seqs, a.B);
-    if (is_narrow(a.seqs.slots * a.Hk, a.dtype))
+    // With heads of 64 in bf16, room for a third workgroup on a compute unit pays where
+    // there are enough of them: the whole backward, us, two and three, 1 x 4096 x 24 heads
+    // (768) 206 and 215, 1 x 4096 x 32 (1024) 268 and 259, 4 x 4096 x 32 (4096) 1018 and 963.
+    constexpr bool kThree = sizeof(T) == 2 && D == 64;
+    const int64_t keys = a.seqs.slots * a.Hk;
+    if (is_narrow(keys, a.dtype))
         hipLaunchKernelGGL((attn_dkdv_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hk)), dim3(256), 0, stream,
                            few);
+    else if (kThree && keys >= 1024)
+        hipLaunchKernelGGL((attn_dkdv_kernel<T, D, kThree ? 3 : 1>), dim3((unsigned)keys), dim3(256), 0, stream, p);
     else
-        hipLaunchKernelGGL((attn_dkdv_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hk)), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL((attn_dkdv_kernel<T, D, kThree ? 2 : 1>), dim3((unsigned)keys), dim3(256), 0, stream, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (is_narrow(a.seqs.slots * a.Hq, a.dtype))
