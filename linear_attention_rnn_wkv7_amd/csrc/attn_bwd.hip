@@ -3,11 +3,11 @@
 // With P_ij = exp(s_ij - lse_i) and D_i = dy_i . y_i:
 //     dv_j = sum_i P_ij dy_i,   dS_ij = P_ij (dy_i . v_j - D_i)
 //     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i
-// P is formed again from q, k and lse.  Three kernels: D and lse log2 e of
-// every token and head into a table; dk and dv, a workgroup to kTile keys,
-// which goes over the queries behind them, of every query head that reads the
-// key head, in order; dq, a workgroup to kTile queries, which goes over the keys
-// before them; narrow forms of both for few of them.  The scores and dy . v are
+// P is formed again from q, k and lse.  Two kernels: dq, a workgroup to kTile
+// queries, which goes over the keys before them, and which leaves D and lse log2 e
+// of every token and head in a table; dk and dv, a workgroup to kTile keys, which
+// goes over the queries behind them, of every query head that reads the key head,
+// in order; narrow forms of both for few of them.  The scores and dy . v are
 // formed twice (7 products instead of 5): dq would otherwise be a sum over
 // workgroups, by atomics in an order of their own.
 
@@ -39,29 +39,6 @@ __device__ __forceinline__ f32x8 wide(Oct<T> x)
         return x;
     else
         return __builtin_convertvector(x, f32x8);
-}
-
-// D / 8 lanes to a token's head, heads side by side.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attn_stats_kernel(BwdArgs<T> p)
-{
-    constexpr int L = D / 8;
-    const int64_t all = p.tokens * p.Hq;
-    for (int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; row < all;   // whole rows
-         row += (int64_t)gridDim.x * (256 / L)) {
-        const int64_t e = row * D + 8 * (threadIdx.x % L);
-        const f32x8 dy = wide<T>(*reinterpret_cast<const Oct<T> *>(p.dy + e));
-        f32x8 y = wide<T>(*reinterpret_cast<const Oct<T> *>(p.y + e));
-        if (sizeof(T) == 2 && p.record) y += wide<bf16>(*reinterpret_cast<const bf16x8 *>(p.record + e));
-        float d = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d = fmaf(dy[j], y[j], d);
-        d = group_allreduce<L>(d);
-        if (threadIdx.x % L == 0) {
-            const int64_t tok = row / p.Hq, h = row - tok * p.Hq;
-            p.stats[h * p.tokens + tok] = f32x2{p.lse[row] * kLog2e, d};
-        }
-    }
 }
 
 constexpr int kRows = 64;   // of q and dy, or of k and v, in LDS at a time
@@ -287,7 +264,8 @@ struct Rows {
     float c;
     int row, half;
 
-    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int h, int row0, int lane)
+    // `leave`: into the table too.
+    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int h, int row0, int lane, bool leave)
     {
         tl.init(lane);
         half = lane >> 5;
@@ -299,7 +277,18 @@ struct Rows {
             q[ks] = *reinterpret_cast<const Oct<T> *>(qp + 16 * ks);
             dy[ks] = *reinterpret_cast<const Oct<T> *>(yp + 16 * ks);
         }
-        st = p.stats[h * p.tokens + r];
+        const int64_t e = (r * p.Hq + h) * D + 8 * half;
+        float d = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const f32x8 a = wide<T>(dy[ks]);
+            f32x8 y = wide<T>(*reinterpret_cast<const Oct<T> *>(p.y + e + 16 * ks));
+            if (sizeof(T) == 2 && p.record) y += wide<bf16>(*reinterpret_cast<const bf16x8 *>(p.record + e + 16 * ks));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d = fmaf(a[j], y[j], d);
+        }
+        st = f32x2{p.lse[r * p.Hq + h] * kLog2e, half_sum(d)};
+        if (leave && half == 0 && row < at.len) p.stats[h * p.tokens + r] = st;
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) dq[dt] = zero16();
         c = p.scale * kLog2e;
@@ -352,7 +341,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
     cv.issue(base + kBytes, vp, at.len, wave, lane);
     const int row0 = at.at + 32 * wave;
     Rows<T, D> r;
-    r.init(p, at, h, row0, lane);
+    r.init(p, at, h, row0, lane, true);
     auto arrive = [&](int n) __attribute__((always_inline)) {
         wait_dma();
         __syncthreads();
@@ -414,7 +403,7 @@ __global__ void __launch_bounds__(256, 1) attn_dq_narrow_kernel(BwdArgs<T> p)
     };
     if (wave <= last) send(wave);
     Rows<T, D> r;
-    r.init(p, at, h, at.at, lane);
+    r.init(p, at, h, at.at, lane, wave == 0);
     for (int n = wave; n <= last; n += 4) {
         wait_dma();
         if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
@@ -457,13 +446,15 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.tokens = a.B * a.seqs.T;
     p.group = (int)(a.Hq / a.Hk);
     p.scale = a.scale;
-    const int64_t per = 256 / (D / 8);
-    hipLaunchKernelGGL((attn_stats_kernel<T, D>), dim3(grid_of((p.tokens * a.Hq + per - 1) / per)), dim3(256), 0,
-                       stream, p);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
     BwdArgs<T> few = p;
     few.seqs = narrow(a.seqs, a.B);
+    if (is_narrow(a.seqs.slots * a.Hq, a.dtype))
+        hipLaunchKernelGGL((attn_dq_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hq)), dim3(256), 0, stream,
+                           few);
+    else
+        hipLaunchKernelGGL((attn_dq_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     // With heads of 64 in bf16, room for a third workgroup on a compute unit pays where
     // there are enough of them: the whole backward, us, two and three, 1 x 4096 x 24 heads
     // (768) 206 and 215, 1 x 4096 x 32 (1024) 268 and 259, 4 x 4096 x 32 (4096) 1018 and 963.
@@ -476,13 +467,6 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
         hipLaunchKernelGGL((attn_dkdv_kernel<T, D, kThree ? 3 : 1>), dim3((unsigned)keys), dim3(256), 0, stream, p);
     else
         hipLaunchKernelGGL((attn_dkdv_kernel<T, D, kThree ? 2 : 1>), dim3((unsigned)keys), dim3(256), 0, stream, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (is_narrow(a.seqs.slots * a.Hq, a.dtype))
-        hipLaunchKernelGGL((attn_dq_narrow_kernel<T, D>), dim3((unsigned)(few.seqs.slots * a.Hq)), dim3(256), 0, stream,
-                           few);
-    else
-        hipLaunchKernelGGL((attn_dq_kernel<T, D>), dim3((unsigned)(a.seqs.slots * a.Hq)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
 
