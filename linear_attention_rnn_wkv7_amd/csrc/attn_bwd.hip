@@ -29,6 +29,7 @@ struct BwdArgs {
     f32x2 *stats;   // [Hq][tokens]: lse log2 e, D
     int64_t B, Hq, Hk, q_stride, k_stride, v_stride, tokens;
     int group;
+    uint32_t chunk_q, chunk_k;   // units of a die at a time, of queries and of keys
     float scale;
 };
 
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(256, kWaves) attn_dkdv_kernel(BwdArgs<T> p)
     __shared__ __attribute__((aligned(16))) float table[2][2][kRows];   // [buffer][lse, D]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, hk;
-    unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
+    unit_of(p.seqs, p.B, p.Hk, p.chunk_k, false, blockIdx.x, slot, hk);
     const Place at = locate<kTile>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int first = at.at / kRows, last = (at.len + kRows - 1) / kRows;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(256, 1) attn_dkdv_narrow_kernel(BwdArgs<T> p)
     __shared__ __attribute__((aligned(16))) float table[4][2][32];   // lse, D
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, hk;
-    unit_of(p.seqs, p.B, p.Hk, false, blockIdx.x, slot, hk);
+    unit_of(p.seqs, p.B, p.Hk, p.chunk_k, false, blockIdx.x, slot, hk);
     const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int first = at.at / 32, per = (at.len + 31) / 32 - first;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    unit_of(p.seqs, p.B, p.Hq, p.chunk_q, true, blockIdx.x, slot, h);
     const Place at = locate<kTile>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(256, 1) attn_dq_narrow_kernel(BwdArgs<T> p)
     __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    unit_of(p.seqs, p.B, p.Hq, p.chunk_q, true, blockIdx.x, slot, h);
     const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
@@ -446,6 +447,9 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.tokens = a.B * a.seqs.T;
     p.group = (int)(a.Hq / a.Hk);
     p.scale = a.scale;
+    const int64_t bytes = a.seqs.T * 2 * D * (int64_t)sizeof(T);   // of k and v, or q and dy, of a head
+    p.chunk_q = chunk_of(a.seqs, a.seqs.starts ? a.Hq : a.B * a.Hq, bytes, p.group);
+    p.chunk_k = chunk_of(a.seqs, a.seqs.starts ? a.Hk : a.B * a.Hk, bytes * p.group, 1);
     BwdArgs<T> few = p;
     few.seqs = narrow(a.seqs, a.B);
     if (is_narrow(a.seqs.slots * a.Hq, a.dtype))

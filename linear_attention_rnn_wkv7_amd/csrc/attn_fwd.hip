@@ -28,6 +28,7 @@ struct FwdArgs {
     bf16 *record;
     int64_t B, Hq, Hk, q_stride, k_stride, v_stride;
     int group;
+    uint32_t chunk;
     float scale;
 };
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) attn_fwd_kernel(F
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    unit_of(p.seqs, p.B, p.Hq, p.chunk, true, blockIdx.x, slot, h);
     const Place at = locate<kTile>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(256, 1) attn_fwd_narrow_kernel(FwdArgs<T> p)
     __shared__ float stat[4][2][kNarrow];   // reference, sum
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
-    unit_of(p.seqs, p.B, p.Hq, true, blockIdx.x, slot, h);
+    unit_of(p.seqs, p.B, p.Hq, p.chunk, true, blockIdx.x, slot, h);
     const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
@@ -271,6 +272,7 @@ hipError_t launch_t(const Launch &a, hipStream_t stream)
     p.v_stride = a.v_stride;
     p.group = (int)(a.Hq / a.Hk);
     p.scale = a.scale;
+    p.chunk = chunk_of(a.seqs, a.seqs.starts ? a.Hq : a.B * a.Hq, a.seqs.T * 2 * D * (int64_t)sizeof(T), p.group);
     if (is_narrow(a.seqs.slots * a.Hq, a.dtype)) {
         p.seqs = narrow(a.seqs, a.B);
         hipLaunchKernelGGL((attn_fwd_narrow_kernel<T, D>), dim3((unsigned)(p.seqs.slots * a.Hq)), dim3(256), 0, stream,
