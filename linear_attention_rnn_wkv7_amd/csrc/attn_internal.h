@@ -98,13 +98,16 @@ struct DecodeLaunch {
 constexpr int kDecodeRows = 32;
 // Tokens of a wave's step.
 constexpr int kDecodeStep = 32;
-// Parts of the cache that are read at once: enough for four workgroups to a
-// compute unit, none under 8 steps (of which each wave has two).
+// Parts of the cache that are read at once: enough for two workgroups to a compute
+// unit, which it holds at a time, none under 8 steps (of which each wave has two).
+// 256, 512, 768 and 1024 workgroups, us, bf16: 2 rows of 131072 positions, 4 new
+// tokens, 32 / 8 heads of 64, 132, 103, 123, 105 (in 8 bits 122, 81, 102, 86); 16 of
+// 4096, 16 / 4 heads of 128, 33, 31, 36, 34.  At least 4, 8 or 16 steps: the same.
 inline int64_t decode_splits(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t capacity)
 {
     const int64_t rows = T * (Hq / Hk), units = B * Hk * ((rows + kDecodeRows - 1) / kDecodeRows);
     const int64_t steps = (capacity + kDecodeStep - 1) / kDecodeStep;
-    int64_t n = (1024 + units - 1) / units;
+    int64_t n = (512 + units - 1) / units;
     if (n > (steps + 7) / 8) n = (steps + 7) / 8;
     return n < 1 ? 1 : n;
 }

@@ -152,7 +152,7 @@ void check_decode(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64
         CHECK(attn_decode(&s, kIn, kIn, kIn, scale, scale, kInt, kInt, kIn, kWs + 16, ws, nullptr) == WKV7_ERR_WORKSPACE);
     }
     const int64_t rows = T * (Hq / Hk), tiles = (rows + kDecodeRows - 1) / kDecodeRows;
-    CHECK(B <= 65535 && Hk * tiles <= 65535 && a.splits >= 1 && a.splits <= 1024);
+    CHECK(B <= 65535 && Hk * tiles <= 65535 && a.splits >= 1 && a.splits <= 512);
     CHECK(max_pages * page <= (int64_t(1) << 30));
 }
 
