@@ -5,6 +5,11 @@
 // one pass.  The scale of a head in 8 bits is max|x| times the fp32 number
 // nearest to 1 / 448, and x is divided by it in correctly rounded fp32, so that
 // a stored value depends on nothing but its head.
+//
+// 32768 packed tokens, 8 heads of 128, bf16 to 8 bits: write 57 us (3.6 TB/s), read
+// back 37 (5.5).  The write has 378 vector instructions a wave, most of them for the
+// quotients; with the compiler's division, and each load after the last store, it
+// took 74 us, the read 43.
 
 #include "attn_device.h"
 

@@ -9,6 +9,10 @@
 //     dx = r (dn w - x r m),  m = r mean(dn w x);   dw = sum dn x r
 // Gradients of the weights are kept in registers over a workgroup's tokens and
 // added up by a second kernel in a fixed order.
+//
+// 8 x 4096 tokens, 32 / 8 heads of 64, bf16: forward 73 us (4.6 TB/s), backward 103
+// (4.9), the sum of the weights' 5.  One head at a time to a group of lanes instead
+// of two has fewer loads in flight: 78 and 117.
 
 #include <type_traits>
 
