@@ -243,15 +243,24 @@ def test_many_workgroups(case):
     check(run(d), reference(d), str(case), D=D, T=T)
 
 
-@pytest.mark.parametrize("dt, D, Hq, Hk", [(BF16, 64, 6, 3), (BF16, 128, 4, 4), (F32, 64, 8, 8), (F32, 128, 16, 8)])
-def test_many_workgroups_packed(dt, D, Hq, Hk):
+@pytest.mark.parametrize("dt, D, Hq, Hk, nseq", [(BF16, 64, 6, 3, 64), (BF16, 128, 4, 4, 65), (F32, 64, 8, 8, 90),
+                                                 (F32, 128, 16, 8, 50), (BF16, 64, 16, 8, 60), (BF16, 128, 8, 8, 64)])
+def test_many_workgroups_packed(dt, D, Hq, Hk, nseq):
     gen = torch.Generator().manual_seed(14)
-    n = torch.randint(0, 200, (60,), generator=gen)
+    n = torch.randint(0, 200, (nseq,), generator=gen)
     n[7], n[8], n[20], n[40] = 0, 1, 128, 385
     starts = [5] + (5 + n.cumsum(0)).tolist()
     T = starts[-1] + 9
     d = inputs(1, T, Hq, Hk, D, dt, seed=15)
     check(run(d, starts=starts), reference(d, starts=starts), f"{dt} {D}", D=D, T=385)
+
+
+@pytest.mark.parametrize("dt, Hq", [(BF16, 1), (F32, 8)])
+def test_one_long_sequence_among_short_ones(dt, Hq):
+    """More tiles in a sequence than the search for them looks at in one step."""
+    starts = [0, 3, 3, 40, 40 + 2090, 2140, 2269]
+    d = inputs(1, 2269, Hq, 1, 64, dt, seed=18)
+    check(run(d, starts=starts), reference(d, starts=starts), f"{dt}", D=64, T=2090)
 
 
 def test_nothing_to_do():
