@@ -14,7 +14,7 @@
 // 64 rows of 8192 positions, 32 / 8 heads of 128, bf16: 283 us, 5.7 TB/s (a large
 // copy: 5.2).  An 8-bit cache is bound by instructions: widened to bf16 and written
 // to LDS it takes as many of them as twice the bytes; 2 rows of 131072, heads of 64,
-// 57 to 62 us, 3.5 to 3.8 TB/s.  In fp32 the matrix instruction bounds it, which
+// 57 to 70 us, 3.1 to 3.8 TB/s.  In fp32 the matrix instruction bounds it, which
 // takes 8 times bf16's time for 32 rows of queries however few there are: 8 bits
 // under fp32 1.2 to 1.5 TB/s.  Two steps ahead: slower, for want of registers.
 
