@@ -111,6 +111,17 @@ __device__ __forceinline__ float half_sum(float x)
     return h.a + h.b;
 }
 
+// A pointer that is the same in all lanes, into scalar registers (what is made of it in
+// loops is else vector arithmetic as soon as it lives past them).
+template <typename T>
+__device__ __forceinline__ const T *uniform(const T *p)
+{
+    typedef const __attribute__((address_space(1))) T *Global;
+    const uint64_t b = (uint64_t)(uintptr_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = __builtin_amdgcn_readfirstlane((int)(b >> 32));
+    return (const T *)(Global)((uintptr_t)((uint64_t)hi << 32 | lo));
+}
+
 // Rows of D entries in LDS, in 16-byte pieces, 64 of them to a group: what one
 // copy straight into LDS lays end to end.  Groups are 16 or 32 bytes apart, and
 // piece p of row t lies at p ^ x(t) in its row: so the 16 rows that a read of one
@@ -360,6 +371,66 @@ struct Own {
 
 // Between a wave's reads of LDS and copies to the same place.
 __device__ __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// A value that a row does not see has weight 0, which makes nothing of it if it is
+// finite, and else NaN.  Only in the tile that the mask cuts through do some rows see
+// what others do not.  So where a result has come out not finite, all is gone over once
+// more with care: in that tile infinities and NaN stay out of the products, and the rows
+// that see them get them at the end.  The loops that run else know nothing of this: what
+// they pay is one look at the results, an instruction to two of them, and a barrier.
+// Forward, us, without and with: 12288 tokens in 24 prompts, 32 / 8 heads of 128, 140 and
+// 143; 16384 tokens, 32 / 4 heads of 64, 1120 and 1128.  Looking at the tile within the
+// loop, or leaving such values out there: 148 to 150 for the prompts.
+
+// Whether the wave's results are finite (the same in all lanes).
+template <int N>
+__device__ __forceinline__ bool all_finite(const f32x16 (&x)[N])
+{
+    float top = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(top, __builtin_fabsf(x[n][i]));
+    return !__any(!(top < -kNegInf));
+}
+// Whether they are in all four waves, which have then all read what they read from LDS.
+__device__ __forceinline__ bool all_waves(bool finite, int (&flags)[4], int wave, int lane)
+{
+    if (lane == 0) flags[wave] = finite;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(flags[0] & flags[1] & flags[2] & flags[3]);
+}
+// An operand with 0 for what is not finite.
+template <typename T>
+__device__ __forceinline__ Oct<T> finite_of(Oct<T> x)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __builtin_fabsf((float)x[j]) < -kNegInf ? x[j] : (T)0.f;
+    return x;
+}
+// acc (by columns) += what is not finite of `rows` rows of `src`, as it is, or as NaN
+// where its own score has made its weight NaN or 0; bit j of `sees`: whether the lane's
+// column sees row j.
+template <typename T, int D, bool kNan>
+__device__ __forceinline__ void add_odd(f32x16 (&acc)[D / 32], const T *src, int64_t stride, int rows, uint32_t sees,
+                                        int half)
+{
+#pragma unroll 1
+    for (int j = 0; j < rows; ++j) {
+        const bool seen = sees >> j & 1;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const Quad<T> x = *reinterpret_cast<const Quad<T> *>(src + j * stride + 32 * dt + reg_row(i, half));
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float y = (float)x[m];
+                    if (seen && !(__builtin_fabsf(y) < -kNegInf)) acc[dt][i + m] += kNan ? __builtin_nanf("") : y;
+                }
+            }
+    }
+}
 
 // A result by columns (its column on lane % 32) into LDS by rows of that, and the
 // sum of the four waves' over them, in order.

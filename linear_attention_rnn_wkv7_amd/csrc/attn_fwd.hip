@@ -58,25 +58,31 @@ struct Rows {
     Oct<T> q[D / 16];
     f32x16 o[D / 32];
     float ref, l, c;   // ref: what stands for the maximum, times c
-    int row, half;
+    int row0, row, half;
 
-    __device__ __forceinline__ void init(const FwdArgs<T> &p, const Place &at, int h, int row0, int lane)
+    __device__ __forceinline__ void init(const FwdArgs<T> &p, const Place &at, int h, int first, int lane)
     {
         tl.init(lane);
         half = lane >> 5;
+        row0 = first;
         row = row0 + (lane & 31);
         const int r = row < at.len ? row : at.len - 1;
         const T *qp = p.q + (at.tok + r) * p.q_stride + h * D + 8 * half;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) q[ks] = *reinterpret_cast<const Oct<T> *>(qp + 16 * ks);
+        c = p.scale * kLog2e;
+        clear();
+    }
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
         ref = kLowest;
         l = 0.f;
-        c = p.scale * kLog2e;
     }
-    // 32 N keys from key0 on; kMask where some row does not see all.
-    template <int N, bool kMask>
+    // 32 N keys from key0 on; kMask where some row does not see all: the tile that begins
+    // with the wave's first row is cut through, and what follows it hidden.
+    template <int N, bool kMask, bool kCareful>
     __device__ __forceinline__ void keys(const char *kt, const char *vt, int key0)
     {
         using L = Tile<T, D>;
@@ -122,10 +128,22 @@ struct Rows {
             for (int ss = 0; ss < 2; ++ss) {
                 const Oct<T> w = as_operand<T>(s[t], ss);
 #pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) o[dt] = mma(tl.col(vt, dt, 2 * t + ss), w, o[dt]);
+                for (int dt = 0; dt < D / 32; ++dt) {
+                    Oct<T> x = tl.col(vt, dt, 2 * t + ss);
+                    if (kCareful && kMask && key0 + 32 * t >= row0) x = finite_of<T>(x);
+                    o[dt] = mma(x, w, o[dt]);
+                }
             }
             l += sum[t];
         }
+    }
+    // After the last of them, with care: what was left out of the tile that is cut through.
+    __device__ __forceinline__ void finish(const T *vp, int64_t stride, int len)
+    {
+        int own = row;
+        asm volatile("" : "+v"(own));   // else a register holds row - row0 from the start
+        add_odd<T, D, false>(o, vp + row0 * stride, stride, len - row0 < 32 ? len - row0 : 32, (2u << (own - row0)) - 1,
+                             half);
     }
 };
 
@@ -145,17 +163,18 @@ __device__ __forceinline__ void store_y(const FwdArgs<T> &p, int64_t e, f32x4 x)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) attn_fwd_kernel(FwdArgs<T> p)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? (D == 64 ? 4 : 3) : 1) attn_fwd_kernel(FwdArgs<T> p)
 {
     constexpr int kKeys = kKeysOf<T, D>, kBytes = Tile<T, D>::bytes(kKeys);
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
+    __shared__ int finite[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
     unit_of(p.seqs, p.B, p.Hq, p.chunk, true, blockIdx.x, slot, h);
     const Place at = locate<kTile>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    const T *kp = uniform(p.k + at.tok * p.k_stride + hk * D), *vp = uniform(p.v + at.tok * p.v_stride + hk * D);
 
     const int end = at.at + kTile < at.len ? at.at + kTile : at.len;   // keys that any row sees
     const int blocks = (end + kKeys - 1) / kKeys;
@@ -163,8 +182,11 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) attn_fwd_kernel(F
     ck.init(p.k_stride, wave, lane);
     cv.init(p.v_stride, wave, lane);
     const unsigned base = lds_address(lds);
-    ck.issue(base, kp, at.len, wave, lane);
-    cv.issue(base + kBytes, vp, at.len, wave, lane);
+    auto first = [&]() __attribute__((always_inline)) {
+        ck.issue(base, kp, at.len, wave, lane);
+        cv.issue(base + kBytes, vp, at.len, wave, lane);
+    };
+    first();
     const int row0 = at.at + 32 * wave;
     Rows<T, D> r;
     r.init(p, at, h, row0, lane);
@@ -180,14 +202,25 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 1) attn_fwd_kernel(F
         }
         return lds[n & 1];
     };
-    int n = 0;
-    for (; n < at.at / kKeys; ++n) {   // every row sees all of these
-        const auto *kv = arrive(n);
-        r.template keys<kKeys / 32, false>(kv[0], kv[1], n * kKeys);
-    }
-    for (; n < blocks; ++n) {
-        const auto *kv = arrive(n);
-        if (n * kKeys <= row0 + 31 && row0 < at.len) r.template keys<kKeys / 32, true>(kv[0], kv[1], n * kKeys);
+    auto pass = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(careful)::value;
+        int n = 0;
+        for (; n < at.at / kKeys; ++n) {   // every row sees all of these
+            const auto *kv = arrive(n);
+            r.template keys<kKeys / 32, false, kCareful>(kv[0], kv[1], n * kKeys);
+        }
+        for (; n < blocks; ++n) {
+            const auto *kv = arrive(n);
+            if (n * kKeys <= row0 + 31 && row0 < at.len)
+                r.template keys<kKeys / 32, true, kCareful>(kv[0], kv[1], n * kKeys);
+        }
+    };
+    pass(std::false_type{});
+    if (!all_waves(all_finite(r.o), finite, wave, lane)) {
+        first();
+        r.clear();
+        pass(std::true_type{});
+        if (row0 < at.len) r.finish(vp, p.v_stride, at.len);
     }
     if (r.row >= at.len) return;
     const float l = half_sum(r.l), inv = 1.f / l;
@@ -213,7 +246,7 @@ __global__ void __launch_bounds__(256, 1) attn_fwd_narrow_kernel(FwdArgs<T> p)
     const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    const T *kp = uniform(p.k + at.tok * p.k_stride + hk * D), *vp = uniform(p.v + at.tok * p.v_stride + hk * D);
     Copy<T, D, 32, 1> ck, cv;
     ck.init(p.k_stride, 0, lane);
     cv.init(p.v_stride, 0, lane);
@@ -228,16 +261,26 @@ __global__ void __launch_bounds__(256, 1) attn_fwd_narrow_kernel(FwdArgs<T> p)
     if (wave <= last) send(wave);
     Rows<T, D> r;
     r.init(p, at, h, at.at, lane);
-    for (int n = wave; n <= last; n += 4) {
-        wait_dma();
-        if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
-        const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
-        if (n < last)
-            r.template keys<1, false>(kv, kv + O::kBytes, n * 32);
-        else
-            r.template keys<1, true>(kv, kv + O::kBytes, n * 32);
-        reads_done();
-        if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+    auto pass = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(careful)::value;
+        for (int n = wave; n <= last; n += 4) {
+            wait_dma();
+            if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
+            const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+            if (n < last)
+                r.template keys<1, false, kCareful>(kv, kv + O::kBytes, n * 32);
+            else
+                r.template keys<1, true, kCareful>(kv, kv + O::kBytes, n * 32);
+            reads_done();
+            if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+        }
+    };
+    pass(std::false_type{});
+    if (!all_finite(r.o)) {   // (a wave by itself)
+        send(wave);
+        r.clear();
+        pass(std::true_type{});
+        if (last % 4 == wave) r.finish(vp, p.v_stride, at.len);
     }
     r.l = half_sum(r.l);
     if (r.half == 0) {

@@ -1,0 +1,86 @@
+"""Values that a token does not see, on the device: infinities and NaN there
+reach nothing, and where they are seen they reach what the formulas say,
+MI355X only.
+
+A hidden value has weight 0, and 0 times any finite value is 0, so that every
+result which does not see the value has the same bits as with a finite one in
+its place: no tolerance is needed."""
+import math
+
+import pytest
+import torch
+
+from linear_attention_rnn_wkv7_amd import api
+
+pytestmark = pytest.mark.gpu
+F32, BF16, E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+
+
+def randn(gen, *s):
+    return torch.randn(s, generator=gen)
+
+
+SHAPES = [
+    # B, T, Hq, Hk, D, dtype, starts: few workgroups (the narrow form) and many (the wide one)
+    (1, 100, 2, 1, 64, BF16, None), (2, 75, 2, 2, 128, BF16, None), (1, 90, 4, 2, 64, F32, None), (1, 70, 2, 1, 128, F32, None),
+    (1, 300, 4, 2, 64, BF16, [0, 3, 3, 101, 290]),
+    (9, 233, 16, 16, 64, BF16, None), (9, 233, 32, 16, 128, BF16, None), (17, 161, 16, 16, 64, F32, None),
+    (9, 150, 32, 32, 128, F32, None), (1, 3000, 16, 8, 64, BF16, [0, 40] + [41 + 59 * i for i in range(51)]),
+]
+IDS = ["-".join(map(str, c[:6])).replace("torch.", "") + ("-packed" if c[6] else "") for c in SHAPES]
+
+
+def inputs(case, seed):
+    B, T, Hq, Hk, D, dt, starts = case
+    gen = torch.Generator().manual_seed(seed)
+    d = {n: (randn(gen, B, T, h, D)).to(dt).cuda() for n, h in (("q", Hq), ("k", Hk), ("v", Hk), ("dy", Hq))}
+    return d, None if starts is None else torch.tensor(starts, dtype=torch.int32, device="cuda")
+
+
+def places(case):
+    """(row, token, sequence's first token and end) in some sequences of the case."""
+    B, T, starts = case[0], case[1], case[6]
+    if starts is None:
+        at = [0, 1, 30, 31, 32, 33, 63, 64, 66, 95, 127, 128, 140, 160, T - 2, T - 1]
+        return [(i % B, t, 0, T) for i, t in enumerate(t for t in at if t < T)]
+    out = []
+    for lo, hi in list(zip(starts[:-1], starts[1:]))[-8:]:
+        out += [(0, t, lo, hi) for t in (lo, lo + 17, lo + 33, hi - 1) if lo <= t < hi]
+    return out
+
+
+def inside(case):
+    m = torch.zeros(case[0], case[1], dtype=torch.bool, device="cuda")
+    if case[6] is None:
+        return ~m
+    m[:, case[6][0]:case[6][-1]] = True
+    return m
+
+
+def same(a, b, keep, label):
+    """a and b are bit for bit the same where keep holds."""
+    x, y = (t.contiguous().view(torch.int32 if t.dtype is F32 else torch.int16) for t in (a, b))
+    assert (x == y)[keep].all(), label
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_forward_values(case, bad):
+    """One entry of one token's v: it reaches that entry of the tokens from there on."""
+    B, T, Hq, Hk, D, dt, _ = case
+    d, st = inputs(case, 1)
+    args = d["q"], d["k"]
+    clean, lse, rec = api.attn_forward(*args, d["v"], seq_starts=st, want_lse=True, want_record=True)
+    for n, (b, t, lo, hi) in enumerate(places(case)):
+        v, g, e = d["v"].clone(), n % Hk, (7 * n + 5) % D
+        v[b, t, g, e] = bad
+        y, lse2, rec2 = api.attn_forward(*args, v, seq_starts=st, want_lse=True, want_record=True)
+        heads = slice(g * (Hq // Hk), (g + 1) * (Hq // Hk))
+        keep = inside(case)[:, :, None, None].expand_as(y).clone()
+        keep[b, t:hi, heads, e] = False
+        same(y, clean, keep, (case, b, t))
+        if rec is not None:
+            same(rec2, rec, keep, (case, b, t))
+        same(lse2, lse, keep[..., (e + 1) % D], (case, b, t))
+        hit = y[b, t:hi, heads, e]
+        assert (torch.isnan(hit) if math.isnan(bad) else hit == bad).all(), (case, b, t)
