@@ -275,13 +275,14 @@ struct Rows {
     f32x16 dq[D / 32];
     f32x2 st;
     float c;
-    int row, half;
+    int row0, row, half;
 
     // `leave`: into the table too.
-    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int h, int row0, int lane, bool leave)
+    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int h, int first, int lane, bool leave)
     {
         tl.init(lane);
         half = lane >> 5;
+        row0 = first;
         row = row0 + (lane & 31);
         const int64_t r = at.tok + (row < at.len ? row : at.len - 1);
         const T *qp = p.q + r * p.q_stride + h * D + 8 * half, *yp = p.dy + (r * p.Hq + h) * D + 8 * half;
@@ -302,12 +303,17 @@ struct Rows {
         }
         st = f32x2{p.lse[r * p.Hq + h] * kLog2e, half_sum(d)};
         if (leave && half == 0 && row < at.len) p.stats[h * p.tokens + r] = st;
+        c = p.scale * kLog2e;
+        clear();
+    }
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) dq[dt] = zero16();
-        c = p.scale * kLog2e;
     }
-    // 32 keys from key0 on; kMask where some row does not see all of them.
-    template <bool kMask>
+    // 32 keys from key0 on; kMask where some row may not see all of them: the tile that
+    // begins with the wave's first row is cut through.
+    template <bool kMask, bool kCareful>
     __device__ __forceinline__ void keys(const char *kt, const char *vt, int key0)
     {
         f32x16 s = zero16(), ds = zero16();
@@ -326,8 +332,21 @@ struct Rows {
         for (int ss = 0; ss < 2; ++ss) {
             const Oct<T> w = as_operand<T>(ds, ss);
 #pragma unroll
-            for (int dt = 0; dt < D / 32; ++dt) dq[dt] = mma(tl.col(kt, dt, ss), w, dq[dt]);
+            for (int dt = 0; dt < D / 32; ++dt) {
+                Oct<T> x = tl.col(kt, dt, ss);
+                if (kCareful && kMask && key0 == row0) x = finite_of<T>(x);
+                dq[dt] = mma(x, w, dq[dt]);
+            }
         }
+    }
+    // After the last of them, with care: what was left out of the tile that is cut through.
+    // (A k that is not finite makes the score, and so the row's sum or its own weight.)
+    __device__ __forceinline__ void finish(const T *kp, int64_t stride, int len)
+    {
+        int own = row;
+        asm volatile("" : "+v"(own));   // else a register holds row - row0 from the start
+        add_odd<T, D, true>(dq, kp + row0 * stride, stride, len - row0 < 32 ? len - row0 : 32, (2u << (own - row0)) - 1,
+                            half);
     }
 };
 
@@ -337,21 +356,25 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
     using L = Tile<T, D>;
     constexpr int kBytes = L::bytes(kRows);
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];   // [buffer][k, v]
+    __shared__ int finite[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, h;
     unit_of(p.seqs, p.B, p.Hq, p.chunk_q, true, blockIdx.x, slot, h);
     const Place at = locate<kTile>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    const T *kp = uniform(p.k + at.tok * p.k_stride + hk * D), *vp = uniform(p.v + at.tok * p.v_stride + hk * D);
     const int end = at.at + kTile < at.len ? at.at + kTile : at.len;
     const int blocks = (end + kRows - 1) / kRows;
     Copy<T, D, kRows, 4> ck, cv;
     ck.init(p.k_stride, wave, lane);
     cv.init(p.v_stride, wave, lane);
     const unsigned base = lds_address(lds);
-    ck.issue(base, kp, at.len, wave, lane);
-    cv.issue(base + kBytes, vp, at.len, wave, lane);
+    auto first = [&]() __attribute__((always_inline)) {
+        ck.issue(base, kp, at.len, wave, lane);
+        cv.issue(base + kBytes, vp, at.len, wave, lane);
+    };
+    first();
     const int row0 = at.at + 32 * wave;
     Rows<T, D> r;
     r.init(p, at, h, row0, lane, true);
@@ -366,18 +389,29 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) attn_dq_kernel(Bw
         }
         return lds[n & 1];
     };
-    int n = 0;
-    for (; n < at.at / kRows; ++n) {   // every row sees all of these
-        const auto *kv = arrive(n);
+    auto pass = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(careful)::value;
+        int n = 0;
+        for (; n < at.at / kRows; ++n) {   // every row sees all of these
+            const auto *kv = arrive(n);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            r.template keys<false>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t);
-    }
-    for (; n < blocks; ++n) {
-        const auto *kv = arrive(n);
-        for (int t = 0; t < 2; ++t)
-            if (n * kRows + 32 * t <= row0 + 31 && row0 < at.len)
-                r.template keys<true>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t);
+            for (int t = 0; t < 2; ++t)
+                r.template keys<false, kCareful>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t, n * kRows + 32 * t);
+        }
+        for (; n < blocks; ++n) {
+            const auto *kv = arrive(n);
+            for (int t = 0; t < 2; ++t)
+                if (n * kRows + 32 * t <= row0 + 31 && row0 < at.len)
+                    r.template keys<true, kCareful>(kv[0] + L::bytes(32) * t, kv[1] + L::bytes(32) * t,
+                                                    n * kRows + 32 * t);
+        }
+    };
+    pass(std::false_type{});
+    if (!all_waves(all_finite(r.dq), finite, wave, lane)) {
+        first();
+        r.clear();
+        pass(std::true_type{});
+        if (row0 < at.len) r.finish(kp, p.k_stride, at.len);
     }
     if (r.row >= at.len) return;
     const int64_t to = ((at.tok + r.row) * p.Hq + h) * D;
@@ -402,7 +436,7 @@ __global__ void __launch_bounds__(256, 1) attn_dq_narrow_kernel(BwdArgs<T> p)
     const Place at = locate<kNarrow>(p.seqs, slot, lane);
     if (at.len == 0) return;
     const int hk = h / p.group;
-    const T *kp = p.k + at.tok * p.k_stride + hk * D, *vp = p.v + at.tok * p.v_stride + hk * D;
+    const T *kp = uniform(p.k + at.tok * p.k_stride + hk * D), *vp = uniform(p.v + at.tok * p.v_stride + hk * D);
     Copy<T, D, 32, 1> ck, cv;
     ck.init(p.k_stride, 0, lane);
     cv.init(p.v_stride, 0, lane);
@@ -417,16 +451,26 @@ __global__ void __launch_bounds__(256, 1) attn_dq_narrow_kernel(BwdArgs<T> p)
     if (wave <= last) send(wave);
     Rows<T, D> r;
     r.init(p, at, h, at.at, lane, wave == 0);
-    for (int n = wave; n <= last; n += 4) {
-        wait_dma();
-        if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
-        const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
-        if (n < last)
-            r.template keys<false>(kv, kv + O::kBytes, n * 32);
-        else
-            r.template keys<true>(kv, kv + O::kBytes, n * 32);
-        reads_done();
-        if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+    auto pass = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool kCareful = decltype(careful)::value;
+        for (int n = wave; n <= last; n += 4) {
+            wait_dma();
+            if (O::kBuffers == 2 && n + 4 <= last) send(n + 4);
+            const char *kv = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
+            if (n < last)
+                r.template keys<false, kCareful>(kv, kv + O::kBytes, n * 32);
+            else
+                r.template keys<true, kCareful>(kv, kv + O::kBytes, n * 32);
+            reads_done();
+            if (O::kBuffers == 1 && n + 4 <= last) send(n + 4);
+        }
+    };
+    pass(std::false_type{});
+    if (!all_finite(r.dq)) {   // (a wave by itself)
+        send(wave);
+        r.clear();
+        pass(std::true_type{});
+        if (last % 4 == wave) r.finish(kp, p.k_stride, at.len);
     }
     put_rows<D>(lds[wave], r.dq, lane);
     __syncthreads();

@@ -84,3 +84,29 @@ def test_forward_values(case, bad):
         same(lse2, lse, keep[..., (e + 1) % D], (case, b, t))
         hit = y[b, t:hi, heads, e]
         assert (torch.isnan(hit) if math.isnan(bad) else hit == bad).all(), (case, b, t)
+
+
+def backward(d, starts):
+    a = d["q"], d["k"], d["v"]
+    y, lse, rec = api.attn_forward(*a, seq_starts=starts, want_lse=True, want_record=True)
+    return api.attn_backward(*a, y, lse, d["dy"], rec, seq_starts=starts)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_dq(case, bad):
+    """One entry of one token's k, or of its v: dq of the tokens before it, of other
+    sequences and of other heads does not notice; from there on it is seen."""
+    B, T, Hq, Hk, D, dt, _ = case
+    d, st = inputs(case, 2)
+    clean = backward(d, st)["dq"]
+    for n, (b, t, lo, hi) in enumerate(places(case)):
+        for name in ("k", "v"):
+            x, g, e = d[name].clone(), n % Hk, (7 * n + 5) % D
+            x[b, t, g, e] = bad
+            dq = backward({**d, name: x}, st)["dq"]
+            heads = slice(g * (Hq // Hk), (g + 1) * (Hq // Hk))
+            keep = inside(case)[:, :, None, None].expand_as(dq).clone()
+            keep[b, t:hi, heads] = False
+            same(dq, clean, keep, (case, name, b, t))
+            assert not torch.isfinite(dq[b, t:hi, heads, e]).any(), (case, name, b, t)
