@@ -40,8 +40,8 @@
  * inputs use the fp32 matrix instruction throughout.  Outputs are rounded once.
  * Results are the same bit for bit from run to run: no sum depends on the order
  * in which workgroups run.  What a token does not see reaches none of its
- * outputs, whatever it holds; in the gradients, an infinity or NaN in the q or
- * dy of a token may still reach dk and dv of those less than 64 after it.
+ * outputs, whatever it holds, and none of its gradients what does not see it.
+ * Where results are not finite, their tiles are gone over a second time.
  *
  * Ownership, execution and errors as for wkv7.h: device pointers owned by the
  * caller, work enqueued on `stream`, nothing allocated or synchronised, every

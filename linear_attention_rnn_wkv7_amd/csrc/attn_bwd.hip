@@ -63,12 +63,13 @@ struct Keys {
     Oct<T> k[D / 16], v[D / 16];
     f32x16 dk[D / 32], dv[D / 32];
     float c;
-    int key, half;
+    int key0, key, half;
 
-    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int hk, int key0, int lane)
+    __device__ __forceinline__ void init(const BwdArgs<T> &p, const Place &at, int hk, int first, int lane)
     {
         tl.init(lane);
         half = lane >> 5;
+        key0 = first;
         key = key0 + (lane & 31);
         const int64_t r = at.tok + (key < at.len ? key : at.len - 1);
         const T *kp = p.k + r * p.k_stride + hk * D + 8 * half, *vp = p.v + r * p.v_stride + hk * D + 8 * half;
@@ -81,9 +82,12 @@ struct Keys {
         for (int dt = 0; dt < D / 32; ++dt) dk[dt] = dv[dt] = zero16();
         c = p.scale * kLog2e;
     }
-    // 32 rows of queries from r0 on, with their table of lse and D; kMask where some see not all keys.
-    template <bool kMask>
-    __device__ __forceinline__ void rows(const char *qt, const char *yt, const float *lses, const float *dots, int r0)
+    // 32 rows of queries from r0 on (len: the sequence's), with their table of lse and D;
+    // kMask where some may not see all keys: the tile that begins with the wave's first
+    // key is cut through.
+    template <bool kMask, bool kCareful>
+    __device__ __forceinline__ void rows(const char *qt, const char *yt, const float *lses, const float *dots, int r0,
+                                         int len)
     {
         f32x16 s = zero16(), ds = zero16();
 #pragma unroll
@@ -104,19 +108,86 @@ struct Keys {
         if constexpr (kMask) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (r0 + reg_row(i, half) < key) s[i] = ds[i] = 0.f;
+                if (r0 + reg_row(i, half) < key || (kCareful && r0 + reg_row(i, half) >= len)) s[i] = ds[i] = 0.f;
         }
 #pragma unroll
         for (int ss = 0; ss < 2; ++ss) {
             const Oct<T> w = as_operand<T>(s, ss), dw = as_operand<T>(ds, ss);
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt) {
-                dv[dt] = mma(tl.col(yt, dt, ss), w, dv[dt]);
-                dk[dt] = mma(tl.col(qt, dt, ss), dw, dk[dt]);
+                Oct<T> y = tl.col(yt, dt, ss);
+                if (kCareful && r0 == key0) y = finite_of<T>(y);
+                dv[dt] = mma(y, w, dv[dt]);
+                Oct<T> q = tl.col(qt, dt, ss);
+                if (kCareful && r0 == key0) q = finite_of<T>(q);
+                dk[dt] = mma(q, dw, dk[dt]);
             }
         }
     }
+    __device__ __forceinline__ void store(const BwdArgs<T> &p, const Place &at, int hk) const
+    {
+        const int64_t to = ((at.tok + key) * p.Hk + hk) * D;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const int64_t e = to + 32 * dt + reg_row(i, half);
+                const f32x4 a = f32x4{dk[dt][i], dk[dt][i + 1], dk[dt][i + 2], dk[dt][i + 3]} * p.scale;
+                const f32x4 b = f32x4{dv[dt][i], dv[dt][i + 1], dv[dt][i + 2], dv[dt][i + 3]};
+                *reinterpret_cast<Quad<T> *>(p.dk + e) = __builtin_convertvector(a, Quad<T>);
+                *reinterpret_cast<Quad<T> *>(p.dv + e) = __builtin_convertvector(b, Quad<T>);
+            }
+    }
+    // After the last of them, with care: what was left out of the tiles that are cut
+    // through, of all the heads.  (A q that is not finite makes its scores, and so the
+    // row's sum or its own weights.)
+    __device__ __forceinline__ void finish(const BwdArgs<T> &p, const Place &at, int hk)
+    {
+        const int count = at.len - key0 < 32 ? at.len - key0 : 32;
+        const int64_t first = at.tok + key0;
+        for (int h = hk * p.group; h < (hk + 1) * p.group; ++h) {
+            add_odd<T, D, false>(dv, p.dy + (first * p.Hq + h) * D, p.Hq * D, count, ~0u << (key - key0), half);
+            add_odd<T, D, true>(dk, p.q + first * p.q_stride + h * D, p.q_stride, count, ~0u << (key - key0), half);
+        }
+    }
 };
+
+// 32 keys by a wave, with care: after the forms below, where these have found results
+// that are not finite.  A function that is not inlined, for what it needs of registers
+// would be missing in their loops (heads of 64: 68 bytes of them in memory, two reads of
+// those between copies).  Its tiles are in `lds`, the wave's own.
+template <typename T, int D, int kWaves>
+__device__ __forceinline__ void careful_keys(const BwdArgs<T> &p, Place at, int hk, int key0, char *lds, float *table)
+{
+    using L = Tile<T, D>;
+    constexpr int kBytes = L::bytes(32);
+    Keys<T, D> w;
+    w.init(p, at, hk, key0, lane_anew());
+#pragma unroll 1
+    for (int h = hk * p.group; h < (hk + 1) * p.group; ++h)
+#pragma unroll 1
+        for (int row0 = key0; row0 < at.len; row0 += 32) {
+            const int lane = lane_anew();
+            Copy<T, D, 32, 1> cq, cy;
+            cq.init(p.q_stride, 0, lane);
+            cy.init(p.Hq * D, 0, lane);
+            const int rows = at.len - row0;   // the others are zeros, with no weights
+            cq.issue(lds_address(lds), p.q + (at.tok + row0) * p.q_stride + h * D, rows, 0, lane);
+            cy.issue(lds_address(lds) + kBytes, p.dy + ((at.tok + row0) * p.Hq + h) * D, rows, 0, lane);
+            f32x2 st = {-kNegInf, 0.f};
+            if ((lane & 31) < rows) st = p.stats[h * p.tokens + at.tok + row0 + (lane & 31)];
+            wait_dma();
+            cq.clear(lds, rows, 0, lane);
+            cy.clear(lds + kBytes, rows, 0, lane);
+            table[lane] = st[lane >> 5];
+            gdr::wave_sync();
+            w.template rows<true, true>(lds, lds + kBytes, table, table + 32, row0, at.len);
+            gdr::wave_sync();
+            reads_done();
+        }
+    w.finish(p, at, hk);
+    if (w.key < at.len) w.store(p, at, hk);
+}
 
 // kWaves: on a SIMD, that the registers are divided for.
 template <typename T, int D, int kWaves>
@@ -126,6 +197,7 @@ __global__ void __launch_bounds__(256, kWaves) attn_dkdv_kernel(BwdArgs<T> p)
     constexpr int kBytes = L::bytes(kRows);
     __shared__ __attribute__((aligned(16))) char lds[2][2][kBytes];     // [buffer][q, dy]
     __shared__ __attribute__((aligned(16))) float table[2][2][kRows];   // [buffer][lse, D]
+    __shared__ int finite[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, hk;
     unit_of(p.seqs, p.B, p.Hk, p.chunk_k, false, blockIdx.x, slot, hk);
@@ -174,28 +246,22 @@ __global__ void __launch_bounds__(256, kWaves) attn_dkdv_kernel(BwdArgs<T> p)
         arrive();
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            w.template rows<false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                                   &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t);
+            w.template rows<false, false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                          &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t, at.len);
     }
     while (block >= first) {
         arrive();
         for (int t = 0; t < 2; ++t)
             if (row0 + 32 * t + 31 >= key0 && key0 < at.len)
-                w.template rows<true>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
-                                      &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t);
+                w.template rows<true, false>(lds[buffer][0] + L::bytes(32) * t, lds[buffer][1] + L::bytes(32) * t,
+                                             &table[buffer][0][32 * t], &table[buffer][1][32 * t], row0 + 32 * t,
+                                             at.len);
     }
-    if (w.key >= at.len) return;
-    const int64_t to = ((at.tok + w.key) * p.Hk + hk) * D;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const int64_t e = to + 32 * dt + reg_row(i, w.half);
-            const f32x4 a = f32x4{w.dk[dt][i], w.dk[dt][i + 1], w.dk[dt][i + 2], w.dk[dt][i + 3]} * p.scale;
-            const f32x4 b = f32x4{w.dv[dt][i], w.dv[dt][i + 1], w.dv[dt][i + 2], w.dv[dt][i + 3]};
-            *reinterpret_cast<Quad<T> *>(p.dk + e) = __builtin_convertvector(a, Quad<T>);
-            *reinterpret_cast<Quad<T> *>(p.dv + e) = __builtin_convertvector(b, Quad<T>);
-        }
+    if (!all_waves(all_finite(w.dk) && all_finite(w.dv), finite, wave, lane)) {
+        if (key0 < at.len) careful_keys<T, D, kWaves>(p, at, hk, key0, lds[wave >> 1][wave & 1], table[wave >> 1][wave & 1]);
+        return;
+    }
+    if (w.key < at.len) w.store(p, at, hk);
 }
 
 // The sum of the four waves' results, by rows of `count` tokens, times `by`.
@@ -218,6 +284,7 @@ __global__ void __launch_bounds__(256, 1) attn_dkdv_narrow_kernel(BwdArgs<T> p)
     using O = Own<T, D>;
     __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
     __shared__ __attribute__((aligned(16))) float table[4][2][32];   // lse, D
+    __shared__ int finite[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int slot, hk;
     unit_of(p.seqs, p.B, p.Hk, p.chunk_k, false, blockIdx.x, slot, hk);
@@ -249,12 +316,16 @@ __global__ void __launch_bounds__(256, 1) attn_dkdv_narrow_kernel(BwdArgs<T> p)
         const char *qy = lds[wave] + (O::kBuffers == 2 ? (n >> 2 & 1) * 2 * O::kBytes : 0);
         const int at_row = n % per;
         if (at_row == 0)
-            w.template rows<true>(qy, qy + O::kBytes, table[wave][0], table[wave][1], first * 32);
+            w.template rows<true, false>(qy, qy + O::kBytes, table[wave][0], table[wave][1], first * 32, at.len);
         else
-            w.template rows<false>(qy, qy + O::kBytes, table[wave][0], table[wave][1], (first + at_row) * 32);
+            w.template rows<false, false>(qy, qy + O::kBytes, table[wave][0], table[wave][1], (first + at_row) * 32, at.len);
         gdr::wave_sync();
         reads_done();
         if (O::kBuffers == 1 && n + 4 < steps) send(n + 4);
+    }
+    if (!all_waves(all_finite(w.dk) && all_finite(w.dv), finite, wave, lane)) {
+        if (wave == 0) careful_keys<T, D, 0>(p, at, hk, at.at, lds[0], table[0][0]);
+        return;
     }
     const int count = at.len - at.at < kNarrow ? at.len - at.at : kNarrow;
     const int64_t to = ((at.tok + at.at) * p.Hk + hk) * D;

@@ -242,6 +242,14 @@ struct Copy {
             }
         }
     }
+    // Zeros for those that were not there, of what this wave has copied.
+    __device__ __forceinline__ void clear(char *lds, int rows, int wave, int lane) const
+    {
+#pragma unroll
+        for (int n = 0; n < kEach; ++n)
+            if ((wave * kEach + n) * L::kPerCopy + lane / L::kPieces >= rows)
+                *reinterpret_cast<f32x4 *>(lds + to + n * L::kGroup + lane * 16) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 };
 
 __device__ __forceinline__ unsigned lds_address(const void *p)
@@ -399,6 +407,14 @@ __device__ __forceinline__ bool all_waves(bool finite, int (&flags)[4], int wave
     if (lane == 0) flags[wave] = finite;
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(flags[0] & flags[1] & flags[2] & flags[3]);
+}
+// The lane's number for the pass with care: what is made of it is made anew where it is
+// used, and takes no registers elsewhere.
+__device__ __forceinline__ int lane_anew()
+{
+    uint32_t all = ~0u;
+    asm volatile("" : "+s"(all));
+    return (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
 }
 // An operand with 0 for what is not finite.
 template <typename T>

@@ -2,15 +2,18 @@
 reach nothing, and where they are seen they reach what the formulas say,
 MI355X only.
 
-A hidden value has weight 0, and 0 times any finite value is 0, so that every
-result which does not see the value has the same bits as with a finite one in
-its place: no tolerance is needed."""
+A hidden value has weight 0, and 0 times any finite value is 0, so that a result
+which does not see the value has the same bits as with a finite one in its place:
+no tolerance is needed.  (dk and dv of the tile that the value lies in are summed in
+another order then, and are compared with the oracle.)"""
 import math
 
 import pytest
 import torch
 
+import oracle.attention as R
 from linear_attention_rnn_wkv7_amd import api
+from test_attention_gpu import check
 
 pytestmark = pytest.mark.gpu
 F32, BF16, E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
@@ -110,3 +113,63 @@ def test_dq(case, bad):
             keep[b, t:hi, heads] = False
             same(dq, clean, keep, (case, name, b, t))
             assert not torch.isfinite(dq[b, t:hi, heads, e]).any(), (case, name, b, t)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_dk_dv(case, bad):
+    """One entry of one token's dy, or of its q: the keys behind it, of other sequences
+    and of other heads do not notice.  In dv the entry of a dy is seen as it is, by
+    itself; nothing of dk is finite then."""
+    B, T, Hq, Hk, D, dt, starts = case
+    d, st = inputs(case, 3)
+    if starts is not None:
+        for n in d:
+            d[n][:, ~inside(case)[0]] = 0
+    clean = backward(d, st)
+    exact = R.attention(d["q"], d["k"], d["v"], d["dy"], starts=starts)
+    longest = T if starts is None else max(b - a for a, b in zip(starts[:-1], starts[1:]))
+    for n, (b, t, lo, hi) in enumerate(places(case)):
+        for name in ("dy", "q"):
+            x, h, e = d[name].clone(), (5 * n + 1) % Hq, (7 * n + 5) % D
+            g = h * Hk // Hq
+            x[b, t, h, e] = bad
+            got = backward({**d, name: x}, st)
+            label = (case, name, b, t)
+            keep = inside(case)[:, :, None, None].expand_as(got["dk"]).clone()
+            keep[b, lo:hi, g] = False
+            for m in ("dk", "dv"):
+                same(got[m], clean[m], keep, label)
+            keep = inside(case)[:, :, None, None].expand_as(got["dq"]).clone()
+            keep[b, t, h] = False
+            same(got["dq"], clean["dq"], keep, label)
+            behind = slice(t + 1, hi)
+            want = {m: w[b:b + 1, behind, g:g + 1] for m, w in exact.items() if m[:2] in ("dk", "dv")}
+            check({m: got[m][b:b + 1, behind, g:g + 1] for m in ("dk", "dv")}, want, str(label), D=D, T=longest)
+            seen = got["dv"][b, lo:t + 1, g]
+            if name == "dy":
+                assert (torch.isnan(seen[:, e]) if math.isnan(bad) else seen[:, e] == bad).all(), label
+                assert not torch.isfinite(got["dk"][b, lo:t + 1, g]).any(), label
+                want = {m: w[b:b + 1, lo:t + 1, g:g + 1].clone() for m, w in exact.items() if m[:2] == "dv"}
+                want["dv"][..., e] = math.nan   # not compared
+                check({"dv": got["dv"][b:b + 1, lo:t + 1, g:g + 1]}, want, str(label), D=D, T=longest)
+            else:
+                assert not torch.isfinite(got["dk"][b, lo:t + 1, g, e]).any(), label
+
+
+@pytest.mark.parametrize("dt, B, H", [(BF16, 1, 2), (F32, 1, 2), (BF16, 130, 2), (F32, 130, 4)])
+def test_rows_behind_the_last(dt, B, H):
+    """A length that ends inside a tile, a key whose scores are all minus infinity and an
+    infinity in the last dy: what stands for the rows behind the last adds nothing."""
+    d, _ = inputs((B, 77, H, H, 64, dt, None), 4)
+    d["q"].abs_().add_(0.1)
+    d["k"][:, 40] = -math.inf
+    clean = backward(d, None)
+    assert torch.isfinite(clean["dk"]).all() and torch.isfinite(clean["dv"]).all()
+    assert (clean["dk"][:, 40] == 0).all() and (clean["dv"][:, 40] == 0).all()
+    dy = d["dy"].clone()
+    dy[:, -1, :, 3] = math.inf
+    dv = backward({**d, "dy": dy}, None)["dv"]
+    others = torch.arange(64, device="cuda") != 3
+    assert (dv[:, torch.arange(77) != 40, :, 3] == math.inf).all()
+    assert (dv[:, 40][..., others] == 0).all() and torch.isfinite(dv[..., others]).all()
