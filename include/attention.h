@@ -186,9 +186,11 @@ int kv_read(const kv_cache_shape *shape, const void *k_pages, const void *v_page
 /* The T last tokens of each of B rows, whose keys and values the cache holds
  * already: token t of row b sees the positions below lens[b] - (T - 1 - t).
  * Positions past the table or in a page that is not in [0, pages) are seen by
- * nobody, and what lies there, or behind lens in a page, is not used.  A token
- * that sees nothing, or nothing but scores of minus infinity, has y = 0.  lens
- * below 0 count as 0. */
+ * nobody, and what lies there, or behind lens in a page, is not used.  What a
+ * later one of the new tokens holds does not reach an earlier one, whatever it
+ * is.  A token that sees nothing, or nothing but scores of minus infinity, has
+ * y = 0.  (In bf16, whose weights have two parts, an infinity in a v that is seen
+ * gives an infinity or NaN.)  lens below 0 count as 0. */
 typedef struct {
     int64_t B;           /* rows, at most 65535 */
     int64_t T;           /* new tokens of each row, >= 0 */

@@ -18,6 +18,8 @@
 // takes 8 times bf16's time for 32 rows of queries however few there are: 8 bits
 // under fp32 1.2 to 1.5 TB/s.  Two steps ahead: slower, for want of registers.
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace wkv7 {
@@ -153,7 +155,7 @@ struct Step {
 
 // O += the weights' products with the values: in two bf16 parts, or in one where
 // the values have been rounded to 8 bits before.
-template <typename T, int D, bool kParts>
+template <typename T, int D, bool kParts, bool kFinite>
 __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w, const Tile<T, D> &tl, const char *vt)
 {
     f32x16 rest;
@@ -172,9 +174,54 @@ __device__ __forceinline__ void add_values(f32x16 (&o)[D / 32], const f32x16 &w,
         if constexpr (kParts) b = as_operand<T>(rest, ss);
 #pragma unroll
         for (int dt = 0; dt < D / 32; ++dt) {
-            const Oct<T> x = tl.col(vt, dt, ss);
+            Oct<T> x = tl.col(vt, dt, ss);
+            if constexpr (kFinite) x = finite_of<T>(x);
             o[dt] = mma(x, a, o[dt]);
             if constexpr (kParts) o[dt] = mma(x, b, o[dt]);
+        }
+    }
+}
+
+// Whether a tile's 32 rows are finite (the same in all lanes).
+template <typename T, int D>
+__device__ __forceinline__ bool tile_finite(const char *tile, int lane)
+{
+    using L = Tile<T, D>;
+    typedef T Piece __attribute__((ext_vector_type(16 / sizeof(T))));
+    float top = 0.f;
+#pragma unroll 2
+    for (int n = 0; n < 32 / L::kPerCopy; ++n) {
+        const Piece x = *reinterpret_cast<const Piece *>(tile + n * L::kGroup + lane * 16);
+#pragma unroll
+        for (int j = 0; j < 16 / (int)sizeof(T); ++j) top = __builtin_elementwise_maximum(top, __builtin_fabsf((float)x[j]));
+    }
+    return !__any(!(top < -kNegInf));
+}
+
+// What is not finite of the values of `n` tokens of the row from tok0 on, to the lanes
+// whose columns see them: the first `here` of them.
+template <typename T, typename C, int D>
+__device__ __forceinline__ void add_cached(f32x16 (&o)[D / 32], const DecArgs<T> &p, const int32_t *table, int64_t hk,
+                                           int64_t tok0, int n, int here, int half)
+{
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+        const int64_t tok = tok0 + j;
+        const int page = __builtin_amdgcn_readfirstlane(table[tok >> p.log_page]);
+        if (page < 0 || page >= p.pages) continue;
+        const int64_t row = ((page * p.Hk + hk) << p.log_page) + (tok & ((1 << p.log_page) - 1));
+        if constexpr (sizeof(C) == sizeof(T)) {
+            add_odd<T, D, false>(o, reinterpret_cast<const T *>(p.v) + row * D, 0, 1, j < here ? 1 : 0, half);
+        } else {
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const uint32_t u = *reinterpret_cast<const uint32_t *>(p.v + row * D + 32 * dt + reg_row(i, half));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)   // e4m3 has NaN, and no infinity
+                        if (j < here && (u >> 8 * m & 0x7f) == 0x7f) o[dt][i + m] += __builtin_nanf("");
+                }
         }
     }
 }
@@ -191,7 +238,11 @@ __device__ __forceinline__ f32x4 quotient(f32x4 x, float sum)
 template <typename T, int D>
 constexpr int kDecodeOccupancy = sizeof(T) == 2 ? (D == 64 ? 1 : 2) : (D == 64 ? 2 : 1);
 
-template <typename T, typename C, int D>
+// kMany: several new tokens to a row, of which the earlier ones do not see the later
+// ones' values.  The few steps where they differ run in a loop of their own, which costs
+// nothing (4 tokens over 131072, heads of 64, in 8 bits 57 and 56 us, in bf16 97 and 98);
+// the kernel for single tokens is without it.
+template <typename T, typename C, int D, bool kMany>
 __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_kernel(DecArgs<T> p)
 {
     using L = Tile<T, D>;
@@ -245,7 +296,9 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
     S next;
     const int64_t begin = split * per + wave;
     if (begin < last) next.load(p, table, hk, begin * kDecodeStep, len - begin * kDecodeStep, lane);
-    auto step = [&](int64_t at) __attribute__((always_inline)) {
+    bool odd = false;   // whether something was left out
+    auto step = [&](int64_t at, auto cut) __attribute__((always_inline)) {
+        constexpr bool kCut = decltype(cut)::value;
         next.land(kt, vt, scales[wave], lane);
         const bool there0 = next.there[0], there1 = next.there[1];
         if (at + 4 < last) next.load(p, table, hk, (at + 4) * kDecodeStep, len - (at + 4) * kDecodeStep, lane);
@@ -300,10 +353,31 @@ __global__ void __launch_bounds__(256, (kDecodeOccupancy<T, D>)) attn_decode_ker
                 for (int j = 0; j < 4; ++j) s[i + j] *= x[j];
             }
         }
-        add_values<T, D, sizeof(T) == 2 && !S::kE4m3>(o, s, tl, vt);
+        if (kCut) {
+            const int64_t seen = sees - at * kDecodeStep;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (reg_row(i, half) >= seen) s[i] = 0.f;   // also times a scale that is NaN
+            odd = odd || !tile_finite<T, D>(vt, lane);
+        }
+        add_values<T, D, sizeof(T) == 2 && !S::kE4m3, kCut>(o, s, tl, vt);
         gdr::wave_sync();
     };
-    for (int64_t at = begin; at < last; at += 4) step(at);
+    int64_t at = begin;
+    for (; at < last && (!kMany || (at + 1) * kDecodeStep <= all || all == len); at += 4) step(at, std::false_type{});
+    if constexpr (kMany) {
+        // Steps that the mask cuts through, one or two of the tile's: what is not finite of
+        // the values stays out, and the tokens that see it get it behind the last step.
+        const int64_t cut = at;
+#pragma unroll 1
+        for (; at < last; at += 4) step(at, std::true_type{});
+        if (odd)
+            for (at = cut; at < last; at += 4) {
+                const int64_t n = len - at * kDecodeStep, seen = sees - at * kDecodeStep;
+                add_cached<T, C, D>(o, p, table, hk, at * kDecodeStep, n < kDecodeStep ? (int)n : kDecodeStep,
+                                    seen < 0 ? 0 : seen < kDecodeStep ? (int)seen : kDecodeStep, half);
+            }
+    }
 
     // the four waves
     l = half_sum(l);
@@ -410,8 +484,11 @@ hipError_t launch_t(const DecodeLaunch &a, hipStream_t stream)
     p.splits = (int)a.splits;
     p.scale = a.scale;
     const int64_t tiles = (p.rows + kDecodeRows - 1) / kDecodeRows;
-    hipLaunchKernelGGL((attn_decode_kernel<T, C, D>), dim3((unsigned)a.splits, (unsigned)(a.Hk * tiles), (unsigned)a.B),
-                       dim3(256), 0, stream, p);
+    const dim3 grid((unsigned)a.splits, (unsigned)(a.Hk * tiles), (unsigned)a.B);
+    if (a.T > 1)
+        hipLaunchKernelGGL((attn_decode_kernel<T, C, D, true>), grid, dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL((attn_decode_kernel<T, C, D, false>), grid, dim3(256), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = a.B * a.T * a.Hq;

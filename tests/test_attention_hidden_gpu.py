@@ -13,7 +13,7 @@ import torch
 
 import oracle.attention as R
 from linear_attention_rnn_wkv7_amd import api
-from test_attention_gpu import check
+from test_attention_gpu import cache, cargs, check
 
 pytestmark = pytest.mark.gpu
 F32, BF16, E4M3 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
@@ -173,3 +173,48 @@ def test_rows_behind_the_last(dt, B, H):
     others = torch.arange(64, device="cuda") != 3
     assert (dv[:, torch.arange(77) != 40, :, 3] == math.inf).all()
     assert (dv[:, 40][..., others] == 0).all() and torch.isfinite(dv[..., others]).all()
+
+
+DECODE = [
+    # B, T, Hq, Hk, D, page, most, dtype, kind, lens
+    (2, 2, 4, 2, 64, 16, 5, BF16, BF16, [80, 33]), (2, 5, 12, 2, 128, 32, 9, BF16, BF16, [287, 4]),
+    (2, 3, 6, 2, 64, 64, 4, F32, F32, [200, 65]), (1, 4, 2, 1, 128, 16, 60, F32, F32, [932]),
+    (2, 4, 32, 8, 64, 128, 3, BF16, E4M3, [383, 130]), (1, 6, 40, 1, 128, 256, 2, BF16, E4M3, [512]),
+    (2, 5, 3, 3, 64, 16, 8, F32, E4M3, [100, 35]), (1, 70, 6, 2, 64, 16, 20, BF16, BF16, [311]),
+    (1, 70, 6, 2, 128, 16, 20, BF16, E4M3, [311]), (2, 40, 4, 4, 64, 32, 4, F32, F32, [70, 20]),
+]
+
+
+@pytest.mark.parametrize("case", DECODE, ids=["-".join(map(str, c[:9])).replace("torch.", "") for c in DECODE])
+def test_decode_values(case):
+    """One entry of a new token's v in the cache (or its scale): the tokens before it do
+    not notice, the others see it."""
+    B, T, Hq, Hk, D, page, most, dt, kind, lens = case
+    c = cache(B, most, page, Hk, D, dt, kind, seed=90)
+    gen = torch.Generator().manual_seed(91)
+    q = randn(gen, B, T, Hq, D).to(dt).cuda()
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    clean = api.attn_decode(q, *cargs(c, ln))
+    last = [(b, n - 1 - i) for b, n in enumerate(lens) for i in {0, 1, T // 2, T - 1, T, T + 40} if i < n]
+    for m, (b, pos) in enumerate(last):
+        place, at, g, e = int(c["table"][b, pos // page]), pos % page, m % Hk, (7 * m + 5) % D
+        heads = slice(g * (Hq // Hk), (g + 1) * (Hq // Hk))
+        t = max(0, pos - (lens[b] - T))      # the first token that sees it
+        for bad in ("nan", "inf", "scale"):
+            if (bad == "scale") != (kind is E4M3) and bad != "nan":
+                continue
+            x = {n: y if y is None or n == "table" else y.clone() for n, y in c.items()}
+            if bad == "scale":
+                x["v_scale"][place, g, at] = math.nan
+            elif kind is E4M3:
+                x["v_pages"].view(torch.uint8)[place, g, at, e] = 0xFF
+            else:
+                x["v_pages"][place, g, at, e] = math.nan if bad == "nan" else -math.inf
+            y = api.attn_decode(q, *cargs(x, ln))
+            keep = torch.ones_like(y, dtype=torch.bool)
+            keep[b, t:, heads, slice(None) if bad == "scale" else e] = False
+            same(y, clean, keep, (case, b, pos, bad))
+            hit = y[~keep]
+            # (an infinity times the second part of a weight in two, which may be 0 or below, is any of them)
+            want = ~torch.isfinite(hit) if bad == "inf" and dt is BF16 else hit == -math.inf if bad == "inf" else torch.isnan(hit)
+            assert want.all(), (case, b, pos, bad)
