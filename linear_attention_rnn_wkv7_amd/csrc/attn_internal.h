@@ -99,10 +99,16 @@ constexpr int kDecodeRows = 32;
 // Tokens of a wave's step.
 constexpr int kDecodeStep = 32;
 // Parts of the cache that are read at once: enough for two workgroups to a compute
-// unit, which it holds at a time, none under 8 steps (of which each wave has two).
+// unit, which it holds at a time, and of a table's full rows none under 8 steps (of
+// which each wave has two).
 // 256, 512, 768 and 1024 workgroups, us, bf16: 2 rows of 131072 positions, 4 new
 // tokens, 32 / 8 heads of 64, 132, 103, 123, 105 (in 8 bits 122, 81, 102, 86); 16 of
 // 4096, 16 / 4 heads of 128, 33, 31, 36, 34.  At least 4, 8 or 16 steps: the same.
+// A row that fills less of its table is cut into as many parts, of fewer steps, down to
+// one for a workgroup.  Parts of 8 steps at least, and the others empty, took longer: 2
+// rows of 1000 in tables for 131072, 32 / 8 heads of 64, 8.4 us as it is and 10.6; 8 of
+// 10 to 2000 in tables for 32768, 16 / 4 heads of 128, 9.0 and 12.3; one of 6000 in a
+// table for 16384, 32 / 8 of 128, 11.7 and 14.6.
 inline int64_t decode_splits(int64_t B, int64_t T, int64_t Hq, int64_t Hk, int64_t capacity)
 {
     const int64_t rows = T * (Hq / Hk), units = B * Hk * ((rows + kDecodeRows - 1) / kDecodeRows);
