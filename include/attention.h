@@ -69,7 +69,7 @@ typedef struct {
     int64_t q_stride, k_stride, v_stride;
     int32_t dtype;  /* wkv7_dtype */
     int32_t flags;  /* 0 */
-    float scale;    /* positive, finite, not denormal */
+    float scale;    /* positive, not denormal, at most 2^127 */
 } attn_shape;
 
 /* Bytes of the record attn_forward leaves for attn_backward beside lse: what

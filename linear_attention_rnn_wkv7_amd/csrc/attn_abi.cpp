@@ -22,6 +22,8 @@ size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void *p, uintptr_t to = 16) { return (uintptr_t)p % to == 0; }
 int status(hipError_t e) { return e == hipSuccess ? WKV7_OK : WKV7_ERR_HIP; }
 bool is_dtype(int32_t d) { return d == WKV7_F32 || d == WKV7_BF16; }
+// (times log2 e it is still finite)
+bool is_scale(float s) { return std::isnormal(s) && s > 0.f && s <= 0x1p127f; }
 bool is_cache(int32_t d) { return d == KV_CACHE_SAME || d == KV_CACHE_E4M3; }
 
 int check_workspace(const void *ws, size_t given, size_t need)
@@ -54,7 +56,7 @@ int check(const attn_shape *s, wkv7::attn::Launch *L)
 {
     if (!s) return WKV7_ERR_INVALID;
     if (s->B < 0 || s->T < 0 || s->nseq < 0 || s->flags != 0 || !is_dtype(s->dtype)) return WKV7_ERR_INVALID;
-    if (!std::isnormal(s->scale) || s->scale < 0.f) return WKV7_ERR_INVALID;
+    if (!is_scale(s->scale)) return WKV7_ERR_INVALID;
     if (s->nseq > 0 && s->B != 1) return WKV7_ERR_INVALID;
     int rc = check_heads(s->Hq, s->Hk, s->D);
     if (rc != WKV7_OK) return rc;
@@ -214,7 +216,7 @@ int check(const attn_decode_shape *s, wkv7::attn::DecodeLaunch *L)
 {
     if (!s) return WKV7_ERR_INVALID;
     if (s->B < 0 || s->T < 0 || !is_dtype(s->dtype)) return WKV7_ERR_INVALID;
-    if (!std::isnormal(s->scale) || s->scale < 0.f) return WKV7_ERR_INVALID;
+    if (!is_scale(s->scale)) return WKV7_ERR_INVALID;
     int rc = check_heads(s->Hq, s->Hk, s->D);
     if (rc != WKV7_OK) return rc;
     rc = check_pool({s->pages, s->page, s->max_pages, s->Hk, s->D, s->B, s->cache_dtype});
