@@ -315,57 +315,6 @@ __device__ __forceinline__ Place locate(const Seqs &m, int slot, int lane)
     return {lo, (int)len, at * kRows};
 }
 
-// Block -> (slot, head).  Of a unit (row, head), the tiles that have the most to go
-// over start first.  Workgroups go to the 8 dies in turn: each die has units of its
-// own, neighbours, and takes `chunk` of them at a time, tile by tile, so that its
-// cache holds what these read.
-__device__ __forceinline__ void unit_of(const Seqs &m, int64_t B, int64_t heads_, uint32_t chunk, bool last_first,
-                                        uint32_t id, int &slot, int &head)
-{
-    const uint32_t heads = (uint32_t)heads_, units = m.starts ? heads : (uint32_t)(B * heads_);
-    const uint32_t tiles = (uint32_t)(m.starts ? m.slots : m.tiles);
-    uint32_t tile, u;
-    if (units % 8 == 0) {
-        const uint32_t per = units / 8, n = id / 8, c = n / (tiles * chunk), first = c * chunk;
-        const uint32_t here = per - first < chunk ? per - first : chunk, rest = n - first * tiles;
-        tile = rest / here;
-        u = id % 8 * per + first + (rest - tile * here);
-    } else {
-        tile = id / units;
-        u = id - tile * units;
-    }
-    if (last_first) tile = tiles - 1 - tile;
-    const uint32_t b = u / heads;
-    head = (int)(u - b * heads);
-    slot = (int)(m.starts ? tile : b * (uint32_t)m.tiles + tile);
-}
-
-// Units of a die's that are taken at a time, where `sharing` of them read the same
-// `bytes`: as many as read 8 MB, twice a die's cache, and keep its compute units
-// busy.  8 x 4096 x 32 heads of 64, us, forward, dq, dk and dv: all at a time (10
-// times the bytes from memory) 744, 857, 1135; 2 MB 668, 833, 1085; 4 MB 675, 829,
-// 1066; 8 MB 670, 821, 1059.  With 128 workgroups or fewer to a die, the order of
-// their lengths counts: dk and dv of 4 x 4096 x 16 / 4 heads of 128 680, and 711 by
-// units.
-inline uint32_t chunk_of(const Seqs &m, int64_t units, int64_t bytes, int64_t sharing)
-{
-    if (m.starts || units < 8) return (uint32_t)(units < 8 ? 1 : units / 8);
-    int64_t n = bytes < (8 << 20) ? (8 << 20) / bytes * sharing : sharing;
-    if (n * m.tiles < 128) n = (127 + m.tiles) / m.tiles;
-    return (uint32_t)(n < units / 8 ? n : units / 8);
-}
-
-// Where few workgroups of kTile rows would leave compute units without one, a
-// workgroup has kNarrow rows and its four waves share what they have to go over.
-constexpr int kNarrow = 32;
-inline Seqs narrow(const Seqs &s, int64_t B)
-{
-    Seqs n = s;
-    n.tiles = (s.T + kNarrow - 1) / kNarrow;
-    n.slots = s.starts ? s.T / kNarrow + s.nseq : B * n.tiles;
-    return n;
-}
-
 // A wave's own tiles in a narrow workgroup: two arrays of 32 rows, twice where
 // LDS has room.
 template <typename T, int D>
