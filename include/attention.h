@@ -41,7 +41,9 @@
  * Results are the same bit for bit from run to run: no sum depends on the order
  * in which workgroups run.  What a token does not see reaches none of its
  * outputs, whatever it holds, and none of its gradients what does not see it.
- * Where results are not finite, their tiles are gone over a second time.
+ * Where results are not finite, their tiles are gone over a second time.  A token
+ * whose scores are all minus infinity has NaN for y in attn_forward, and minus
+ * infinity for lse: there is no weight to divide by (in attn_decode y is 0).
  *
  * Ownership, execution and errors as for wkv7.h: device pointers owned by the
  * caller, work enqueued on `stream`, nothing allocated or synchronised, every
@@ -86,8 +88,8 @@ int attn_forward(const attn_shape *shape, const void *q, const void *k, const vo
 
 /* Backward, from a forward's y, lse and record (NULL: y alone stands for
  * itself, and its rounding enters dq and dk: their errors in bf16 grow from
- * 1.41 to 1.49 times those of one rounding).  dq, dk, dv required, contiguous
- * whatever the strides of q, k, v.  dk and dv are summed over the query heads
+ * 1.41 to 1.49 times those of one rounding).  y, dy, dq, dk and dv are contiguous
+ * whatever the strides of q, k, v, and required.  dk and dv are summed over the query heads
  * that read them.  workspace: 256-byte aligned. */
 int attn_backward(const attn_shape *shape, const void *q, const void *k, const void *v,
                   const int32_t *seq_starts, const void *y, const float *lse, const void *record,

@@ -776,8 +776,8 @@ def attn_forward(q, k, v, *, seq_starts=None, scale=None, want_lse=False, want_r
 def attn_backward(q, k, v, y, lse, dy, record=None, *, seq_starts=None, scale=None, workspace=None, stream=None,
                   out=None):
     """The gradients of attn_forward (attn_backward), with the same inputs and
-    options and its y, lse and record: dict(dq, dk, dv), contiguous, dk and dv
-    summed over the query heads that read them.  Without the record y's own
+    options and its y, lse and record, and dy, contiguous: dict(dq, dk, dv),
+    contiguous, dk and dv summed over the query heads that read them.  Without the record y's own
     rounding to bf16 enters dq and dk."""
     (_, sh, _, need), ys, at = _attn_dims(q, k, v, seq_starts, scale)
     _check_like("y", y, ys, q.dtype, at)

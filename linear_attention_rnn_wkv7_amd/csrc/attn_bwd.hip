@@ -17,8 +17,10 @@
 //
 // Bound as the forward by matrix and vector instructions in turn, and at D = 128 by
 // registers: with k, v, dk and dv of 32 keys a wave has a SIMD to itself.  8 x 4096,
-// 32 heads of 64: dk and dv 1050 us, dq 810, the matrix units busy 0.57 of the time;
-// 4 x 4096, 16 / 4 heads of 128: 670 (busy 0.34) and 388.  Slower for dk and dv: 64
+// 32 heads of 64: dk and dv 1040 to 1070 us, dq 810, the matrix units busy 0.55 of the
+// time; 4 x 4096, 16 / 4 heads of 128: 665 to 695 (busy 0.33) and 382.  Both together, 24
+// sequences in 12288 tokens, 32 / 8 heads of 128: 574 us, 300 TFLOP/s of 5 products;
+// fp32, 4096 tokens, 16 heads of 64: 1174 us, 73.  Slower for dk and dv: 64
 // keys to a wave (heads of 64) 1726 against 1194; two waves with spills (128) 1177
 // against 697, with v in LDS 1089 against 685; dk and dv apart 702 against 749 for the
 // kernel, the same for a run of calls, in which the clock falls with more products.

@@ -3,20 +3,22 @@
 // Bound by the bytes of the cache: the queries of all heads that share a key
 // head (and of all new tokens) go over it together, kDecodeRows to a
 // workgroup, and few of them leave the matrix units idle most of the time, so
-// the weights take part in two bf16 parts at no cost (over an 8-bit cache, which
-// is bound by instructions, in one).  The cache of a row is cut
+// the weights take part in two bf16 parts at no cost (over an 8-bit cache, whose
+// values are rounded more coarsely, in one).  The cache of a row is cut
 // into `splits` parts of whole steps; within a workgroup each wave takes
 // every fourth step of the part by itself, with its own running maximum, sum
 // and O^T, without a barrier: the next step's keys and values are on their
 // way to registers while one is computed, and go to LDS of the wave's own.  The
 // waves are joined through LDS, the parts by a second kernel, both in order.
 //
-// 64 rows of 8192 positions, 32 / 8 heads of 128, bf16: 283 us, 5.7 TB/s (a large
-// copy: 5.2).  An 8-bit cache is bound by instructions: widened to bf16 and written
-// to LDS it takes as many of them as twice the bytes; 2 rows of 131072, heads of 64,
-// 57 to 70 us, 3.1 to 3.8 TB/s.  In fp32 the matrix instruction bounds it, which
+// 64 rows of 8192 positions, 32 / 8 heads of 128, bf16: 285 us, 5.7 TB/s (a large
+// copy: 5.2).  Over an 8-bit cache it waits for memory with too little on its way, one
+// step of 4 KB a wave, half of bf16's: 2 rows of 131072, heads of 64, 39 us where the
+// cache lies in the device's own, 55 to 72 from memory, 3.0 to 3.9 TB/s; its vector
+// instructions are some 0.4 of the time.  In fp32 the matrix instruction bounds it, which
 // takes 8 times bf16's time for 32 rows of queries however few there are: 8 bits
-// under fp32 1.2 to 1.5 TB/s.  Two steps ahead: slower, for want of registers.
+// under fp32 1.2 to 1.5 TB/s.  Two steps ahead, tried with heads of 128: slower, for want
+// of registers.
 
 #include <type_traits>
 
