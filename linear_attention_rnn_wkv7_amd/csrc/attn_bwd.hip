@@ -280,8 +280,12 @@ __device__ __forceinline__ void join(const char (&lds)[4][kWave], T *out, int64_
 }
 
 // The narrow form: a wave has every fourth 32 rows of all the heads.
+// With heads of 64 in bf16 the registers are divided for two waves on a SIMD: divided
+// for one, matrix results go by way of the other half of the registers.  The whole
+// backward, us, for one and two: 1 x 8192, 8 / 1 heads 802 and 730; 1 x 2048, 8 / 8 51 and
+// 46; 4 x 2000, 12 / 3 192 and 133; 3000 tokens in 9 sequences, 16 / 4 57 and 53.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 1) attn_dkdv_narrow_kernel(BwdArgs<T> p)
+__global__ void __launch_bounds__(256, (sizeof(T) == 2 && D == 64 ? 2 : 1)) attn_dkdv_narrow_kernel(BwdArgs<T> p)
 {
     using O = Own<T, D>;
     __shared__ __attribute__((aligned(16))) char lds[4][O::kWave];
