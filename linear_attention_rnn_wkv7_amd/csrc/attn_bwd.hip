@@ -155,10 +155,11 @@ struct Keys {
 };
 
 // 32 keys by a wave, with care: after the forms below, where these have found results
-// that are not finite.  A function that is not inlined, for what it needs of registers
-// would be missing in their loops (heads of 64: 68 bytes of them in memory, two reads of
-// those between copies).  Its tiles are in `lds`, the wave's own.
-template <typename T, int D, int kWaves>
+// that are not finite.  Its tiles are in `lds`, the wave's own.  It makes all that it needs
+// anew and stores its results itself: with anything shared between it and the loops of
+// those forms, registers of these were kept in memory (heads of 64: up to 68 bytes, two
+// reads of them between the copies of a step).
+template <typename T, int D>
 __device__ __forceinline__ void careful_keys(const BwdArgs<T> &p, Place at, int hk, int key0, char *lds, float *table)
 {
     using L = Tile<T, D>;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(256, kWaves) attn_dkdv_kernel(BwdArgs<T> p)
                                              at.len);
     }
     if (!all_waves(all_finite(w.dk) && all_finite(w.dv), finite, wave, lane)) {
-        if (key0 < at.len) careful_keys<T, D, kWaves>(p, at, hk, key0, lds[wave >> 1][wave & 1], table[wave >> 1][wave & 1]);
+        if (key0 < at.len) careful_keys<T, D>(p, at, hk, key0, lds[wave >> 1][wave & 1], table[wave >> 1][wave & 1]);
         return;
     }
     if (w.key < at.len) w.store(p, at, hk);
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(256, (sizeof(T) == 2 && D == 64 ? 2 : 1)) attn
         if (O::kBuffers == 1 && n + 4 < steps) send(n + 4);
     }
     if (!all_waves(all_finite(w.dk) && all_finite(w.dv), finite, wave, lane)) {
-        if (wave == 0) careful_keys<T, D, 0>(p, at, hk, at.at, lds[0], table[0][0]);
+        if (wave == 0) careful_keys<T, D>(p, at, hk, at.at, lds[0], table[0][0]);
         return;
     }
     const int count = at.len - at.at < kNarrow ? at.len - at.at : kNarrow;

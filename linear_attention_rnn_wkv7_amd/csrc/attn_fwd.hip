@@ -17,11 +17,12 @@
 // Bound by matrix and vector instructions in turn: a 32 x 32 tile of heads of 64 is
 // 256 cycles of the matrix unit and about 280 of the vector unit (16 exponentials of
 // 8, the maximum, sum and conversion), of which three or four waves on a SIMD overlap
-// most.  16384 tokens, 32 / 4 heads of 64: 1.13 to 1.18 ms, 930 to 970 TFLOP/s (a large
-// product of matrices: 1300); 4 x 4096, 16 / 4 heads of 128: 283 us, 970; 24 prompts
-// of 12288 tokens, 32 / 8 heads of 128: 131 us, 530 (short rows: the fill and end of
-// each workgroup).  fp32, 4096 tokens, 16 heads of 64: 400 us, 86 TFLOP/s (153).  Slower or equal: 64 rows to a wave, scores of a block ahead,
-// three or four buffers.
+// most.  16384 tokens, 32 / 4 heads of 64: 1.13 to 1.18 ms, 930 to 970 TFLOP/s (a
+// large product of matrices: 1300); 4 x 4096, 16 / 4 heads of 128: 283 us, 970; 24
+// prompts of 12288 tokens, 32 / 8 heads of 128: 131 us, 530 (short rows: the fill and
+// end of each workgroup).  fp32, 4096 tokens, 16 heads of 64: 400 us, 86 TFLOP/s
+// (153).  Slower or equal: 64 rows to a wave, scores of a block ahead, three or four
+// buffers.
 
 #include <type_traits>
 
